@@ -439,6 +439,158 @@ int moe_layer_forward_noalloc(const moe_layer* L, const void* x, int32_t x_dtype
                               float* wt_out, int32_t path, void* stream);
 
 /*
+ * -------------------------------------------------------------------------
+ * Gate: experts from given router logits
+ * -------------------------------------------------------------------------
+ * moe_route_topk is the sigmoid router of one group.  moe_gate_topk takes
+ * logits that a caller already has (moe_router_logits, or a product of its
+ * own) and covers the gates of the layer's family: sigmoid or softmax
+ * scores, a balance bias, expert groups, renormalised or plain weights, a
+ * routed scaling factor, masked experts.  For token t with logits z[e]:
+ *
+ *   masked   expert e is out if z[e] is NaN or z[e] <= -2^127 (-inf and the
+ *            lowest finite bf16 and fp32 values are); a larger z[e] counts
+ *            as the largest finite fp32 value at most.
+ *   exp32(u), u in [-80, 80]: the fp32 steps of sigmoid32 (top of this
+ *            header) from kf on, with t = u; its value is e.
+ *   scores   MOE_SCORE_SIGMOID: s[e] = sigmoid32(z[e]);
+ *            MOE_SCORE_SOFTMAX: s[e] = a[e] / S (an IEEE division), where
+ *            a[e] = exp32(max(z[e] - m, -80)), m = the largest z of the
+ *            experts that are not masked, a = 0 for masked ones, and S is
+ *            the fp32 sum of 64 partials, a[e] added to partial e % 64 in
+ *            increasing e, folded p[l] = p[l] + p[l + s], s = 32 .. 1.
+ *   values   v[e] = s[e] + bias[e] with a bias (one fp32 addition); without
+ *            one, s[e] if groups are chosen by MOE_GROUP_TOP2_SUM (and
+ *            top_groups < n_groups), else z[e].  An expert whose v is NaN
+ *            or -inf is out.
+ *   groups   (only if top_groups < n_groups) expert e is in group
+ *            e / (E / n_groups).  A group's value is its largest v
+ *            (MOE_GROUP_MAX) or the fp32 sum of its two largest
+ *            (MOE_GROUP_TOP2_SUM; a single expert that is in counts alone);
+ *            the top_groups groups of largest value are kept, equal values
+ *            to the smaller group, and the others' experts are out.
+ *   top-k    the top_k experts that are in, by v descending, equal v (-0 ==
+ *            +0) to the smaller index: idx[t][0..], best first.
+ *   weights  wt[t][j] = scale * s_j, or with renormalize scale * (s_j / (s_0
+ *            + ... )), the sum over the chosen experts in rank order, fp32.
+ *   If fewer than top_k experts are in, the remaining entries are idx = -1
+ *   and wt = 0 (moe_bucket gives such a route no place).
+ *
+ * z is [T] rows of E logits in z_dtype (MOE_F32 or MOE_BF16), row t starting
+ * at element t * z_stride (z_stride >= E; any element-aligned address).
+ */
+#define MOE_SCORE_SIGMOID 0
+#define MOE_SCORE_SOFTMAX 1
+#define MOE_GROUP_MAX 0
+#define MOE_GROUP_TOP2_SUM 1
+
+typedef struct moe_gate {
+  uint32_t abi_version; /* must equal MOE_ABI_VERSION */
+  int32_t n_experts;    /* E, 1 .. 1024 */
+  int32_t top_k;        /* 1 .. 16, at most top_groups * (E / n_groups) */
+  int32_t score;        /* MOE_SCORE_* */
+  int32_t n_groups;     /* 1 .. 64, divides E */
+  int32_t top_groups;   /* 1 .. n_groups */
+  int32_t group_score;  /* MOE_GROUP_* */
+  int32_t renormalize;  /* 0 or 1 */
+  float scale;          /* routed scaling factor, finite */
+  const float* bias;    /* nullable fp32 [E]: selection-only bias */
+} moe_gate;
+
+/*
+ * Router logits z[t][e] in the fixed fp32 order at the top of this header:
+ * w_router fp32 [E][d], x [T][d] in x_dtype, z fp32 [T][E].
+ */
+int moe_router_logits(const float* w_router, int32_t E, int32_t d, const void* x,
+                      int32_t x_dtype, int32_t T, float* z, void* stream);
+
+/* idx int32 [T][top_k], wt fp32 [T][top_k]; definition above. */
+int moe_gate_topk(const moe_gate* G, const void* z, int32_t z_dtype, int64_t z_stride,
+                  int32_t T, int32_t* idx, float* wt, void* stream);
+
+/*
+ * -------------------------------------------------------------------------
+ * Block-scaled E4M3 operators
+ * -------------------------------------------------------------------------
+ * Matrices of E4M3 bytes (OCP: bias 7, largest 448, 0x7f and 0xff not
+ * numbers) with one fp32 scale for each block of 128 along the inputs:
+ *   activations  q [M][K], s fp32 [M][KB]: value = q * s[m][i / 128]
+ *   weights      q [N][K], s fp32 [NB][KB]: value = q * s[n / 128][i / 128]
+ * KB = ceil(K / 128), NB = ceil(N / 128): the last blocks may be short.
+ * Tensors of several experts are such matrices back to back, [E][N][K] and
+ * [E][NB][KB].  These are the layouts in which 8-bit checkpoints of the
+ * layer's family come, so nothing is repacked.
+ *
+ * Products are summed in fp32: the dot products of one block of 128 on the
+ * matrix units, then one fused multiply-add per block with the product of
+ * the two scales.  A code or scale that is not a number makes the outputs
+ * that it enters NaN.  Identical inputs give bitwise identical outputs.
+ *
+ * Limits: K (inputs) a multiple of 16 in [16, 16384]; N (outputs) in [1,
+ * 65536] with N * K < 2^31; M in [0, 2^20] rows; q pointers 16-byte aligned,
+ * their row strides multiples of 16 bytes; outputs, scales and int32 arrays
+ * 16-byte aligned.  M = 0 and T = 0 are valid no-ops.
+ */
+
+/*
+ * Activations to E4M3: per row and group of 128 inputs
+ *   s = max(max|x|, 2^-100) / 448,  q = e4m3(x / s)
+ * (fp32 divisions, the codes rounded to nearest even; the largest value of a
+ * group becomes 448).  A group that holds a NaN or an infinity gets s = NaN
+ * and codes 0.  x [M] rows of K in x_dtype (MOE_F32 or MOE_BF16), ldx
+ * elements apart (rows 16-byte aligned); q [M] rows ldq bytes apart;
+ * s [M][KB].
+ */
+int moe_blockscale_quantize(const void* x, int32_t x_dtype, int64_t ldx, int32_t M,
+                            int32_t K, uint8_t* q, int64_t ldq, float* s, void* stream);
+
+/*
+ * y[m][n] = sum over blocks b of xs[m][b] ws[n/128][b] (xq[m] . wq[n])_b.
+ * xq [M] rows ldx bytes apart; wq [N][K]; y [M] rows of N in y_dtype
+ * (MOE_F32 or MOE_BF16, rounded once), ldy elements apart (rows aligned to
+ * their element).  Workspace: moe_blockscale_matmul_workspace_bytes of the
+ * same M, N, K (null if that is 0): partial sums where few outputs share a
+ * long K.
+ */
+int moe_blockscale_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K, size_t* bytes);
+int moe_blockscale_matmul(const uint8_t* xq, int64_t ldx, const float* xs, int32_t M,
+                          const uint8_t* wq, const float* ws, int32_t N, int32_t K,
+                          void* y, int32_t y_dtype, int64_t ldy, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
+ * The routed experts' gate and up products with SwiGLU, requantised: for
+ * every bucket row r of expert e (offsets[e] <= r < offsets[e + 1], offsets
+ * and perm as moe_bucket writes them for T tokens of k routes) with token
+ * t = perm[r] / k
+ *   h = silu(G_e x_t) * (U_e x_t),  (hq[r], hs[r]) = h quantised as above.
+ * xq [T][d], xs [T][ceil(d/128)]; w_gate, w_up [E][f][d] with scales
+ * [E][ceil(f/128)][ceil(d/128)]; hq [T*k][f] and hs [T*k][ceil(f/128)]: rows
+ * from offsets[E] on are not written.  d and f obey the limits of K.
+ */
+int moe_blockscale_gateup(const uint8_t* xq, const float* xs, int32_t T, int32_t k,
+                          const int32_t* offsets, const int32_t* perm, int32_t E,
+                          const uint8_t* w_gate, const float* s_gate,
+                          const uint8_t* w_up, const float* s_up, int32_t f, int32_t d,
+                          uint8_t* hq, float* hs, void* stream);
+
+/*
+ * The routed experts' down products and each token's weighted sum:
+ *   y[t] = add[t] + sum_j wt[t][j] * (D_e h)[pos[t*k + j]]
+ * in the order of j, fp32, where bucket row r belongs to expert e as above
+ * and routes with pos = T*k (no place) add nothing; add [T][d] is nullable
+ * (no term) and may be y itself.  hq [T*k][f], hs [T*k][ceil(f/128)]; w_down
+ * [E][d][f] with scales [E][ceil(d/128)][ceil(f/128)]; y fp32 [T][d].
+ * Workspace: moe_blockscale_down_workspace_bytes of the same T, k, d.
+ */
+int moe_blockscale_down_workspace_bytes(int32_t T, int32_t k, int32_t d, size_t* bytes);
+int moe_blockscale_down(const uint8_t* hq, const float* hs, int32_t T, int32_t k,
+                        const float* wt, const int32_t* offsets, const int32_t* pos,
+                        int32_t E, const uint8_t* w_down, const float* s_down, int32_t d,
+                        int32_t f, const float* add, float* y, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
  * Per-kernel timing with HIP events recorded on the stream each kernel is
  * launched on.  Eager use only: do not enable it while a stream is being
  * captured into a graph.  moe_profile_collect synchronises the recorded

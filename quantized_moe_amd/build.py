@@ -1,8 +1,8 @@
 """Build libqmoe.so (the HIP library) in-tree for gfx950.
 
-Each .hip source is compiled separately (the router file with floating-point
-contraction off, so its fixed summation order is exactly what the source
-says), then linked into one shared library next to this file.
+Each .hip source is compiled separately (the router and gate files with
+floating-point contraction off, so their fixed fp32 steps are exactly what the
+source says), then linked into one shared library next to this file.
 """
 from __future__ import annotations
 
@@ -20,12 +20,13 @@ OBJ = os.path.join(HERE, "_build")
 ARCH = "gfx950"
 
 SOURCES = ["api.hip", "route.hip", "bucket.hip", "repack.hip", "decode.hip", "decode_k1.hip", "decode_k2.hip",
-           "decode_k3.hip", "decode_unique.hip", "prefill.hip", "dense.hip"]
+           "decode_k3.hip", "decode_unique.hip", "prefill.hip", "dense.hip", "gate.hip", "blockscale_quant.hip",
+           "blockscale_matmul.hip", "blockscale_experts.hip"]
 PROBE_SOURCES = ["probe.hip"]
 # packed-fp32 VALU forms are disabled: only ordinary fp32 instructions
 COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang",
           "-packed-fp32-ops", "-I", os.path.join(ROOT, "include"), "-Wall", "-Wno-unused-function"]
-PER_FILE = {"route.hip": ["-ffp-contract=off"]}
+PER_FILE = {"route.hip": ["-ffp-contract=off"], "gate.hip": ["-ffp-contract=off"]}
 # hipBLASLt runs the dense shared-expert GEMMs of long prefill chunks (dense.hip)
 LIBS = ["-L/opt/rocm/lib", "-lhipblaslt"]
 

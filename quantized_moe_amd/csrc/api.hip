@@ -7,6 +7,7 @@
 // timeline", files.btbytes.com: ds4.h as the narrow public API), and the
 // refusal of unknown formats and versions follows the fail-loudly format
 // whitelist on "YoungAi -- DeepSeek V4.1 Flash on one DGX Spark", section 4.1.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
@@ -895,4 +896,234 @@ extern "C" int moe_layer_forward_noalloc(const moe_layer* L, const void* x, int3
                                          int32_t* idx_out, float* wt_out, int32_t path, void* stream) {
   return layer_forward("moe_layer_forward_noalloc", L, x, x_dtype, T, y, idx_out, wt_out, path, nullptr, 0, true,
                        stream);
+}
+
+// ---------------------------------------------------------------------------
+// gate and block-scaled E4M3 operators
+// ---------------------------------------------------------------------------
+extern "C" int moe_router_logits(const float* w_router, int32_t E, int32_t d, const void* x, int32_t x_dtype, int32_t T,
+                                 float* z, void* stream) {
+  const char* fn = "moe_router_logits";
+  int rc = check_dims(fn, E, d, 1);
+  if (rc) return rc;
+  if ((rc = check_T(fn, T)) || (rc = check_dtype(fn, x_dtype))) return rc;
+  if (T == 0) return ok();
+  NEED_PTR(w_router, "w_router");
+  NEED_PTR(x, "x");
+  NEED_PTR(z, "z");
+  hipStream_t s = (hipStream_t)stream;
+  const int pid = prof_begin(T <= ROUTER_ROWS_MAX_T ? "router_rows" : "router_tiled", s);
+  hipError_t e = launch_router(w_router, E, d, x, x_dtype, T, z, s);
+  prof_end(pid, s);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
+extern "C" int moe_gate_topk(const moe_gate* G, const void* z, int32_t z_dtype, int64_t z_stride, int32_t T,
+                             int32_t* idx, float* wt, void* stream) {
+  const char* fn = "moe_gate_topk";
+  if (!G) return fail(MOE_ERR_INVALID_ARG, "%s: gate is null", fn);
+  if (G->abi_version != MOE_ABI_VERSION)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: gate abi_version %u, library speaks %d", fn, G->abi_version, MOE_ABI_VERSION);
+  const int E = G->n_experts;
+  if (E < 1 || E > MAX_EXPERTS) return fail(MOE_ERR_INVALID_ARG, "%s: n_experts %d not in [1, %d]", fn, E, MAX_EXPERTS);
+  if (G->n_groups < 1 || G->n_groups > GATE_MAX_GROUPS || E % G->n_groups != 0)
+    return fail(MOE_ERR_INVALID_ARG, "%s: n_groups %d not in [1, %d] or does not divide n_experts %d", fn, G->n_groups,
+                GATE_MAX_GROUPS, E);
+  if (G->top_groups < 1 || G->top_groups > G->n_groups)
+    return fail(MOE_ERR_INVALID_ARG, "%s: top_groups %d not in [1, n_groups %d]", fn, G->top_groups, G->n_groups);
+  const int most = G->top_groups * (E / G->n_groups);
+  if (G->top_k < 1 || G->top_k > TOPK_MAX_K || G->top_k > most)
+    return fail(MOE_ERR_INVALID_ARG, "%s: top_k %d not in [1, min(%d experts of the kept groups, %d)]", fn, G->top_k,
+                most, TOPK_MAX_K);
+  if (G->score != MOE_SCORE_SIGMOID && G->score != MOE_SCORE_SOFTMAX)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: unknown score %d", fn, G->score);
+  if (G->group_score != MOE_GROUP_MAX && G->group_score != MOE_GROUP_TOP2_SUM)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: unknown group_score %d", fn, G->group_score);
+  if (G->renormalize != 0 && G->renormalize != 1) return fail(MOE_ERR_INVALID_ARG, "%s: renormalize must be 0 or 1", fn);
+  if (!isfinite(G->scale)) return fail(MOE_ERR_INVALID_ARG, "%s: scale is not finite", fn);
+  if (G->bias && ((uintptr_t)G->bias & 3u)) return fail(MOE_ERR_INVALID_ARG, "%s: bias is not 4-byte aligned", fn);
+  int rc = check_T(fn, T);
+  if (rc) return rc;
+  if ((rc = check_dtype(fn, z_dtype))) return rc;
+  if (z_stride < E) return fail(MOE_ERR_INVALID_ARG, "%s: z_stride %lld below n_experts %d", fn, (long long)z_stride, E);
+  if (T == 0) return ok();
+  if (!z) return fail(MOE_ERR_INVALID_ARG, "%s: z is null", fn);
+  if ((uintptr_t)z & (z_dtype == MOE_BF16 ? 1u : 3u))
+    return fail(MOE_ERR_INVALID_ARG, "%s: z is not aligned to its elements", fn);
+  NEED_PTR(idx, "idx");
+  NEED_PTR(wt, "wt");
+  GateLaunch a{};
+  a.E = E;
+  a.k = G->top_k;
+  a.score = G->score;
+  a.n_groups = G->n_groups;
+  a.top_groups = G->top_groups;
+  a.group_score = G->group_score;
+  a.renormalize = G->renormalize;
+  a.scale = G->scale;
+  a.bias = G->bias;
+  a.z = z;
+  a.z_dtype = z_dtype;
+  a.z_stride = z_stride;
+  a.T = T;
+  a.idx = idx;
+  a.wt = wt;
+  hipStream_t s = (hipStream_t)stream;
+  const int pid = prof_begin("gate_topk", s);
+  hipError_t e = launch_gate(a, s);
+  prof_end(pid, s);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
+// Inputs per row of a block-scaled matrix.
+static int check_bs_k(const char* fn, const char* name, int K) {
+  if (K < 16 || K > BS_MAX_K || K % 16 != 0)
+    return fail(MOE_ERR_INVALID_ARG, "%s: %s %d is not a multiple of 16 in [16, %d]", fn, name, K, BS_MAX_K);
+  return MOE_OK;
+}
+
+static int check_bs_rows(const char* fn, int M) {
+  if (M < 0 || M > BS_MAX_ROWS) return fail(MOE_ERR_INVALID_ARG, "%s: M %d not in [0, %d]", fn, M, BS_MAX_ROWS);
+  return MOE_OK;
+}
+
+static int check_bs_outputs(const char* fn, int N, int K) {
+  if (N < 1 || N > BS_MAX_N) return fail(MOE_ERR_INVALID_ARG, "%s: N %d not in [1, %d]", fn, N, BS_MAX_N);
+  if ((int64_t)N * K >= (int64_t(1) << 31))
+    return fail(MOE_ERR_INVALID_ARG, "%s: N %d by K %d is not below 2^31 weights", fn, N, K);
+  return MOE_OK;
+}
+
+static int check_bs_experts(const char* fn, int E, int k, int d, int f) {
+  if (E < 1 || E > MAX_EXPERTS) return fail(MOE_ERR_INVALID_ARG, "%s: n_experts %d not in [1, %d]", fn, E, MAX_EXPERTS);
+  if (k < 1 || k > TOPK_MAX_K || k > E)
+    return fail(MOE_ERR_INVALID_ARG, "%s: top_k %d not in [1, min(n_experts, %d)]", fn, k, TOPK_MAX_K);
+  int rc;
+  if ((rc = check_bs_k(fn, "d", d)) || (rc = check_bs_k(fn, "f", f))) return rc;
+  return MOE_OK;
+}
+
+extern "C" int moe_blockscale_quantize(const void* x, int32_t x_dtype, int64_t ldx, int32_t M, int32_t K, uint8_t* q,
+                                       int64_t ldq, float* s, void* stream) {
+  const char* fn = "moe_blockscale_quantize";
+  int rc;
+  if ((rc = check_bs_rows(fn, M)) || (rc = check_bs_k(fn, "K", K)) || (rc = check_dtype(fn, x_dtype))) return rc;
+  if (ldx < K || ldx % (x_dtype == MOE_BF16 ? 8 : 4) != 0)
+    return fail(MOE_ERR_INVALID_ARG, "%s: ldx %lld is below K %d or leaves rows unaligned to 16 bytes", fn, (long long)ldx, K);
+  if (ldq < K || ldq % 16 != 0)
+    return fail(MOE_ERR_INVALID_ARG, "%s: ldq %lld is below K %d or not a multiple of 16", fn, (long long)ldq, K);
+  if (M == 0) return ok();
+  NEED_PTR(x, "x");
+  NEED_PTR(q, "q");
+  NEED_PTR(s, "s");
+  hipStream_t st = (hipStream_t)stream;
+  const int pid = prof_begin("bs_quantize", st);
+  hipError_t e = launch_bs_quantize(x, x_dtype, ldx, M, K, q, ldq, s, st);
+  prof_end(pid, st);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
+extern "C" int moe_blockscale_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K, size_t* bytes) {
+  const char* fn = "moe_blockscale_matmul_workspace_bytes";
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "%s: bytes is null", fn);
+  int rc;
+  if ((rc = check_bs_rows(fn, M)) || (rc = check_bs_k(fn, "K", K)) || (rc = check_bs_outputs(fn, N, K))) return rc;
+  *bytes = bs_matmul_ws(M, N, K);
+  return ok();
+}
+
+extern "C" int moe_blockscale_matmul(const uint8_t* xq, int64_t ldx, const float* xs, int32_t M, const uint8_t* wq,
+                                     const float* ws, int32_t N, int32_t K, void* y, int32_t y_dtype, int64_t ldy,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_blockscale_matmul";
+  int rc;
+  if ((rc = check_bs_rows(fn, M)) || (rc = check_bs_k(fn, "K", K)) || (rc = check_bs_outputs(fn, N, K))) return rc;
+  if (y_dtype != MOE_F32 && y_dtype != MOE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: unknown output dtype %d", fn, y_dtype);
+  if (ldx < K || ldx % 16 != 0)
+    return fail(MOE_ERR_INVALID_ARG, "%s: ldx %lld is below K %d or not a multiple of 16", fn, (long long)ldx, K);
+  if (ldy < N) return fail(MOE_ERR_INVALID_ARG, "%s: ldy %lld below N %d", fn, (long long)ldy, N);
+  if (M == 0) return ok();
+  NEED_PTR(xq, "xq");
+  NEED_PTR(xs, "xs");
+  NEED_PTR(wq, "wq");
+  NEED_PTR(ws, "ws");
+  NEED_PTR(y, "y");
+  const size_t need = bs_matmul_ws(M, N, K);
+  if (need) {
+    if (workspace_bytes < need)
+      return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, workspace_bytes, need);
+    NEED_PTR(workspace, "workspace");
+  }
+  BsMatmul a{xq, ldx, xs, M, wq, ws, N, K, y, y_dtype, ldy, (float*)workspace};
+  hipError_t e = launch_bs_matmul(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
+extern "C" int moe_blockscale_gateup(const uint8_t* xq, const float* xs, int32_t T, int32_t k, const int32_t* offsets,
+                                     const int32_t* perm, int32_t E, const uint8_t* w_gate, const float* s_gate,
+                                     const uint8_t* w_up, const float* s_up, int32_t f, int32_t d, uint8_t* hq,
+                                     float* hs, void* stream) {
+  const char* fn = "moe_blockscale_gateup";
+  int rc;
+  if ((rc = check_T(fn, T)) || (rc = check_bs_experts(fn, E, k, d, f))) return rc;
+  if (T == 0) return ok();
+  NEED_PTR(xq, "xq");
+  NEED_PTR(xs, "xs");
+  NEED_PTR(offsets, "offsets");
+  NEED_PTR(perm, "perm");
+  NEED_PTR(w_gate, "w_gate");
+  NEED_PTR(s_gate, "s_gate");
+  NEED_PTR(w_up, "w_up");
+  NEED_PTR(s_up, "s_up");
+  NEED_PTR(hq, "hq");
+  NEED_PTR(hs, "hs");
+  BsGateup a{xq, xs, T, k, offsets, perm, E, w_gate, s_gate, w_up, s_up, f, d, hq, hs};
+  hipStream_t s = (hipStream_t)stream;
+  const int pid = prof_begin("bs_gateup", s);
+  hipError_t e = launch_bs_gateup(a, s);
+  prof_end(pid, s);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
+extern "C" int moe_blockscale_down_workspace_bytes(int32_t T, int32_t k, int32_t d, size_t* bytes) {
+  const char* fn = "moe_blockscale_down_workspace_bytes";
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "%s: bytes is null", fn);
+  int rc;
+  if ((rc = check_T(fn, T)) || (rc = check_bs_k(fn, "d", d))) return rc;
+  if (k < 1 || k > TOPK_MAX_K) return fail(MOE_ERR_INVALID_ARG, "%s: top_k %d not in [1, %d]", fn, k, TOPK_MAX_K);
+  *bytes = bs_down_ws(T, k, d);
+  return ok();
+}
+
+extern "C" int moe_blockscale_down(const uint8_t* hq, const float* hs, int32_t T, int32_t k, const float* wt,
+                                   const int32_t* offsets, const int32_t* pos, int32_t E, const uint8_t* w_down,
+                                   const float* s_down, int32_t d, int32_t f, const float* add, float* y,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_blockscale_down";
+  int rc;
+  if ((rc = check_T(fn, T)) || (rc = check_bs_experts(fn, E, k, d, f))) return rc;
+  if (T == 0) return ok();
+  NEED_PTR(hq, "hq");
+  NEED_PTR(hs, "hs");
+  NEED_PTR(wt, "wt");
+  NEED_PTR(offsets, "offsets");
+  NEED_PTR(pos, "pos");
+  NEED_PTR(w_down, "w_down");
+  NEED_PTR(s_down, "s_down");
+  NEED_PTR(y, "y");
+  if (add && !aligned16(add)) return fail(MOE_ERR_INVALID_ARG, "%s: add is not 16-byte aligned", fn);
+  const size_t need = bs_down_ws(T, k, d);
+  if (workspace_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, workspace_bytes, need);
+  if (need) NEED_PTR(workspace, "workspace");
+  BsDown a{hq, hs, T, k, wt, offsets, pos, E, w_down, s_down, d, f, add, y, (float*)workspace};
+  hipError_t e = launch_bs_down(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
 }

@@ -1,0 +1,113 @@
+// Shared pieces of the block-scaled E4M3 operators (contracts: include/moe.h).
+//
+// Matrix-unit step: a block of 128 inputs is 16 x 16 dot products that leave
+// the matrix unit on their own and meet the product of their two scales in one
+// fused multiply-add.  The E4M3 codes enter as fp16, which holds each exactly,
+// through 16x16x32 steps whose sums are full fp32 (measured: 1.2e-8 of the
+// result per block).  The unit's own E4M3 steps align groups of eight products
+// to the largest and drop what lies 14 bits below it (measured: 1.4e-5 of the
+// result): too coarse for fp32 outputs.
+// The operands are taken as (weights, activations): the result's 16 columns
+// (lane % 16) are activation rows, so a lane needs one activation scale per
+// tile, and its 4 values are 4 consecutive outputs of that row (rows 4 (lane /
+// 16) .. + 3), which leave as one store.
+// Operand layout: lane l holds row l % 16, 32 bytes of the block.  Which 32
+// does not matter as long as both operands agree: lane l takes the 16-byte
+// pieces l / 16 and 4 + l / 16, so each load instruction covers 64 contiguous
+// bytes of a row, and step s takes bytes 8 s .. 8 s + 7 of its 32.
+#pragma once
+
+#include "common.hpp"
+#include "kernels.hpp"
+
+namespace qmoe {
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+
+constexpr int BS = 128;  // inputs (and, for weights, outputs) per scale
+__host__ __device__ constexpr int bs_blocks(int n) { return (n + BS - 1) / BS; }
+
+// 8 E4M3 bytes (two words) as fp16.
+__device__ __forceinline__ f16x8_t e4m3_to_f16(int a, int b) {
+  const f16x2_t v0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false);
+  const f16x2_t v1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true);
+  const f16x2_t v2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false);
+  const f16x2_t v3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true);
+  return f16x8_t{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
+}
+
+// 16 x 16 dot products over one block of 128.
+__device__ __forceinline__ f32x4_t mfma_block(i32x8_t w, i32x8_t x) {
+  f32x4_t p = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int s = 0; s < 4; s++)
+    p = __builtin_amdgcn_mfma_f32_16x16x32_f16(e4m3_to_f16(w[2 * s], w[2 * s + 1]),
+                                               e4m3_to_f16(x[2 * s], x[2 * s + 1]), p, 0, 0, 0);
+  return p;
+}
+
+__device__ __forceinline__ i32x8_t join_pieces(i32x4_t a, i32x4_t b) {
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Four fp32 values (|v| <= 448) to E4M3 bytes, nearest even.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
+}
+
+// The scale of a group whose largest magnitude has the bits `amax` (order of
+// non-negative floats = order of their bits; infinities and NaN come last).
+__device__ __forceinline__ float bs_scale(uint32_t amax) {
+  if (amax >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
+  return fmaxf(__uint_as_float(amax), 0x1p-100f) / 448.0f;
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// One output value, fp32 or bf16 (nearest even).
+__device__ __forceinline__ uint16_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+
+// The M tile of `bm` bucket rows that is the `tile`-th over all experts:
+// expert e, first row and row count.  false: there are fewer tiles.  Every
+// lane of a wave calls it with the same tile.
+__device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, int E, int bm, int tile, int* e_out,
+                                          int* row0, int* rows) {
+  const int lane = threadIdx.x & 63;
+  int base = 0;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    const int e = e0 + lane;
+    const int a = offsets[min(e, E)], b = offsets[min(e + 1, E)];
+    const int n = (b - a + bm - 1) / bm;
+    int incl = n;
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+      const int o = __shfl_up(incl, s, 64);
+      if (lane >= s) incl += o;
+    }
+    const int total = __builtin_amdgcn_readlane(incl, 63);
+    if (tile < base + total) {
+      const uint64_t m = __ballot(tile < base + incl);
+      const int src = __builtin_ctzll(m);
+      const int first = __builtin_amdgcn_readlane(a, src) + (tile - base - __builtin_amdgcn_readlane(incl - n, src)) * bm;
+      *e_out = e0 + src;
+      *row0 = first;
+      *rows = min(bm, __builtin_amdgcn_readlane(b, src) - first);
+      return true;
+    }
+    base += total;
+  }
+  return false;
+}
+
+// Upper bound on the number of M tiles of n rows in E buckets.
+inline int64_t max_tiles(int64_t n, int E, int bm) {
+  const int64_t full = n / bm + (E < n ? E : n);
+  return full < n ? full : n;
+}
+
+}  // namespace qmoe

@@ -15,6 +15,8 @@ constexpr int MAX_EXPERTS = 1024;
 constexpr int TOPK_MAX_K = 16;
 constexpr int TOPK_MAX_PER_LANE = MAX_EXPERTS / 64;
 constexpr int ROUTER_ROWS_MAX_T = 8;  // above this the tiled router runs (router + top-k measured 29 / 32 us at 8 tokens, 51 / 33 us at 16)
+constexpr int GATE_MAX_GROUPS = 64;
+constexpr int BS_MAX_K = 16384, BS_MAX_N = 65536, BS_MAX_ROWS = 1 << 20;  // block-scaled operators
 constexpr int DECODE_MAX_T = MOE_DECODE_MAX_T;            // the decode path's limit
 constexpr int AUTO_DECODE_MAX_T = MOE_AUTO_DECODE_MAX_T;  // MOE_PATH_AUTO's switch to prefill
 
@@ -153,6 +155,71 @@ hipError_t launch_shared_dense_down(const SharedDense& S, hipStream_t s);
 inline bool prefill_fits(int T, int k, int d, int f) {
   return (int64_t)T * d * 2 < (int64_t(1) << 31) && (int64_t)T * k * f * 2 < (int64_t(1) << 31);
 }
+
+// gate.hip
+struct GateLaunch {
+  int E, k, score, n_groups, top_groups, group_score, renormalize;
+  float scale;
+  const float* bias;
+  const void* z;
+  int z_dtype;
+  int64_t z_stride;
+  int T;
+  int32_t* idx;
+  float* wt;
+};
+hipError_t launch_gate(const GateLaunch& a, hipStream_t s);
+
+// blockscale_quant.hip, blockscale_matmul.hip, blockscale_experts.hip: E4M3
+// operators with a scale per block of 128 (arguments as in include/moe.h)
+hipError_t launch_bs_quantize(const void* x, int x_dtype, int64_t ldx, int M, int K, uint8_t* q, int64_t ldq, float* s,
+                              hipStream_t st);
+struct BsMatmul {
+  const uint8_t* xq;
+  int64_t ldx;
+  const float* xs;
+  int M;
+  const uint8_t* wq;
+  const float* ws;
+  int N, K;
+  void* y;
+  int y_dtype;
+  int64_t ldy;
+  float* part;  // bs_matmul_ws() bytes
+};
+size_t bs_matmul_ws(int M, int N, int K);
+hipError_t launch_bs_matmul(const BsMatmul& a, hipStream_t s);
+struct BsGateup {
+  const uint8_t* xq;
+  const float* xs;
+  int T, k;
+  const int32_t *offsets, *perm;
+  int E;
+  const uint8_t* w_gate;
+  const float* s_gate;
+  const uint8_t* w_up;
+  const float* s_up;
+  int f, d;
+  uint8_t* hq;
+  float* hs;
+};
+hipError_t launch_bs_gateup(const BsGateup& a, hipStream_t s);
+struct BsDown {
+  const uint8_t* hq;
+  const float* hs;
+  int T, k;
+  const float* wt;
+  const int32_t *offsets, *pos;
+  int E;
+  const uint8_t* w_down;
+  const float* s_down;
+  int d, f;
+  const float* add;  // nullable
+  float* y;
+  float* ye;  // bs_down_ws() bytes: the bucket rows' products [T k][d]
+};
+size_t bs_down_ws(int T, int k, int d);
+hipError_t launch_bs_down(const BsDown& a, hipStream_t s);
 
 // repack.hip: n_rows rows of K inputs
 hipError_t launch_repack(int fmt, int64_t n_rows, int K, const void* src, void* dst, int to_device, hipStream_t s);

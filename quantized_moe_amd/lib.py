@@ -28,6 +28,8 @@ MOE_DECODE_MAX_T = 8
 MOE_AUTO_DECODE_MAX_T = 24
 MOE_REPACK_TO_DEVICE, MOE_REPACK_TO_CANONICAL = 0, 1
 MOE_NOALLOC_SCRATCH_BYTES = 8 << 20
+MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2_SUM = 0, 1
 
 
 class MoeError(RuntimeError):
@@ -67,8 +69,23 @@ class MoeLayer(ctypes.Structure):
     ]
 
 
+class MoeGate(ctypes.Structure):
+    _fields_ = [
+        ("abi_version", ctypes.c_uint32),
+        ("n_experts", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("n_groups", ctypes.c_int32),
+        ("top_groups", ctypes.c_int32),
+        ("group_score", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("bias", ctypes.c_void_p),
+    ]
+
+
 _lib = None
-_P, _I32, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+_P, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 
 
 def lib() -> ctypes.CDLL:
@@ -95,6 +112,17 @@ def lib() -> ctypes.CDLL:
             "moe_layer_forward_noalloc": ([ctypes.POINTER(MoeLayer), _P, _I32, _I32, _P, _P, _P, _I32, _P],
                                           ctypes.c_int),
             "moe_prepare_weights": ([ctypes.POINTER(MoeLayer), ctypes.POINTER(MoeLayer), _P], ctypes.c_int),
+            "moe_router_logits": ([_P, _I32, _I32, _P, _I32, _I32, _P, _P], ctypes.c_int),
+            "moe_gate_topk": ([ctypes.POINTER(MoeGate), _P, _I32, _I64, _I32, _P, _P, _P], ctypes.c_int),
+            "moe_blockscale_quantize": ([_P, _I32, _I64, _I32, _I32, _P, _I64, _P, _P], ctypes.c_int),
+            "moe_blockscale_matmul_workspace_bytes": ([_I32, _I32, _I32, ctypes.POINTER(_SZ)], ctypes.c_int),
+            "moe_blockscale_matmul": ([_P, _I64, _P, _I32, _P, _P, _I32, _I32, _P, _I32, _I64, _P, _SZ, _P],
+                                      ctypes.c_int),
+            "moe_blockscale_gateup": ([_P, _P, _I32, _I32, _P, _P, _I32, _P, _P, _P, _P, _I32, _I32, _P, _P, _P],
+                                      ctypes.c_int),
+            "moe_blockscale_down_workspace_bytes": ([_I32, _I32, _I32, ctypes.POINTER(_SZ)], ctypes.c_int),
+            "moe_blockscale_down": ([_P, _P, _I32, _I32, _P, _P, _P, _I32, _P, _P, _I32, _I32, _P, _P, _P, _SZ, _P],
+                                    ctypes.c_int),
             "moe_profile_enable": ([_I32], ctypes.c_int),
             "moe_profile_reset": ([], ctypes.c_int),
             "moe_profile_collect": ([_I32, _P, _P, _P, _P], ctypes.c_int),
@@ -202,6 +230,146 @@ def layer_forward_noalloc(layer: MoeLayer, x, y, idx_out=None, wt_out=None, path
     (MOE_NOALLOC_SCRATCH_BYTES; no workspace argument, nothing allocated)."""
     _check(lib().moe_layer_forward_noalloc(ctypes.byref(layer), _ptr(x), x_dtype_of(x), x.shape[0], _ptr(y),
                                            _ptr(idx_out), _ptr(wt_out), path, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# gate and block-scaled E4M3 operators
+# ---------------------------------------------------------------------------
+_SCORES = {"sigmoid": MOE_SCORE_SIGMOID, "softmax": MOE_SCORE_SOFTMAX}
+_GROUP_SCORES = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2_SUM}
+
+
+def _need(fn: str, **tensors) -> None:
+    """(tensor, dtype, shape) by name: what the C call takes for granted about
+    a tensor's storage (its dtype, its size, no gaps) is checked here."""
+    for name, (t, dtype, shape) in tensors.items():
+        if t.dtype != dtype and not (dtype == torch.uint8 and t.dtype == torch.float8_e4m3fn):
+            raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be contiguous")
+
+
+def _rows_of(fn: str, name: str, t: torch.Tensor, dtypes) -> int:
+    """Row stride (elements) of a 2-D tensor whose rows have no gaps."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{fn}: {name} must be one of {dtypes}, not {t.dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{fn}: {name} must be 2-D with contiguous rows")
+    # (a single row's stride is free; torch leaves any number there)
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def scale_blocks(n: int) -> int:
+    """Scales along n inputs or outputs: one per 128, the last block may be short."""
+    return (n + 127) // 128
+
+
+_F8 = (torch.float8_e4m3fn, torch.uint8)
+_XDT = (torch.float32, torch.bfloat16)
+
+
+def gate(n_experts: int, top_k: int, score="sigmoid", n_groups=1, top_groups=1, group_score="max", renormalize=True,
+         scale=1.0, bias=None) -> MoeGate:
+    """A gate's description for gate_topk (it keeps the bias tensor alive)."""
+    if bias is not None:
+        _need("gate", bias=(bias, torch.float32, (n_experts,)))
+    g = MoeGate(abi_version=MOE_ABI_VERSION, n_experts=n_experts, top_k=top_k, score=_SCORES[score],
+                n_groups=n_groups, top_groups=top_groups, group_score=_GROUP_SCORES[group_score],
+                renormalize=1 if renormalize else 0, scale=scale, bias=_ptr(bias))
+    g.bias_tensor = bias
+    return g
+
+
+def router_logits(w_router, x, z, stream=None) -> None:
+    E, d = w_router.shape
+    T = x.shape[0]
+    _need("router_logits", w_router=(w_router, torch.float32, (E, d)), x=(x, x.dtype, (T, d)),
+          z=(z, torch.float32, (T, E)))
+    _check(lib().moe_router_logits(_ptr(w_router), E, d, _ptr(x), x_dtype_of(x), T, _ptr(z), _stream(stream)))
+
+
+def gate_topk(gate: MoeGate, z, idx, wt, stream=None) -> None:
+    T, k = z.shape[0], gate.top_k
+    stride = _rows_of("gate_topk", "z", z, _XDT)
+    if z.shape[1] != gate.n_experts:
+        raise ValueError(f"gate_topk: z has {z.shape[1]} logits per row, the gate {gate.n_experts} experts")
+    _need("gate_topk", idx=(idx, torch.int32, (T, k)), wt=(wt, torch.float32, (T, k)))
+    _check(lib().moe_gate_topk(ctypes.byref(gate), _ptr(z), x_dtype_of(z), stride, T, _ptr(idx), _ptr(wt),
+                               _stream(stream)))
+
+
+def blockscale_quantize(x, q, s, stream=None) -> None:
+    """x [M][K] to q (float8_e4m3fn or uint8) [M][K] and s [M][ceil(K / 128)]."""
+    fn = "blockscale_quantize"
+    M, K = x.shape
+    ldx, ldq = _rows_of(fn, "x", x, _XDT), _rows_of(fn, "q", q, _F8)
+    if q.shape != x.shape:
+        raise ValueError(f"{fn}: q has shape {tuple(q.shape)}, needs {tuple(x.shape)}")
+    _need(fn, s=(s, torch.float32, (M, scale_blocks(K))))
+    _check(lib().moe_blockscale_quantize(_ptr(x), x_dtype_of(x), ldx, M, K, _ptr(q), ldq, _ptr(s), _stream(stream)))
+
+
+def blockscale_matmul_workspace_bytes(M: int, N: int, K: int) -> int:
+    out = _SZ()
+    _check(lib().moe_blockscale_matmul_workspace_bytes(M, N, K, ctypes.byref(out)))
+    return out.value
+
+
+def blockscale_matmul(xq, xs, wq, ws, y, workspace=None, stream=None) -> None:
+    """y [M][N] (float32 or bfloat16) = xq [M][K] times wq [N][K] transposed,
+    with scales xs [M][ceil(K / 128)] and ws [ceil(N / 128)][ceil(K / 128)]."""
+    fn = "blockscale_matmul"
+    (M, K), N = xq.shape, wq.shape[0]
+    KB = scale_blocks(K)
+    ldx, ldy = _rows_of(fn, "xq", xq, _F8), _rows_of(fn, "y", y, _XDT)
+    if y.shape != (M, N):
+        raise ValueError(f"{fn}: y has shape {tuple(y.shape)}, needs {(M, N)}")
+    _need(fn, xs=(xs, torch.float32, (M, KB)), wq=(wq, torch.uint8, (N, K)),
+          ws=(ws, torch.float32, (scale_blocks(N), KB)))
+    n_ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().moe_blockscale_matmul(_ptr(xq), ldx, _ptr(xs), M, _ptr(wq), _ptr(ws), N, K, _ptr(y), x_dtype_of(y),
+                                       ldy, _ptr(workspace), n_ws, _stream(stream)))
+
+
+def blockscale_gateup(xq, xs, k, offsets, perm, w_gate, s_gate, w_up, s_up, hq, hs, stream=None) -> None:
+    """hq [T*k][f], hs [T*k][ceil(f / 128)]: the bucket rows' silu(gate) * up,
+    requantised; offsets and perm as bucket() writes them."""
+    fn = "blockscale_gateup"
+    (T, d), (E, f, _) = xq.shape, w_gate.shape
+    DB, FB = scale_blocks(d), scale_blocks(f)
+    _need(fn, xq=(xq, torch.uint8, (T, d)), xs=(xs, torch.float32, (T, DB)), offsets=(offsets, torch.int32, (E + 1,)),
+          perm=(perm, torch.int32, (T * k,)), w_gate=(w_gate, torch.uint8, (E, f, d)),
+          s_gate=(s_gate, torch.float32, (E, FB, DB)), w_up=(w_up, torch.uint8, (E, f, d)),
+          s_up=(s_up, torch.float32, (E, FB, DB)), hq=(hq, torch.uint8, (T * k, f)),
+          hs=(hs, torch.float32, (T * k, FB)))
+    _check(lib().moe_blockscale_gateup(_ptr(xq), _ptr(xs), T, k, _ptr(offsets), _ptr(perm), E, _ptr(w_gate),
+                                       _ptr(s_gate), _ptr(w_up), _ptr(s_up), f, d, _ptr(hq), _ptr(hs),
+                                       _stream(stream)))
+
+
+def blockscale_down_workspace_bytes(T: int, k: int, d: int) -> int:
+    out = _SZ()
+    _check(lib().moe_blockscale_down_workspace_bytes(T, k, d, ctypes.byref(out)))
+    return out.value
+
+
+def blockscale_down(hq, hs, wt, offsets, pos, w_down, s_down, y, workspace, add=None, stream=None) -> None:
+    """y [T][d] = add + the weighted sum of each token's experts' down products."""
+    fn = "blockscale_down"
+    (T, k), (E, d, f) = wt.shape, w_down.shape
+    FB = scale_blocks(f)
+    _need(fn, hq=(hq, torch.uint8, (T * k, f)), hs=(hs, torch.float32, (T * k, FB)), wt=(wt, torch.float32, (T, k)),
+          offsets=(offsets, torch.int32, (E + 1,)), pos=(pos, torch.int32, (T * k,)),
+          w_down=(w_down, torch.uint8, (E, d, f)), s_down=(s_down, torch.float32, (E, scale_blocks(d), FB)),
+          y=(y, torch.float32, (T, d)))
+    if add is not None:
+        _need(fn, add=(add, torch.float32, (T, d)))
+    n_ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().moe_blockscale_down(_ptr(hq), _ptr(hs), T, k, _ptr(wt), _ptr(offsets), _ptr(pos), E, _ptr(w_down),
+                                     _ptr(s_down), d, f, _ptr(add), _ptr(y), _ptr(workspace), n_ws,
+                                     _stream(stream)))
 
 
 def profile_enable(on: bool) -> None:
