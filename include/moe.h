@@ -546,7 +546,7 @@ int moe_blockscale_quantize(const void* x, int32_t x_dtype, int64_t ldx, int32_t
 
 /*
  * y[m][n] = sum over blocks b of xs[m][b] ws[n/128][b] (xq[m] . wq[n])_b.
- * xq [M] rows ldx bytes apart; wq [N][K]; y [M] rows of N in y_dtype
+ * xq [M] rows ldx bytes apart (at most 2^22); wq [N][K]; y [M] rows of N in y_dtype
  * (MOE_F32 or MOE_BF16, rounded once), ldy elements apart (rows aligned to
  * their element).  Workspace: moe_blockscale_matmul_workspace_bytes of the
  * same M, N, K (null if that is 0): partial sums where few outputs share a

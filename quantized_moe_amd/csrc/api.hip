@@ -1043,8 +1043,9 @@ extern "C" int moe_blockscale_matmul(const uint8_t* xq, int64_t ldx, const float
   if ((rc = check_bs_rows(fn, M)) || (rc = check_bs_k(fn, "K", K)) || (rc = check_bs_outputs(fn, N, K))) return rc;
   if (y_dtype != MOE_F32 && y_dtype != MOE_BF16)
     return fail(MOE_ERR_UNSUPPORTED, "%s: unknown output dtype %d", fn, y_dtype);
-  if (ldx < K || ldx % 16 != 0)
-    return fail(MOE_ERR_INVALID_ARG, "%s: ldx %lld is below K %d or not a multiple of 16", fn, (long long)ldx, K);
+  if (ldx < K || ldx % 16 != 0 || ldx > BS_MAX_LDX)
+    return fail(MOE_ERR_INVALID_ARG, "%s: ldx %lld is below K %d, above %d or not a multiple of 16", fn, (long long)ldx,
+                K, BS_MAX_LDX);
   if (ldy < N) return fail(MOE_ERR_INVALID_ARG, "%s: ldy %lld below N %d", fn, (long long)ldy, N);
   if (M == 0) return ok();
   NEED_PTR(xq, "xq");

@@ -72,6 +72,88 @@ __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v
 // One output value, fp32 or bf16 (nearest even).
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 
+// E4M3 bytes on the matrix unit's own E4M3 step (see above for its sums).
+__device__ __forceinline__ f32x4_t mfma_block_e4m3(i32x8_t w, i32x8_t x) {
+  const f32x4_t z = {0.0f, 0.0f, 0.0f, 0.0f};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, z, 0, 0, 0, 127, 0, 127);  // unit scales 2^0
+}
+
+// One lane's operand of a block as fp16, converted once and used for several
+// tiles.
+struct F16Block {
+  f16x8_t s[4];
+  __device__ __forceinline__ void set(i32x8_t v) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) s[i] = e4m3_to_f16(v[2 * i], v[2 * i + 1]);
+  }
+};
+__device__ __forceinline__ f32x4_t mfma_block(const F16Block& w, const F16Block& x) {
+  f32x4_t p = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 4; i++) p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w.s[i], x.s[i], p, 0, 0, 0);
+  return p;
+}
+
+// Asynchronous copies from a buffer straight into LDS: lane l's 16 (or 4)
+// bytes land at LDS byte address lds + 16 l (4 l); offsets outside the buffer
+// give zeros.  Written out because the compiler cannot tell the LDS buffers of
+// a pipeline apart and would wait for every copy in flight before each read of
+// LDS.  They have no output registers; the waits are lds_landed() below.  (m0
+// holds the address; nothing else in these kernels uses m0.)
+__device__ __forceinline__ void lds_copy16(__amdgpu_buffer_rsrc_t r, uint32_t lds, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               ::"s"(lds), "v"(off), "s"(r)
+               : "memory");
+}
+__device__ __forceinline__ void lds_copy4(__amdgpu_buffer_rsrc_t r, uint32_t lds, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               ::"s"(lds), "v"(off), "s"(r)
+               : "memory");
+}
+// All but the N youngest copies of this wave have landed, its reads of LDS are
+// done, and so it is for every wave of the block.
+template <int N>
+__device__ __forceinline__ void lds_landed() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+// A buffer of `bytes` (< 2^31) bytes at p (the same in every lane).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
+}
+constexpr uint32_t BUFFER_OUT = 0x80000000u;  // an offset outside every such buffer
+
+// Work ids such that the blocks of one XCD (block id mod 8) take a contiguous
+// eighth of them: a bijection on [0, n).
+__device__ __forceinline__ int xcd_order(int block, int n) {
+  const int xcd = block & 7, i = block >> 3, base = n >> 3, more = n & 7;
+  return xcd * base + min(xcd, more) + i;
+}
+
+// Four consecutive outputs; `left` of them exist (<= 0: none).
+__device__ __forceinline__ void store4(float* p, f32x4_t v, int left, bool vec) {
+  if (vec && left >= 4) {
+    *reinterpret_cast<f32x4_t*>(p) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      if (i < left) p[i] = v[i];
+  }
+}
+__device__ __forceinline__ void store4(uint16_t* p, f32x4_t v, int left, bool vec) {
+  if (vec && left >= 4) {
+    const uint32_t lo = bf16_bits(v[0]) | (uint32_t)bf16_bits(v[1]) << 16;
+    const uint32_t hi = bf16_bits(v[2]) | (uint32_t)bf16_bits(v[3]) << 16;
+    *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      if (i < left) p[i] = bf16_bits(v[i]);
+  }
+}
+
 // The M tile of `bm` bucket rows that is the `tile`-th over all experts:
 // expert e, first row and row count.  false: there are fewer tiles.  Every
 // lane of a wave calls it with the same tile.

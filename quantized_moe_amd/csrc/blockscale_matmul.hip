@@ -47,20 +47,171 @@ __global__ __launch_bounds__(256) void bs_matmul_kernel(const uint8_t* __restric
   }
 }
 
+// Tiled form: WN x WM waves, each TN x TM tiles of 16 outputs x 16 rows.  The
+// operands of a block of 128 inputs go to LDS by asynchronous copies while the
+// block before is multiplied; 16-byte piece p of row i lies at place p ^ (i %
+// 8), so the 8 rows that a read touches at once are in different banks.
+// EXACT: fp16 steps (fp32 outputs); else the unit's E4M3 steps, twice as fast.
+template <int WN, int WM, int TN, int TM, bool EXACT>
+struct Tile {
+  static constexpr int BN = WN * TN * 16, BM = WM * TM * 16, THREADS = 64 * WN * WM;
+  static constexpr int W_BYTES = BN * BS, X_BYTES = BM * BS, S_BYTES = BM * 4;
+  static constexpr int STAGE = W_BYTES + X_BYTES + S_BYTES;
+  static constexpr int LDS = 2 * STAGE;
+  static constexpr int W_COPIES = BN / 8 / (WN * WM), X_COPIES = BM / 8 / (WN * WM);  // per wave and block
+  static_assert(TN * 16 <= BS && BS % (TN * 16) == 0, "one weight scale per wave and block");
+  static_assert(BM % 64 == 0 && BM / 64 <= WN * WM, "scale copies");
+};
+
+template <int WN, int WM, int TN, int TM, bool EXACT, typename OUT>
+__global__ __launch_bounds__(64 * WN * WM, 2) void bs_matmul_tile_kernel(BsMatmul a, int n_tiles, int m_tiles) {
+  using C = Tile<WN, WM, TN, TM, EXACT>;
+  extern __shared__ __align__(1024) uint8_t lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, quad = lane >> 4;
+  // an XCD (block id mod 8) takes a contiguous eighth of the tiles, in strips
+  // of 4 M tiles so that neighbours in time share operands in its L2
+  const int tiles = n_tiles * m_tiles;
+  const int id = xcd_order(blockIdx.x, tiles);
+  const int strip = id / (4 * n_tiles), in_strip = id - strip * 4 * n_tiles;
+  const int strip_m = min(4, m_tiles - 4 * strip);
+  const int mt = 4 * strip + in_strip % strip_m, nt = in_strip / strip_m;
+  const int n0 = nt * C::BN, m0 = mt * C::BM;
+  const int KB = bs_blocks(a.K);
+  const int rows_n = min(C::BN, a.N - n0), rows_m = min(C::BM, a.M - m0);
+
+  const __amdgpu_buffer_rsrc_t wbuf = buffer_of(a.wq + (int64_t)n0 * a.K, (int64_t)rows_n * a.K);
+  const __amdgpu_buffer_rsrc_t xbuf = buffer_of(a.xq + m0 * a.ldx, (rows_m - 1) * a.ldx + a.K);
+  const __amdgpu_buffer_rsrc_t sbuf = buffer_of(a.xs + (int64_t)m0 * KB, (int64_t)rows_m * KB * 4);
+  // copy i of a wave brings rows 8 (wave + i waves) .. + 7; lane l row l / 8
+  const int col = ((lane & 7) ^ (lane >> 3)) * 16;
+  constexpr int WAVES = WN * WM;
+  uint32_t woff[C::W_COPIES], xoff[C::X_COPIES];
+#pragma unroll
+  for (int i = 0; i < C::W_COPIES; i++) woff[i] = (uint32_t)(8 * (wave + i * WAVES) + (lane >> 3)) * a.K + col;
+#pragma unroll
+  for (int i = 0; i < C::X_COPIES; i++) {
+    const int row = 8 * (wave + i * WAVES) + (lane >> 3);
+    xoff[i] = row < rows_m ? (uint32_t)(row * a.ldx) + col : BUFFER_OUT;
+  }
+  const uint32_t soff = (uint32_t)(wave * 64 + lane) * KB * 4;
+  const uint32_t base = lds_address(lds);
+  auto fetch = [&](int kb, int stage) {
+    const uint32_t at = base + stage * C::STAGE;
+    // past K (a short last block) a lane's piece is zeros, not the next row's
+    const uint32_t out = kb * BS + col < a.K ? 0u : BUFFER_OUT;
+#pragma unroll
+    for (int i = 0; i < C::W_COPIES; i++)
+      lds_copy16(wbuf, at + (wave + i * WAVES) * 1024, (woff[i] + kb * BS) | out);
+#pragma unroll
+    for (int i = 0; i < C::X_COPIES; i++)
+      lds_copy16(xbuf, at + C::W_BYTES + (wave + i * WAVES) * 1024, (xoff[i] + kb * BS) | out);
+    if (wave < C::BM / 64) lds_copy4(sbuf, at + C::W_BYTES + C::X_BYTES + wave * 256, soff + kb * 4);
+  };
+
+  const int wn = wave % WN, wm = wave / WN;
+  const float* wsr = a.ws + (int64_t)min((n0 + wn * TN * 16) / BS, bs_blocks(a.N) - 1) * KB;
+  const int swz0 = (quad ^ (r & 7)) * 16, swz1 = ((quad + 4) ^ (r & 7)) * 16;
+  auto frag = [&](const uint8_t* tile, int row) {  // the lane's 32 bytes of the tile's row (row % 8 == r % 8)
+    const uint8_t* p = tile + row * BS;
+    return join_pieces(*reinterpret_cast<const i32x4_t*>(p + swz0), *reinterpret_cast<const i32x4_t*>(p + swz1));
+  };
+  f32x4_t acc[TN][TM] = {};
+  fetch(0, 0);
+  lds_landed<0>();
+  for (int kb = 0; kb < KB; kb++) {
+    const uint8_t* st = lds + (kb & 1) * C::STAGE;
+    if (kb + 1 < KB) fetch(kb + 1, (kb + 1) & 1);
+    const uint8_t* wt = st + wn * TN * 16 * BS;
+    const uint8_t* xt = st + C::W_BYTES + wm * TM * 16 * BS;
+    const float* xsc = reinterpret_cast<const float*>(st + C::W_BYTES + C::X_BYTES) + wm * TM * 16;
+    const float wsc = wsr[kb];
+    float sc[TM];
+#pragma unroll
+    for (int j = 0; j < TM; j++) sc[j] = xsc[j * 16 + r] * wsc;
+    if constexpr (EXACT) {
+      F16Block x[TM];
+#pragma unroll
+      for (int j = 0; j < TM; j++) x[j].set(frag(xt, j * 16 + r));
+#pragma unroll
+      for (int i = 0; i < TN; i++) {
+        F16Block w;
+        w.set(frag(wt, i * 16 + r));
+#pragma unroll
+        for (int j = 0; j < TM; j++) {
+          const f32x4_t p = mfma_block(w, x[j]);
+#pragma unroll
+          for (int q = 0; q < 4; q++) acc[i][j][q] = __builtin_fmaf(p[q], sc[j], acc[i][j][q]);
+        }
+      }
+    } else {
+      i32x8_t x[TM];
+#pragma unroll
+      for (int j = 0; j < TM; j++) x[j] = frag(xt, j * 16 + r);
+#pragma unroll
+      for (int i = 0; i < TN; i++) {
+        const i32x8_t w = frag(wt, i * 16 + r);
+        f32x4_t p[TM];
+#pragma unroll
+        for (int j = 0; j < TM; j++) p[j] = mfma_block_e4m3(w, x[j]);
+#pragma unroll
+        for (int j = 0; j < TM; j++)
+#pragma unroll
+          for (int q = 0; q < 4; q++) acc[i][j][q] = __builtin_fmaf(p[j][q], sc[j], acc[i][j][q]);
+      }
+    }
+    lds_landed<0>();
+  }
+
+  OUT* y = static_cast<OUT*>(a.y);
+  // four outputs leave as one store where every row allows it
+  const bool vec = a.ldy % 4 == 0 && ((uintptr_t)a.y & (4 * sizeof(OUT) - 1)) == 0;
+#pragma unroll
+  for (int j = 0; j < TM; j++) {
+    const int m = m0 + (wm * TM + j) * 16 + r;
+    if (m >= a.M) continue;
+    OUT* row = y + m * a.ldy;
+#pragma unroll
+    for (int i = 0; i < TN; i++) {
+      const int n = n0 + (wn * TN + i) * 16 + 4 * quad;
+      store4(row + n, acc[i][j], a.N - n, vec);
+    }
+  }
+}
+
 size_t bs_matmul_ws(int, int, int) { return 0; }
 
-hipError_t launch_bs_matmul(const BsMatmul& a, hipStream_t s) {
-  const int n_tiles = (a.N + 63) / 64;
-  const dim3 grid((unsigned)((int64_t)n_tiles * ((a.M + 15) / 16)));
-  const int pid = prof_begin("bs_matmul", s);
-  if (a.y_dtype == X_BF16)
-    QMOE_LAUNCH(bs_matmul_kernel<uint16_t>, grid, dim3(256), 0, s, a.xq, a.ldx, a.xs, a.M, a.wq, a.ws, a.N, a.K,
-                (uint16_t*)a.y, a.ldy, n_tiles);
-  else
-    QMOE_LAUNCH(bs_matmul_kernel<float>, grid, dim3(256), 0, s, a.xq, a.ldx, a.xs, a.M, a.wq, a.ws, a.N, a.K,
-                (float*)a.y, a.ldy, n_tiles);
-  prof_end(pid, s);
+template <int WN, int WM, int TN, int TM, bool EXACT, typename OUT>
+static hipError_t launch_tile(const BsMatmul& a, hipStream_t s) {
+  using C = Tile<WN, WM, TN, TM, EXACT>;
+  const int n_tiles = (a.N + C::BN - 1) / C::BN, m_tiles = (a.M + C::BM - 1) / C::BM;
+  auto* k = bs_matmul_tile_kernel<WN, WM, TN, TM, EXACT, OUT>;
+  int per_cu, cus;
+  hipError_t e = launch_shape((const void*)k, C::THREADS, C::LDS, C::LDS, &per_cu, &cus);
+  if (e != hipSuccess) return e;
+  QMOE_LAUNCH(k, dim3((unsigned)(n_tiles * m_tiles)), dim3(C::THREADS), C::LDS, s, a, n_tiles, m_tiles);
   return hipGetLastError();
+}
+
+template <typename OUT>
+static hipError_t launch_matmul(const BsMatmul& a, hipStream_t s) {
+  if (a.M <= 32) {
+    const int n_tiles = (a.N + 63) / 64;
+    const dim3 grid((unsigned)((int64_t)n_tiles * ((a.M + 15) / 16)));
+    QMOE_LAUNCH(bs_matmul_kernel<OUT>, grid, dim3(256), 0, s, a.xq, a.ldx, a.xs, a.M, a.wq, a.ws, a.N, a.K, (OUT*)a.y,
+                a.ldy, n_tiles);
+    return hipGetLastError();
+  }
+  if (sizeof(OUT) == 2 && a.K >= 1024 && (int64_t)a.M * a.N >= 256 * 256 * 128)
+    return launch_tile<2, 4, 8, 4, false, OUT>(a, s);
+  return launch_tile<2, 2, 4, 4, true, OUT>(a, s);
+}
+
+hipError_t launch_bs_matmul(const BsMatmul& a, hipStream_t s) {
+  const int pid = prof_begin("bs_matmul", s);
+  const hipError_t e = a.y_dtype == X_BF16 ? launch_matmul<uint16_t>(a, s) : launch_matmul<float>(a, s);
+  prof_end(pid, s);
+  return e;
 }
 
 }  // namespace qmoe

@@ -17,6 +17,7 @@ constexpr int TOPK_MAX_PER_LANE = MAX_EXPERTS / 64;
 constexpr int ROUTER_ROWS_MAX_T = 8;  // above this the tiled router runs (router + top-k measured 29 / 32 us at 8 tokens, 51 / 33 us at 16)
 constexpr int GATE_MAX_GROUPS = 64;
 constexpr int BS_MAX_K = 16384, BS_MAX_N = 65536, BS_MAX_ROWS = 1 << 20;  // block-scaled operators
+constexpr int BS_MAX_LDX = 1 << 22;  // (a tile's rows are addressed with 31-bit byte offsets)
 constexpr int DECODE_MAX_T = MOE_DECODE_MAX_T;            // the decode path's limit
 constexpr int AUTO_DECODE_MAX_T = MOE_AUTO_DECODE_MAX_T;  // MOE_PATH_AUTO's switch to prefill
 

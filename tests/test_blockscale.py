@@ -155,6 +155,24 @@ def test_matmul(M, N, K, out):
 
 
 @gpu
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,N,K", [(2090, 4100, 1040), (4097, 2050, 2064), (700, 640, 4112)])
+def test_matmul_many_tiles(M, N, K, out):
+    """Several tiles of the largest kind in both directions, the last ones short."""
+    rng = np.random.default_rng(M + N)
+    (xq, xs), (wq, ws) = make_rows(rng, M, K), make_weight(rng, N, K)
+    y = torch.empty(M, N, dtype=out, device=DEV)
+    work = torch.empty(max(16, lib.blockscale_matmul_workspace_bytes(M, N, K)), dtype=torch.uint8, device=DEV)
+    lib.blockscale_matmul(up(xq), up(xs), up(wq), up(ws), y, work)
+    rows = torch.from_numpy(np.unique(np.concatenate([np.arange(20), M - 1 - np.arange(60), rng.integers(0, M, 200)])))
+    ref, mag = product(values_rows(xq, xs)[rows], values_weight(wq, ws))
+    tol = SUM(K) * mag + (2.0 ** -8 * ref.abs() if out == torch.bfloat16 else 0)
+    err = (y.cpu().double()[rows] - ref).abs()
+    assert (err <= tol).all(), float((err / tol).max())
+    assert torch.isfinite(y).all()
+
+
+@gpu
 def test_matmul_nan_codes_and_scales_stay_in_their_rows():
     rng = np.random.default_rng(5)
     M, N, K = 40, 200, 400
@@ -423,7 +441,7 @@ def test_quantize_refusals(kw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(y_dtype=7), "UNSUPPORTED"), (dict(M=-2), "INVALID_ARG"), (dict(N=0), "INVALID_ARG"),
     (dict(N=65537), "INVALID_ARG"), (dict(K=40), "INVALID_ARG"), (dict(K=16384, N=65536, ldx=16384, ldy=65536), "OK?"),
-    (dict(ldx=240), "INVALID_ARG"), (dict(ldx=260), "INVALID_ARG"), (dict(ldy=63), "INVALID_ARG"),
+    (dict(ldx=240), "INVALID_ARG"), (dict(ldx=260), "INVALID_ARG"), (dict(ldx=(1 << 22) + 16), "INVALID_ARG"), (dict(ldy=63), "INVALID_ARG"),
     (dict(xq=None), "INVALID_ARG"), (dict(xs=P + 4), "INVALID_ARG"), (dict(wq=P + 1), "INVALID_ARG"),
     (dict(ws=None), "INVALID_ARG"), (dict(y=None), "INVALID_ARG"),
 ])
