@@ -57,7 +57,8 @@ struct Tile {
   static constexpr int BN = WN * TN * 16, BM = WM * TM * 16, THREADS = 64 * WN * WM;
   static constexpr int W_BYTES = BN * BS, X_BYTES = BM * BS, S_BYTES = BM * 4;
   static constexpr int STAGE = W_BYTES + X_BYTES + S_BYTES;
-  static constexpr int LDS = 2 * STAGE;
+  static constexpr int NB = (BN + BS - 1) / BS;                 // weight scale rows of a tile
+  static constexpr int LDS = 2 * STAGE + NB * (BS_MAX_K / BS) * 4;  // ... kept whole behind the stages
   static constexpr int W_COPIES = BN / 8 / (WN * WM), X_COPIES = BM / 8 / (WN * WM);  // per wave and block
   static_assert(TN * 16 <= BS && BS % (TN * 16) == 0, "one weight scale per wave and block");
   static_assert(BM % 64 == 0 && BM / 64 <= WN * WM, "scale copies");
@@ -110,7 +111,14 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void bs_matmul_tile_kernel(BsMatmu
   };
 
   const int wn = wave % WN, wm = wave / WN;
-  const float* wsr = a.ws + (int64_t)min((n0 + wn * TN * 16) / BS, bs_blocks(a.N) - 1) * KB;
+  // The weight scales of the whole tile are staged once: loads of them in the
+  // loop would wait for the copies in flight (one counter counts both).
+  float* wsc_all = reinterpret_cast<float*>(lds + 2 * C::STAGE);
+  for (int i = threadIdx.x; i < C::NB * KB; i += C::THREADS) {
+    const int b = min(n0 / BS + i / KB, bs_blocks(a.N) - 1);
+    wsc_all[i] = a.ws[(int64_t)b * KB + i % KB];
+  }
+  const float* wsr = wsc_all + (wn * TN * 16) / BS * KB;
   const int swz0 = (quad ^ (r & 7)) * 16, swz1 = ((quad + 4) ^ (r & 7)) * 16;
   auto frag = [&](const uint8_t* tile, int row) {  // the lane's 32 bytes of the tile's row (row % 8 == r % 8)
     const uint8_t* p = tile + row * BS;
