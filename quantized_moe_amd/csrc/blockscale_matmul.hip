@@ -156,16 +156,25 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void bs_matmul_tile_kernel(BsMatmu
       i32x8_t x[TM];
 #pragma unroll
       for (int j = 0; j < TM; j++) x[j] = frag(xt, j * 16 + r);
+      // Tile row i is multiplied while row i - 1's sums are scaled: one matrix
+      // step, then the four multiply-adds that run in its shadow.
+      i32x8_t w = frag(wt, r);
+      f32x4_t p[2][TM];
 #pragma unroll
-      for (int i = 0; i < TN; i++) {
-        const i32x8_t w = frag(wt, i * 16 + r);
-        f32x4_t p[TM];
+      for (int i = 0; i <= TN; i++) {
+        i32x8_t w_next = w;
+        if (i + 1 < TN) w_next = frag(wt, (i + 1) * 16 + r);
 #pragma unroll
-        for (int j = 0; j < TM; j++) p[j] = mfma_block_e4m3(w, x[j]);
+        for (int j = 0; j < TM; j++) {
+          if (i < TN) p[i & 1][j] = mfma_block_e4m3(w, x[j]);
+          if (i > 0) {
 #pragma unroll
-        for (int j = 0; j < TM; j++)
-#pragma unroll
-          for (int q = 0; q < 4; q++) acc[i][j][q] = __builtin_fmaf(p[j][q], sc[j], acc[i][j][q]);
+            for (int q = 0; q < 4; q++)
+              acc[i - 1][j][q] = __builtin_fmaf(p[(i - 1) & 1][j][q], sc[j], acc[i - 1][j][q]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        w = w_next;
       }
     }
     lds_landed<0>();
