@@ -58,8 +58,10 @@ struct Tile {
   static constexpr int W_BYTES = BN * BS, X_BYTES = BM * BS, S_BYTES = BM * 4;
   static constexpr int STAGE = W_BYTES + X_BYTES + S_BYTES;
   static constexpr int NB = (BN + BS - 1) / BS;                 // weight scale rows of a tile
-  static constexpr int LDS = 2 * STAGE + NB * (BS_MAX_K / BS) * 4;  // ... kept whole behind the stages
+  static constexpr int SCALES = 2 * STAGE;                      // ... kept whole behind the stages
+  static constexpr int LDS = SCALES + NB * (BS_MAX_K / BS) * 4;
   static constexpr int W_COPIES = BN / 8 / (WN * WM), X_COPIES = BM / 8 / (WN * WM);  // per wave and block
+  static constexpr int COPIES = W_COPIES + X_COPIES, PER_ROW = (COPIES + TN / 2 - 1) / (TN / 2);
   static_assert(TN * 16 <= BS && BS % (TN * 16) == 0, "one weight scale per wave and block");
   static_assert(BM % 64 == 0 && BM / 64 <= WN * WM, "scale copies");
 };
@@ -97,23 +99,29 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void bs_matmul_tile_kernel(BsMatmu
   }
   const uint32_t soff = (uint32_t)(wave * 64 + lane) * KB * 4;
   const uint32_t base = lds_address(lds);
-  auto fetch = [&](int kb, int stage) {
+  // Copy i of block kb, i < COPIES (the scales go with copy 0).
+  auto fetch = [&](int kb, int stage, int i) {
     const uint32_t at = base + stage * C::STAGE;
-    // past K (a short last block) a lane's piece is zeros, not the next row's
+    if (i < C::W_COPIES)
+      lds_copy16(wbuf, at + (wave + i * WAVES) * 1024, woff[i], kb * BS);
+    else
+      lds_copy16(xbuf, at + C::W_BYTES + (wave + (i - C::W_COPIES) * WAVES) * 1024, xoff[i - C::W_COPIES], kb * BS);
+    if (i == 0 && wave < C::BM / 64) lds_copy4(sbuf, at + C::W_BYTES + C::X_BYTES + wave * 256, soff, kb * 4);
+  };
+  // In a short last block the pieces past K are zeros, not the next row's.
+  auto cut_last = [&](int kb) {
+    if (kb * BS + BS <= a.K) return;
     const uint32_t out = kb * BS + col < a.K ? 0u : BUFFER_OUT;
 #pragma unroll
-    for (int i = 0; i < C::W_COPIES; i++)
-      lds_copy16(wbuf, at + (wave + i * WAVES) * 1024, (woff[i] + kb * BS) | out);
+    for (int i = 0; i < C::W_COPIES; i++) woff[i] |= out;
 #pragma unroll
-    for (int i = 0; i < C::X_COPIES; i++)
-      lds_copy16(xbuf, at + C::W_BYTES + (wave + i * WAVES) * 1024, (xoff[i] + kb * BS) | out);
-    if (wave < C::BM / 64) lds_copy4(sbuf, at + C::W_BYTES + C::X_BYTES + wave * 256, soff + kb * 4);
+    for (int i = 0; i < C::X_COPIES; i++) xoff[i] |= out;
   };
 
   const int wn = wave % WN, wm = wave / WN;
   // The weight scales of the whole tile are staged once: loads of them in the
   // loop would wait for the copies in flight (one counter counts both).
-  float* wsc_all = reinterpret_cast<float*>(lds + 2 * C::STAGE);
+  float* wsc_all = reinterpret_cast<float*>(lds + C::SCALES);
   for (int i = threadIdx.x; i < C::NB * KB; i += C::THREADS) {
     const int b = min(n0 / BS + i / KB, bs_blocks(a.N) - 1);
     wsc_all[i] = a.ws[(int64_t)b * KB + i % KB];
@@ -125,11 +133,22 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void bs_matmul_tile_kernel(BsMatmu
     return join_pieces(*reinterpret_cast<const i32x4_t*>(p + swz0), *reinterpret_cast<const i32x4_t*>(p + swz1));
   };
   f32x4_t acc[TN][TM] = {};
-  fetch(0, 0);
+  cut_last(0);
+#pragma unroll
+  for (int i = 0; i < C::COPIES; i++) fetch(0, 0, i);
   lds_landed<0>();
   for (int kb = 0; kb < KB; kb++) {
-    const uint8_t* st = lds + (kb & 1) * C::STAGE;
-    if (kb + 1 < KB) fetch(kb + 1, (kb + 1) & 1);
+    const int stage = kb & 1;
+    const uint8_t* st = lds + stage * C::STAGE;
+    // The next block's copies are spread over the tile rows of this one: all
+    // at once they fill the address queue and hold up the waves.  (After the
+    // last block it is fetched again, into the stage that nothing reads.)
+    const int next = min(kb + 1, KB - 1);
+    cut_last(next);
+    auto fetch_some = [&](int i) {
+#pragma unroll
+      for (int c = i * C::PER_ROW; c < (i + 1) * C::PER_ROW && c < C::COPIES; c++) fetch(next, 1 - stage, c);
+    };
     const uint8_t* wt = st + wn * TN * 16 * BS;
     const uint8_t* xt = st + C::W_BYTES + wm * TM * 16 * BS;
     const float* xsc = reinterpret_cast<const float*>(st + C::W_BYTES + C::X_BYTES) + wm * TM * 16;
@@ -143,6 +162,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void bs_matmul_tile_kernel(BsMatmu
       for (int j = 0; j < TM; j++) x[j].set(frag(xt, j * 16 + r));
 #pragma unroll
       for (int i = 0; i < TN; i++) {
+        fetch_some(i);
         F16Block w;
         w.set(frag(wt, i * 16 + r));
 #pragma unroll
@@ -162,6 +182,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void bs_matmul_tile_kernel(BsMatmu
       f32x4_t p[2][TM];
 #pragma unroll
       for (int i = 0; i <= TN; i++) {
+        fetch_some(i);
         i32x8_t w_next = w;
         if (i + 1 < TN) w_next = frag(wt, (i + 1) * 16 + r);
 #pragma unroll
