@@ -124,6 +124,16 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int64
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
 }
 constexpr uint32_t BUFFER_OUT = 0x80000000u;  // an offset outside every such buffer
+// Offset a + b, outside if one of them is (both below 2^31 otherwise, as is
+// their sum).
+__device__ __forceinline__ uint32_t out_or_sum(uint32_t a, uint32_t b) { return (a + b) | ((a | b) & BUFFER_OUT); }
+// Loads into registers; outside the buffer they give zeros.
+__device__ __forceinline__ i32x4_t buffer_load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+__device__ __forceinline__ float buffer_load4(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+}
 
 // Work ids such that the blocks of one XCD (block id mod 8) take a contiguous
 // eighth of them: a bijection on [0, n).

@@ -3,48 +3,71 @@
 
 namespace qmoe {
 
-// The 32 bytes of one lane's operand row in block kb (see blockscale.hpp), 0
-// past K or for a row that does not exist.
-__device__ __forceinline__ i32x8_t load_frag(const uint8_t* row, bool ok, int kb, int K, int quad) {
-  const i32x4_t z = {0, 0, 0, 0};
-  const int k0 = kb * BS + 16 * quad, k1 = k0 + 64;
-  const i32x4_t a = ok && k0 < K ? *reinterpret_cast<const i32x4_t*>(row + k0) : z;
-  const i32x4_t b = ok && k1 < K ? *reinterpret_cast<const i32x4_t*>(row + k1) : z;
-  return join_pieces(a, b);
-}
-
-// Simplest form: a wave owns 16 outputs x 16 rows and reads its operands from
-// global memory block by block.
-template <typename OUT>
-__global__ __launch_bounds__(256) void bs_matmul_kernel(const uint8_t* __restrict__ xq, int64_t ldx,
-                                                        const float* __restrict__ xs, int M,
-                                                        const uint8_t* __restrict__ wq, const float* __restrict__ ws,
-                                                        int N, int K, OUT* __restrict__ y, int64_t ldy, int n_tiles) {
-  const int lane = threadIdx.x & 63, r = lane & 15, quad = lane >> 4;
-  const int nt = blockIdx.x % n_tiles, mt = blockIdx.x / n_tiles;
-  const int n0 = nt * 64 + (threadIdx.x >> 6) * 16, m = mt * 16 + r;
-  if (n0 >= N) return;
-  const int KB = bs_blocks(K);
-  const uint8_t* wrow = wq + (int64_t)(n0 + r) * K;
-  const uint8_t* xrow = xq + (int64_t)m * ldx;
-  const float* wsr = ws + (int64_t)(n0 / BS) * KB;
-  f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int kb = 0; kb < KB; kb++) {
-    const f32x4_t p = mfma_block(load_frag(wrow, n0 + r < N, kb, K, quad), load_frag(xrow, m < M, kb, K, quad));
-    const float sc = m < M ? xs[(int64_t)m * KB + kb] * wsr[kb] : 0.0f;
+// Few rows (M <= 16 TM): bound by the weights' bytes, each read once.  A block
+// owns 16 outputs and all rows, its 8 waves share the K blocks (wave w takes
+// blocks w, w + 8, ...) and add their sums in the order of the waves; operands
+// go straight to registers, U blocks requested at a time, so that a call of a
+// few MB is one round trip to memory.
+template <int TM, int U, typename OUT>
+__global__ __launch_bounds__(512) void bs_matmul_rows_kernel(BsMatmul a) {
+  __shared__ f32x4_t part[8][TM][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, quad = lane >> 4;
+  const int n0 = blockIdx.x * 16, KB = bs_blocks(a.K);
+  const __amdgpu_buffer_rsrc_t wbuf = buffer_of(a.wq + (int64_t)n0 * a.K, (int64_t)min(16, a.N - n0) * a.K);
+  const __amdgpu_buffer_rsrc_t xbuf = buffer_of(a.xq, (a.M - 1) * a.ldx + a.K);
+  const __amdgpu_buffer_rsrc_t sbuf = buffer_of(a.xs, (int64_t)a.M * KB * 4);
+  const float* wsr = a.ws + (int64_t)(n0 / BS) * KB;
+  const uint32_t woff = r * a.K + 16 * quad;
+  uint32_t xoff[TM], soff[TM];
 #pragma unroll
-    for (int i = 0; i < 4; i++) acc[i] = __builtin_fmaf(p[i], sc, acc[i]);
+  for (int j = 0; j < TM; j++) {
+    const int m = 16 * j + r;
+    xoff[j] = m < a.M ? (uint32_t)(m * a.ldx) + 16 * quad : BUFFER_OUT;
+    soff[j] = m * KB * 4;
   }
-  if (m >= M) return;
+  f32x4_t acc[TM] = {};
+  for (int k0 = wave; k0 < KB; k0 += 8 * U) {
+    i32x8_t w[U], x[U][TM];
+    float wsc[U], xsc[U][TM];
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const int n = n0 + 4 * quad + i;
-    if (n >= N) continue;
-    if constexpr (sizeof(OUT) == 2)
-      y[(int64_t)m * ldy + n] = bf16_bits(acc[i]);
-    else
-      y[(int64_t)m * ldy + n] = acc[i];
+    for (int u = 0; u < U; u++) {
+      const int kb = k0 + 8 * u, c = kb * BS + 16 * quad;
+      const uint32_t o0 = c < a.K ? kb * BS : BUFFER_OUT, o1 = c + 64 < a.K ? kb * BS + 64 : BUFFER_OUT;
+      w[u] = join_pieces(buffer_load16(wbuf, woff + o0), buffer_load16(wbuf, woff + o1));
+      wsc[u] = kb < KB ? wsr[kb] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < TM; j++) {
+        x[u][j] = join_pieces(buffer_load16(xbuf, out_or_sum(xoff[j], o0)), buffer_load16(xbuf, out_or_sum(xoff[j], o1)));
+        xsc[u][j] = buffer_load4(sbuf, kb < KB ? soff[j] + kb * 4 : BUFFER_OUT);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      F16Block wf;
+      wf.set(w[u]);
+#pragma unroll
+      for (int j = 0; j < TM; j++) {
+        F16Block xf;
+        xf.set(x[u][j]);
+        const f32x4_t p = mfma_block(wf, xf);
+        const float sc = xsc[u][j] * wsc[u];
+#pragma unroll
+        for (int q = 0; q < 4; q++) acc[j][q] = __builtin_fmaf(p[q], sc, acc[j][q]);
+      }
+    }
   }
+#pragma unroll
+  for (int j = 0; j < TM; j++) part[wave][j][lane] = acc[j];
+  __syncthreads();
+  const int j = threadIdx.x >> 6;  // wave j adds tile j
+  if (j >= TM) return;
+  f32x4_t y = part[0][j][lane];
+#pragma unroll
+  for (int v = 1; v < 8; v++) y += part[v][j][lane];
+  const int m = 16 * j + r, n = n0 + 4 * quad;
+  const bool vec = a.ldy % 4 == 0 && ((uintptr_t)a.y & (4 * sizeof(OUT) - 1)) == 0;
+  if (m < a.M) store4(static_cast<OUT*>(a.y) + m * a.ldy + n, y, a.N - n, vec);
 }
 
 // Tiled form: WN x WM waves, each TN x TM tiles of 16 outputs x 16 rows.  The
@@ -231,15 +254,18 @@ static hipError_t launch_tile(const BsMatmul& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <int TM, int U, typename OUT>
+static hipError_t launch_rows(const BsMatmul& a, hipStream_t s) {
+  auto* k = bs_matmul_rows_kernel<TM, U, OUT>;
+  QMOE_LAUNCH(k, dim3((a.N + 15) / 16), dim3(512), 0, s, a);
+  return hipGetLastError();
+}
+
 template <typename OUT>
 static hipError_t launch_matmul(const BsMatmul& a, hipStream_t s) {
-  if (a.M <= 32) {
-    const int n_tiles = (a.N + 63) / 64;
-    const dim3 grid((unsigned)((int64_t)n_tiles * ((a.M + 15) / 16)));
-    QMOE_LAUNCH(bs_matmul_kernel<OUT>, grid, dim3(256), 0, s, a.xq, a.ldx, a.xs, a.M, a.wq, a.ws, a.N, a.K, (OUT*)a.y,
-                a.ldy, n_tiles);
-    return hipGetLastError();
-  }
+  if (a.M <= 16) return launch_rows<1, 4, OUT>(a, s);
+  if (a.M <= 32) return launch_rows<2, 2, OUT>(a, s);
+  if (a.M <= 64) return launch_rows<4, 2, OUT>(a, s);
   if (sizeof(OUT) == 2 && a.K >= 1024 && (int64_t)a.M * a.N >= 256 * 256 * 128)
     return launch_tile<2, 4, 8, 4, false, OUT>(a, s);
   return launch_tile<2, 2, 4, 4, true, OUT>(a, s);
