@@ -151,7 +151,9 @@ def _ptr(t) -> int | None:
 
 def _stream(stream=None) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the raw handle: torch.cuda.current_stream() builds a Stream object,
+        # 2.6 us on the host of a call that takes 4
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -239,9 +241,18 @@ _SCORES = {"sigmoid": MOE_SCORE_SIGMOID, "softmax": MOE_SCORE_SOFTMAX}
 _GROUP_SCORES = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2_SUM}
 
 
+_F32, _BF16, _I32T, _U8, _E4M3 = torch.float32, torch.bfloat16, torch.int32, torch.uint8, torch.float8_e4m3fn
+
+
+def _is(t, dtype, shape) -> bool:
+    """What the C call takes for granted about a tensor's storage: its dtype,
+    its size, no gaps.  Codes (dtype uint8) may be float8_e4m3fn."""
+    d = t.dtype
+    return (d is dtype or (dtype is _U8 and d is _E4M3)) and t.shape == shape and t.is_contiguous()
+
+
 def _need(fn: str, **tensors) -> None:
-    """(tensor, dtype, shape) by name: what the C call takes for granted about
-    a tensor's storage (its dtype, its size, no gaps) is checked here."""
+    """Raises for the first (tensor, dtype, shape) that is not as _is() asks."""
     for name, (t, dtype, shape) in tensors.items():
         if t.dtype != dtype and not (dtype == torch.uint8 and t.dtype == torch.float8_e4m3fn):
             raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
@@ -255,10 +266,10 @@ def _rows_of(fn: str, name: str, t: torch.Tensor, dtypes) -> int:
     """Row stride (elements) of a 2-D tensor whose rows have no gaps."""
     if t.dtype not in dtypes:
         raise TypeError(f"{fn}: {name} must be one of {dtypes}, not {t.dtype}")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
         raise ValueError(f"{fn}: {name} must be 2-D with contiguous rows")
     # (a single row's stride is free; torch leaves any number there)
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 def scale_blocks(n: int) -> int:
@@ -295,7 +306,8 @@ def gate_topk(gate: MoeGate, z, idx, wt, stream=None) -> None:
     stride = _rows_of("gate_topk", "z", z, _XDT)
     if z.shape[1] != gate.n_experts:
         raise ValueError(f"gate_topk: z has {z.shape[1]} logits per row, the gate {gate.n_experts} experts")
-    _need("gate_topk", idx=(idx, torch.int32, (T, k)), wt=(wt, torch.float32, (T, k)))
+    if not (_is(idx, _I32T, (T, k)) and _is(wt, _F32, (T, k))):
+        _need("gate_topk", idx=(idx, torch.int32, (T, k)), wt=(wt, torch.float32, (T, k)))
     _check(lib().moe_gate_topk(ctypes.byref(gate), _ptr(z), x_dtype_of(z), stride, T, _ptr(idx), _ptr(wt),
                                _stream(stream)))
 
@@ -307,7 +319,8 @@ def blockscale_quantize(x, q, s, stream=None) -> None:
     ldx, ldq = _rows_of(fn, "x", x, _XDT), _rows_of(fn, "q", q, _F8)
     if q.shape != x.shape:
         raise ValueError(f"{fn}: q has shape {tuple(q.shape)}, needs {tuple(x.shape)}")
-    _need(fn, s=(s, torch.float32, (M, scale_blocks(K))))
+    if not _is(s, _F32, (M, (K + 127) // 128)):
+        _need(fn, s=(s, torch.float32, (M, scale_blocks(K))))
     _check(lib().moe_blockscale_quantize(_ptr(x), x_dtype_of(x), ldx, M, K, _ptr(q), ldq, _ptr(s), _stream(stream)))
 
 
@@ -322,12 +335,12 @@ def blockscale_matmul(xq, xs, wq, ws, y, workspace=None, stream=None) -> None:
     with scales xs [M][ceil(K / 128)] and ws [ceil(N / 128)][ceil(K / 128)]."""
     fn = "blockscale_matmul"
     (M, K), N = xq.shape, wq.shape[0]
-    KB = scale_blocks(K)
+    KB, NB = (K + 127) // 128, (N + 127) // 128
     ldx, ldy = _rows_of(fn, "xq", xq, _F8), _rows_of(fn, "y", y, _XDT)
     if y.shape != (M, N):
         raise ValueError(f"{fn}: y has shape {tuple(y.shape)}, needs {(M, N)}")
-    _need(fn, xs=(xs, torch.float32, (M, KB)), wq=(wq, torch.uint8, (N, K)),
-          ws=(ws, torch.float32, (scale_blocks(N), KB)))
+    if not (_is(xs, _F32, (M, KB)) and _is(wq, _U8, (N, K)) and _is(ws, _F32, (NB, KB))):
+        _need(fn, xs=(xs, torch.float32, (M, KB)), wq=(wq, torch.uint8, (N, K)), ws=(ws, torch.float32, (NB, KB)))
     n_ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().moe_blockscale_matmul(_ptr(xq), ldx, _ptr(xs), M, _ptr(wq), _ptr(ws), N, K, _ptr(y), x_dtype_of(y),
                                        ldy, _ptr(workspace), n_ws, _stream(stream)))
@@ -338,12 +351,16 @@ def blockscale_gateup(xq, xs, k, offsets, perm, w_gate, s_gate, w_up, s_up, hq, 
     requantised; offsets and perm as bucket() writes them."""
     fn = "blockscale_gateup"
     (T, d), (E, f, _) = xq.shape, w_gate.shape
-    DB, FB = scale_blocks(d), scale_blocks(f)
-    _need(fn, xq=(xq, torch.uint8, (T, d)), xs=(xs, torch.float32, (T, DB)), offsets=(offsets, torch.int32, (E + 1,)),
-          perm=(perm, torch.int32, (T * k,)), w_gate=(w_gate, torch.uint8, (E, f, d)),
-          s_gate=(s_gate, torch.float32, (E, FB, DB)), w_up=(w_up, torch.uint8, (E, f, d)),
-          s_up=(s_up, torch.float32, (E, FB, DB)), hq=(hq, torch.uint8, (T * k, f)),
-          hs=(hs, torch.float32, (T * k, FB)))
+    R, DB, FB = T * k, scale_blocks(d), scale_blocks(f)
+    if not (_is(xq, _U8, (T, d)) and _is(xs, _F32, (T, DB)) and _is(offsets, _I32T, (E + 1,))
+            and _is(perm, _I32T, (R,)) and _is(w_gate, _U8, (E, f, d)) and _is(s_gate, _F32, (E, FB, DB))
+            and _is(w_up, _U8, (E, f, d)) and _is(s_up, _F32, (E, FB, DB)) and _is(hq, _U8, (R, f))
+            and _is(hs, _F32, (R, FB))):
+        _need(fn, xq=(xq, torch.uint8, (T, d)), xs=(xs, torch.float32, (T, DB)),
+              offsets=(offsets, torch.int32, (E + 1,)), perm=(perm, torch.int32, (R,)),
+              w_gate=(w_gate, torch.uint8, (E, f, d)), s_gate=(s_gate, torch.float32, (E, FB, DB)),
+              w_up=(w_up, torch.uint8, (E, f, d)), s_up=(s_up, torch.float32, (E, FB, DB)),
+              hq=(hq, torch.uint8, (R, f)), hs=(hs, torch.float32, (R, FB)))
     _check(lib().moe_blockscale_gateup(_ptr(xq), _ptr(xs), T, k, _ptr(offsets), _ptr(perm), E, _ptr(w_gate),
                                        _ptr(s_gate), _ptr(w_up), _ptr(s_up), f, d, _ptr(hq), _ptr(hs),
                                        _stream(stream)))
@@ -359,12 +376,15 @@ def blockscale_down(hq, hs, wt, offsets, pos, w_down, s_down, y, workspace, add=
     """y [T][d] = add + the weighted sum of each token's experts' down products."""
     fn = "blockscale_down"
     (T, k), (E, d, f) = wt.shape, w_down.shape
-    FB = scale_blocks(f)
-    _need(fn, hq=(hq, torch.uint8, (T * k, f)), hs=(hs, torch.float32, (T * k, FB)), wt=(wt, torch.float32, (T, k)),
-          offsets=(offsets, torch.int32, (E + 1,)), pos=(pos, torch.int32, (T * k,)),
-          w_down=(w_down, torch.uint8, (E, d, f)), s_down=(s_down, torch.float32, (E, scale_blocks(d), FB)),
-          y=(y, torch.float32, (T, d)))
-    if add is not None:
+    R, DB, FB = T * k, scale_blocks(d), scale_blocks(f)
+    if not (_is(hq, _U8, (R, f)) and _is(hs, _F32, (R, FB)) and _is(wt, _F32, (T, k))
+            and _is(offsets, _I32T, (E + 1,)) and _is(pos, _I32T, (R,)) and _is(w_down, _U8, (E, d, f))
+            and _is(s_down, _F32, (E, DB, FB)) and _is(y, _F32, (T, d))):
+        _need(fn, hq=(hq, torch.uint8, (R, f)), hs=(hs, torch.float32, (R, FB)), wt=(wt, torch.float32, (T, k)),
+              offsets=(offsets, torch.int32, (E + 1,)), pos=(pos, torch.int32, (R,)),
+              w_down=(w_down, torch.uint8, (E, d, f)), s_down=(s_down, torch.float32, (E, DB, FB)),
+              y=(y, torch.float32, (T, d)))
+    if add is not None and not _is(add, _F32, (T, d)):
         _need(fn, add=(add, torch.float32, (T, d)))
     n_ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().moe_blockscale_down(_ptr(hq), _ptr(hs), T, k, _ptr(wt), _ptr(offsets), _ptr(pos), E, _ptr(w_down),
