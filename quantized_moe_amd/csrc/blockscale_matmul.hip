@@ -72,26 +72,28 @@ __global__ __launch_bounds__(512) void bs_matmul_rows_kernel(BsMatmul a) {
 
 // Tiled form: WN x WM waves, each TN x TM tiles of 16 outputs x 16 rows.  The
 // operands of a block of 128 inputs go to LDS by asynchronous copies while the
-// block before is multiplied; 16-byte piece p of row i lies at place p ^ (i %
+// STAGES - 1 blocks before it are multiplied; 16-byte piece p of row i lies at place p ^ (i %
 // 8), so the 8 rows that a read touches at once are in different banks.
 // EXACT: fp16 steps (fp32 outputs); else the unit's E4M3 steps, twice as fast.
-template <int WN, int WM, int TN, int TM, bool EXACT>
+template <int WN, int WM, int TN, int TM, int ST, bool EXACT>
 struct Tile {
+  static constexpr int STAGES = ST;
   static constexpr int BN = WN * TN * 16, BM = WM * TM * 16, THREADS = 64 * WN * WM;
   static constexpr int W_BYTES = BN * BS, X_BYTES = BM * BS, S_BYTES = BM * 4;
   static constexpr int STAGE = W_BYTES + X_BYTES + S_BYTES;
   static constexpr int NB = (BN + BS - 1) / BS;                 // weight scale rows of a tile
-  static constexpr int SCALES = 2 * STAGE;                      // ... kept whole behind the stages
+  static constexpr int SCALES = STAGES * STAGE;                      // ... kept whole behind the stages
   static constexpr int LDS = SCALES + NB * (BS_MAX_K / BS) * 4;
   static constexpr int W_COPIES = BN / 8 / (WN * WM), X_COPIES = BM / 8 / (WN * WM);  // per wave and block
   static constexpr int COPIES = W_COPIES + X_COPIES, PER_ROW = (COPIES + TN / 2 - 1) / (TN / 2);
   static_assert(TN * 16 <= BS && BS % (TN * 16) == 0, "one weight scale per wave and block");
-  static_assert(BM % 64 == 0 && BM / 64 <= WN * WM, "scale copies");
+  static_assert(BM % 64 == 0 && (WN * WM) % (BM / 64) == 0, "scale copies");
+  static_assert(W_COPIES * 8 * WN * WM == BN && X_COPIES * 8 * WN * WM == BM, "whole copies");
 };
 
-template <int WN, int WM, int TN, int TM, bool EXACT, typename OUT>
+template <int WN, int WM, int TN, int TM, int ST, bool EXACT, typename OUT>
 __global__ __launch_bounds__(64 * WN * WM, 2) void bs_matmul_tile_kernel(BsMatmul a, int n_tiles, int m_tiles) {
-  using C = Tile<WN, WM, TN, TM, EXACT>;
+  using C = Tile<WN, WM, TN, TM, ST, EXACT>;
   extern __shared__ __align__(1024) uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, quad = lane >> 4;
@@ -120,7 +122,10 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void bs_matmul_tile_kernel(BsMatmu
     const int row = 8 * (wave + i * WAVES) + (lane >> 3);
     xoff[i] = row < rows_m ? (uint32_t)(row * a.ldx) + col : BUFFER_OUT;
   }
-  const uint32_t soff = (uint32_t)(wave * 64 + lane) * KB * 4;
+  // the rows' scales: every wave copies 64 of them (some the same ones), so
+  // that each has the same number of copies in flight
+  const int srow = wave % (C::BM / 64) * 64;
+  const uint32_t soff = (uint32_t)(srow + lane) * KB * 4;
   const uint32_t base = lds_address(lds);
   // Copy i of block kb, i < COPIES (the scales go with copy 0).
   auto fetch = [&](int kb, int stage, int i) {
@@ -129,7 +134,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void bs_matmul_tile_kernel(BsMatmu
       lds_copy16(wbuf, at + (wave + i * WAVES) * 1024, woff[i], kb * BS);
     else
       lds_copy16(xbuf, at + C::W_BYTES + (wave + (i - C::W_COPIES) * WAVES) * 1024, xoff[i - C::W_COPIES], kb * BS);
-    if (i == 0 && wave < C::BM / 64) lds_copy4(sbuf, at + C::W_BYTES + C::X_BYTES + wave * 256, soff, kb * 4);
+    if (i == 0) lds_copy4(sbuf, at + C::W_BYTES + C::X_BYTES + srow * 4, soff, kb * 4);
   };
   // In a short last block the pieces past K are zeros, not the next row's.
   auto cut_last = [&](int kb) {
@@ -156,21 +161,25 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void bs_matmul_tile_kernel(BsMatmu
     return join_pieces(*reinterpret_cast<const i32x4_t*>(p + swz0), *reinterpret_cast<const i32x4_t*>(p + swz1));
   };
   f32x4_t acc[TN][TM] = {};
-  cut_last(0);
+  // (blocks past the last: the last again, into a stage that nothing reads)
 #pragma unroll
-  for (int i = 0; i < C::COPIES; i++) fetch(0, 0, i);
-  lds_landed<0>();
+  for (int b = 0; b < C::STAGES - 1; b++) {
+    cut_last(min(b, KB - 1));
+#pragma unroll
+    for (int i = 0; i < C::COPIES; i++) fetch(min(b, KB - 1), b, i);
+  }
+  int stage = 0;
   for (int kb = 0; kb < KB; kb++) {
-    const int stage = kb & 1;
+    lds_landed<(C::STAGES - 2) * (C::COPIES + 1)>();
+    const int fill = stage == 0 ? C::STAGES - 1 : stage - 1;
     const uint8_t* st = lds + stage * C::STAGE;
-    // The next block's copies are spread over the tile rows of this one: all
-    // at once they fill the address queue and hold up the waves.  (After the
-    // last block it is fetched again, into the stage that nothing reads.)
-    const int next = min(kb + 1, KB - 1);
+    // The copies into the free stage are spread over the tile rows of this
+    // block: all at once they fill the address queue and hold up the waves.
+    const int next = min(kb + C::STAGES - 1, KB - 1);
     cut_last(next);
     auto fetch_some = [&](int i) {
 #pragma unroll
-      for (int c = i * C::PER_ROW; c < (i + 1) * C::PER_ROW && c < C::COPIES; c++) fetch(next, 1 - stage, c);
+      for (int c = i * C::PER_ROW; c < (i + 1) * C::PER_ROW && c < C::COPIES; c++) fetch(next, fill, c);
     };
     const uint8_t* wt = st + wn * TN * 16 * BS;
     const uint8_t* xt = st + C::W_BYTES + wm * TM * 16 * BS;
@@ -221,8 +230,9 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void bs_matmul_tile_kernel(BsMatmu
         w = w_next;
       }
     }
-    lds_landed<0>();
+    stage = stage + 1 == C::STAGES ? 0 : stage + 1;
   }
+  lds_landed<0>();  // no copy outlives the block
 
   OUT* y = static_cast<OUT*>(a.y);
   // four outputs leave as one store where every row allows it
@@ -242,11 +252,11 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void bs_matmul_tile_kernel(BsMatmu
 
 size_t bs_matmul_ws(int, int, int) { return 0; }
 
-template <int WN, int WM, int TN, int TM, bool EXACT, typename OUT>
+template <int WN, int WM, int TN, int TM, int ST, bool EXACT, typename OUT>
 static hipError_t launch_tile(const BsMatmul& a, hipStream_t s) {
-  using C = Tile<WN, WM, TN, TM, EXACT>;
+  using C = Tile<WN, WM, TN, TM, ST, EXACT>;
   const int n_tiles = (a.N + C::BN - 1) / C::BN, m_tiles = (a.M + C::BM - 1) / C::BM;
-  auto* k = bs_matmul_tile_kernel<WN, WM, TN, TM, EXACT, OUT>;
+  auto* k = bs_matmul_tile_kernel<WN, WM, TN, TM, ST, EXACT, OUT>;
   int per_cu, cus;
   hipError_t e = launch_shape((const void*)k, C::THREADS, C::LDS, C::LDS, &per_cu, &cus);
   if (e != hipSuccess) return e;
@@ -267,8 +277,10 @@ static hipError_t launch_matmul(const BsMatmul& a, hipStream_t s) {
   if (a.M <= 32) return launch_rows<2, 2, OUT>(a, s);
   if (a.M <= 64) return launch_rows<4, 2, OUT>(a, s);
   if (sizeof(OUT) == 2 && a.K >= 1024 && (int64_t)a.M * a.N >= 256 * 256 * 128)
-    return launch_tile<2, 4, 8, 4, false, OUT>(a, s);
-  return launch_tile<2, 2, 4, 4, true, OUT>(a, s);
+    return launch_tile<2, 4, 8, 4, 2, false, OUT>(a, s);
+  const int64_t tiles128 = (int64_t)((a.M + 127) / 128) * ((a.N + 127) / 128);
+  if (tiles128 >= 512) return launch_tile<2, 2, 4, 4, 2, true, OUT>(a, s);
+  return launch_tile<2, 2, 2, 2, 4, true, OUT>(a, s);
 }
 
 hipError_t launch_bs_matmul(const BsMatmul& a, hipStream_t s) {
