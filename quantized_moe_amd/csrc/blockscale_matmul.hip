@@ -74,28 +74,35 @@ __global__ __launch_bounds__(512) void bs_matmul_rows_kernel(BsMatmul a) {
 // operands of a block of 128 inputs go to LDS by asynchronous copies while the
 // STAGES - 1 blocks before it are multiplied; 16-byte piece p of row i lies at place p ^ (i %
 // 8), so the 8 rows that a read touches at once are in different banks.
+// KS groups of such waves share the K blocks (group g takes blocks g, g + KS,
+// ...), each with stages of its own, and add their sums in the order of the
+// groups: where tiles are few, a CU has more waves and half the steps.
 // EXACT: fp16 steps (fp32 outputs); else the unit's E4M3 steps, twice as fast.
-template <int WN, int WM, int TN, int TM, int ST, bool EXACT>
+template <int WN, int WM, int TN, int TM, int ST, int KS, bool EXACT>
 struct Tile {
   static constexpr int STAGES = ST;
-  static constexpr int BN = WN * TN * 16, BM = WM * TM * 16, THREADS = 64 * WN * WM;
+  static constexpr int BN = WN * TN * 16, BM = WM * TM * 16, WAVES = WN * WM, THREADS = 64 * WAVES * KS;
   static constexpr int W_BYTES = BN * BS, X_BYTES = BM * BS, S_BYTES = BM * 4;
   static constexpr int STAGE = W_BYTES + X_BYTES + S_BYTES;
   static constexpr int NB = (BN + BS - 1) / BS;                 // weight scale rows of a tile
-  static constexpr int SCALES = STAGES * STAGE;                      // ... kept whole behind the stages
+  static constexpr int SCALES = KS * STAGES * STAGE;                      // ... kept whole behind the stages
   static constexpr int LDS = SCALES + NB * (BS_MAX_K / BS) * 4;
   static constexpr int W_COPIES = BN / 8 / (WN * WM), X_COPIES = BM / 8 / (WN * WM);  // per wave and block
-  static constexpr int COPIES = W_COPIES + X_COPIES, PER_ROW = (COPIES + TN / 2 - 1) / (TN / 2);
+  static constexpr int COPIES = W_COPIES + X_COPIES, ROWS = TN > 1 ? TN / 2 : 1;  // tile rows that copies go with
+  static constexpr int PER_ROW = (COPIES + ROWS - 1) / ROWS;
   static_assert(TN * 16 <= BS && BS % (TN * 16) == 0, "one weight scale per wave and block");
+  static_assert((KS - 1) * WAVES * 64 * TN * TM * 16 <= SCALES, "the groups' sums fit the stages");
   static_assert(BM % 64 == 0 && (WN * WM) % (BM / 64) == 0, "scale copies");
   static_assert(W_COPIES * 8 * WN * WM == BN && X_COPIES * 8 * WN * WM == BM, "whole copies");
 };
 
-template <int WN, int WM, int TN, int TM, int ST, bool EXACT, typename OUT>
-__global__ __launch_bounds__(64 * WN * WM, 2) void bs_matmul_tile_kernel(BsMatmul a, int n_tiles, int m_tiles) {
-  using C = Tile<WN, WM, TN, TM, ST, EXACT>;
+template <int WN, int WM, int TN, int TM, int ST, int KS, bool EXACT, typename OUT>
+__global__ __launch_bounds__(64 * WN * WM * KS, 2) void bs_matmul_tile_kernel(BsMatmul a, int n_tiles, int m_tiles) {
+  using C = Tile<WN, WM, TN, TM, ST, KS, EXACT>;
   extern __shared__ __align__(1024) uint8_t lds[];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  constexpr int WAVES = C::WAVES;
+  const int lane = threadIdx.x & 63, block_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = block_wave / WAVES, wave = block_wave % WAVES;
   const int r = lane & 15, quad = lane >> 4;
   // an XCD (block id mod 8) takes a contiguous eighth of the tiles, in strips
   // of 4 M tiles so that neighbours in time share operands in its L2
@@ -113,7 +120,6 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void bs_matmul_tile_kernel(BsMatmu
   const __amdgpu_buffer_rsrc_t sbuf = buffer_of(a.xs + (int64_t)m0 * KB, (int64_t)rows_m * KB * 4);
   // copy i of a wave brings rows 8 (wave + i waves) .. + 7; lane l row l / 8
   const int col = ((lane & 7) ^ (lane >> 3)) * 16;
-  constexpr int WAVES = WN * WM;
   uint32_t woff[C::W_COPIES], xoff[C::X_COPIES];
 #pragma unroll
   for (int i = 0; i < C::W_COPIES; i++) woff[i] = (uint32_t)(8 * (wave + i * WAVES) + (lane >> 3)) * a.K + col;
@@ -122,11 +128,12 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void bs_matmul_tile_kernel(BsMatmu
     const int row = 8 * (wave + i * WAVES) + (lane >> 3);
     xoff[i] = row < rows_m ? (uint32_t)(row * a.ldx) + col : BUFFER_OUT;
   }
-  // the rows' scales: every wave copies 64 of them (some the same ones), so
-  // that each has the same number of copies in flight
+  // the rows' scales, 64 a copy; with more than two stages every wave makes one
+  // (some the same ones), as all need the same number of copies in flight
   const int srow = wave % (C::BM / 64) * 64;
   const uint32_t soff = (uint32_t)(srow + lane) * KB * 4;
-  const uint32_t base = lds_address(lds);
+  const uint8_t* stages = lds + group * C::STAGES * C::STAGE;
+  const uint32_t base = lds_address(stages);
   // Copy i of block kb, i < COPIES (the scales go with copy 0).
   auto fetch = [&](int kb, int stage, int i) {
     const uint32_t at = base + stage * C::STAGE;
@@ -134,7 +141,8 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void bs_matmul_tile_kernel(BsMatmu
       lds_copy16(wbuf, at + (wave + i * WAVES) * 1024, woff[i], kb * BS);
     else
       lds_copy16(xbuf, at + C::W_BYTES + (wave + (i - C::W_COPIES) * WAVES) * 1024, xoff[i - C::W_COPIES], kb * BS);
-    if (i == 0) lds_copy4(sbuf, at + C::W_BYTES + C::X_BYTES + srow * 4, soff, kb * 4);
+    if (i == 0 && (C::STAGES > 2 || wave < C::BM / 64))
+      lds_copy4(sbuf, at + C::W_BYTES + C::X_BYTES + srow * 4, soff, kb * 4);
   };
   // In a short last block the pieces past K are zeros, not the next row's.
   auto cut_last = [&](int kb) {
@@ -164,18 +172,21 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void bs_matmul_tile_kernel(BsMatmu
   // (blocks past the last: the last again, into a stage that nothing reads)
 #pragma unroll
   for (int b = 0; b < C::STAGES - 1; b++) {
-    cut_last(min(b, KB - 1));
+    const int kb = min(group + b * KS, KB - 1);
+    cut_last(kb);
 #pragma unroll
-    for (int i = 0; i < C::COPIES; i++) fetch(min(b, KB - 1), b, i);
+    for (int i = 0; i < C::COPIES; i++) fetch(kb, b, i);
   }
   int stage = 0;
-  for (int kb = 0; kb < KB; kb++) {
+  for (int k0 = 0; k0 < KB; k0 += KS) {
+    const int kb = k0 + group;
     lds_landed<(C::STAGES - 2) * (C::COPIES + 1)>();
     const int fill = stage == 0 ? C::STAGES - 1 : stage - 1;
-    const uint8_t* st = lds + stage * C::STAGE;
+    if (KS > 1 && kb >= KB) break;  // (the last round has no block for this group)
+    const uint8_t* st = stages + stage * C::STAGE;
     // The copies into the free stage are spread over the tile rows of this
     // block: all at once they fill the address queue and hold up the waves.
-    const int next = min(kb + C::STAGES - 1, KB - 1);
+    const int next = min(kb + (C::STAGES - 1) * KS, KB - 1);
     cut_last(next);
     auto fetch_some = [&](int i) {
 #pragma unroll
@@ -189,20 +200,33 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void bs_matmul_tile_kernel(BsMatmu
 #pragma unroll
     for (int j = 0; j < TM; j++) sc[j] = xsc[j * 16 + r] * wsc;
     if constexpr (EXACT) {
-      F16Block x[TM];
+      F16Block x[TM], w;
+      i32x8_t raw = frag(wt, r);
 #pragma unroll
       for (int j = 0; j < TM; j++) x[j].set(frag(xt, j * 16 + r));
+      w.set(raw);
+      // As below, and a quarter of the next row's conversion beside each tile.
+      f32x4_t p[2][TM];
 #pragma unroll
-      for (int i = 0; i < TN; i++) {
+      for (int i = 0; i <= TN; i++) {
         fetch_some(i);
-        F16Block w;
-        w.set(frag(wt, i * 16 + r));
+        F16Block w_next;
+        if (i + 1 < TN) raw = frag(wt, (i + 1) * 16 + r);
 #pragma unroll
         for (int j = 0; j < TM; j++) {
-          const f32x4_t p = mfma_block(w, x[j]);
+          if (i < TN) p[i & 1][j] = mfma_block(w, x[j]);
+          if (i + 1 < TN && j > 0) {
 #pragma unroll
-          for (int q = 0; q < 4; q++) acc[i][j][q] = __builtin_fmaf(p[q], sc[j], acc[i][j][q]);
+            for (int s = 4 * (j - 1) / (TM - 1); s < 4 * j / (TM - 1); s++) w_next.s[s] = e4m3_to_f16(raw[2 * s], raw[2 * s + 1]);
+          }
+          if (i > 0) {
+#pragma unroll
+            for (int q = 0; q < 4; q++)
+              acc[i - 1][j][q] = __builtin_fmaf(p[(i - 1) & 1][j][q], sc[j], acc[i - 1][j][q]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
+        w = w_next;
       }
     } else {
       i32x8_t x[TM];
@@ -233,6 +257,20 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void bs_matmul_tile_kernel(BsMatmu
     stage = stage + 1 == C::STAGES ? 0 : stage + 1;
   }
   lds_landed<0>();  // no copy outlives the block
+  if constexpr (KS > 1) {
+    f32x4_t* sums = reinterpret_cast<f32x4_t*>(lds);  // [group - 1][tile][thread of a group]
+    const int gt = wave * 64 + lane;
+    if (group > 0) {
+#pragma unroll
+      for (int i = 0; i < TN * TM; i++) sums[((group - 1) * TN * TM + i) * WAVES * 64 + gt] = acc[i / TM][i % TM];
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 1; g < KS; g++)
+#pragma unroll
+      for (int i = 0; i < TN * TM; i++) acc[i / TM][i % TM] += sums[((g - 1) * TN * TM + i) * WAVES * 64 + gt];
+  }
 
   OUT* y = static_cast<OUT*>(a.y);
   // four outputs leave as one store where every row allows it
@@ -252,11 +290,11 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void bs_matmul_tile_kernel(BsMatmu
 
 size_t bs_matmul_ws(int, int, int) { return 0; }
 
-template <int WN, int WM, int TN, int TM, int ST, bool EXACT, typename OUT>
+template <int WN, int WM, int TN, int TM, int ST, int KS, bool EXACT, typename OUT>
 static hipError_t launch_tile(const BsMatmul& a, hipStream_t s) {
-  using C = Tile<WN, WM, TN, TM, ST, EXACT>;
+  using C = Tile<WN, WM, TN, TM, ST, KS, EXACT>;
   const int n_tiles = (a.N + C::BN - 1) / C::BN, m_tiles = (a.M + C::BM - 1) / C::BM;
-  auto* k = bs_matmul_tile_kernel<WN, WM, TN, TM, ST, EXACT, OUT>;
+  auto* k = bs_matmul_tile_kernel<WN, WM, TN, TM, ST, KS, EXACT, OUT>;
   int per_cu, cus;
   hipError_t e = launch_shape((const void*)k, C::THREADS, C::LDS, C::LDS, &per_cu, &cus);
   if (e != hipSuccess) return e;
@@ -271,16 +309,39 @@ static hipError_t launch_rows(const BsMatmul& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// The variant: by rows, then the largest tile of which there are enough for
+// the 256 CUs.  Measured on both sides of each step, N = K = 4096 unless
+// given (us, fp16 steps / E4M3 steps):
+//   M 32: rows 9.8, 64 x 64 tiles 14.9 / 12.1;   64: rows 15.3, tiles 14.9 / 12.1
+//   M 128 (64 tiles of 128 x 64): 20.2 / 17.2 on them, 15.2 / 12.0 on 64 x 64
+//   M 1000, N 1100, K 2064 (144): 14.4 / 12.3 on 128 x 64, 19.3 / 16.5 on 64 x 64
+//   M 512 (128 tiles of 128 x 128): 32.0 / 24.4 on them, 22.6 / 18.2 on 128 x 64
+//   M 1024 (256): 34.6 (two groups) / 26.0 (four stages) on 128 x 128, 38.4 /
+//     32.6 with one group and two stages, 42.6 / 29.1 on 128 x 64
+//   M 2048 (512; 128 of 256 x 256): 71.0 / 42.9 with one group and two stages,
+//     66.9 / 53.6 with two groups; 256 x 256 E4M3 61
+//   M 4096 (1024; 256 of 256 x 256): 123 / 82.8 on 128 x 128, 132 with two
+//     groups; 256 x 256 E4M3 71.4
+// The E4M3 steps round a sum by 1.4e-5 of it, bf16 by 2e-3: they serve bf16
+// outputs, and sums of eight blocks or more, where the errors average out.
 template <typename OUT>
 static hipError_t launch_matmul(const BsMatmul& a, hipStream_t s) {
   if (a.M <= 16) return launch_rows<1, 4, OUT>(a, s);
   if (a.M <= 32) return launch_rows<2, 2, OUT>(a, s);
-  if (a.M <= 64) return launch_rows<4, 2, OUT>(a, s);
-  if (sizeof(OUT) == 2 && a.K >= 1024 && (int64_t)a.M * a.N >= 256 * 256 * 128)
-    return launch_tile<2, 4, 8, 4, 2, false, OUT>(a, s);
-  const int64_t tiles128 = (int64_t)((a.M + 127) / 128) * ((a.N + 127) / 128);
-  if (tiles128 >= 512) return launch_tile<2, 2, 4, 4, 2, true, OUT>(a, s);
-  return launch_tile<2, 2, 2, 2, 4, true, OUT>(a, s);
+  auto tiles = [&](int bn, int bm) { return (int64_t)((a.N + bn - 1) / bn) * ((a.M + bm - 1) / bm); };
+  if constexpr (sizeof(OUT) == 2) {
+    if (a.K >= 8 * BS) {
+      if (tiles(256, 256) >= 192) return launch_tile<2, 4, 8, 4, 2, 1, false, OUT>(a, s);
+      if (tiles(128, 128) >= 384) return launch_tile<2, 2, 4, 4, 2, 1, false, OUT>(a, s);
+      if (tiles(128, 128) >= 192) return launch_tile<2, 2, 4, 4, 4, 1, false, OUT>(a, s);
+      if (tiles(128, 64) >= 128) return launch_tile<2, 2, 4, 2, 3, 1, false, OUT>(a, s);
+      return launch_tile<2, 2, 2, 2, 3, 2, false, OUT>(a, s);
+    }
+  }
+  if (tiles(128, 128) >= 768) return launch_tile<2, 2, 4, 4, 2, 1, true, OUT>(a, s);
+  if (tiles(128, 128) >= 192) return launch_tile<2, 2, 4, 4, 2, 2, true, OUT>(a, s);
+  if (tiles(128, 64) >= 128) return launch_tile<2, 2, 4, 2, 3, 2, true, OUT>(a, s);
+  return launch_tile<2, 2, 2, 2, 3, 2, true, OUT>(a, s);
 }
 
 hipError_t launch_bs_matmul(const BsMatmul& a, hipStream_t s) {

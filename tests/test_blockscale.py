@@ -156,7 +156,9 @@ def test_matmul(M, N, K, out):
 
 @gpu
 @pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("M,N,K", [(2090, 4100, 1040), (4097, 2050, 2064), (700, 640, 4112)])
+@pytest.mark.parametrize("M,N,K", [(2090, 4100, 1040), (4097, 2050, 2064), (700, 640, 4112), (4000, 4200, 1040),
+                                   (700, 5000, 144), (1030, 2300, 1168), (530, 4100, 1296), (33, 520, 1552), (1800, 1900, 16),
+                                   (3900, 3800, 272)])
 def test_matmul_many_tiles(M, N, K, out):
     """Several tiles of the largest kind in both directions, the last ones short."""
     rng = np.random.default_rng(M + N)
