@@ -1,94 +1,129 @@
 // The routed experts' products on block-scaled E4M3 weights: gate/up with
 // SwiGLU and requantisation, down with each token's weighted sum.
-#include "blockscale.hpp"
+#include "blockscale_tile.hpp"
 
 namespace qmoe {
 
-__device__ __forceinline__ i32x8_t load_frag(const uint8_t* row, bool ok, int kb, int K, int quad) {
-  const i32x4_t z = {0, 0, 0, 0};
-  const int k0 = kb * BS + 16 * quad, k1 = k0 + 64;
-  const i32x4_t a = ok && k0 < K ? *reinterpret_cast<const i32x4_t*>(row + k0) : z;
-  const i32x4_t b = ok && k1 < K ? *reinterpret_cast<const i32x4_t*>(row + k1) : z;
-  return join_pieces(a, b);
+// Work ids run over the M tiles first: the tiles of one expert meet at the same
+// outputs on one XCD, whose L2 then serves the weights to all but the first.
+struct ExpertTile {
+  int e, row0, rows, nt;
+};
+__device__ __forceinline__ bool expert_tile(const int32_t* offsets, int E, int bm, int tiles, ExpertTile* t) {
+  const int id = xcd_order(blockIdx.x, gridDim.x);
+  t->nt = id / tiles;
+  return find_tile(offsets, E, bm, id - t->nt * tiles, &t->e, &t->row0, &t->rows);
 }
 
-// Simplest form: a block owns 16 bucket rows of one expert and one group of
-// 128 hidden columns (8 waves of 16), so the group's maximum stays in it.
-__global__ __launch_bounds__(512) void bs_gateup_kernel(BsGateup a, int n_tiles) {
-  __shared__ uint32_t smax[8][16];
+// A block owns BM bucket rows of one expert and one group of 128 hidden
+// columns, gate and up, so that the group's maximum stays in it.
+template <class C>
+__global__ __launch_bounds__(C::THREADS, 2) void bs_gateup_kernel(BsGateup a, int tiles) {
+  static_assert(C::BN == BS && C::NMAT == 2, "one group of hidden columns");
+  extern __shared__ __align__(1024) uint8_t lds[];
+  ExpertTile t;
+  if (!expert_tile(a.offsets, a.E, C::BM, tiles, &t)) return;
+  const int KB = bs_blocks(a.d), FB = bs_blocks(a.f), n0 = t.nt * BS;
+  const int64_t woff = ((int64_t)t.e * a.f + n0) * a.d, soff = ((int64_t)t.e * FB + t.nt) * KB;
+  const int64_t wbytes = (int64_t)min(BS, a.f - n0) * a.d;
+  const __amdgpu_buffer_rsrc_t wbuf[2] = {buffer_of(a.w_gate + woff, wbytes), buffer_of(a.w_up + woff, wbytes)};
+  const float* const ws[2] = {a.s_gate + soff, a.s_up + soff};
+  const __amdgpu_buffer_rsrc_t xbuf = buffer_of(a.xq, (int64_t)a.T * a.d);
+  const __amdgpu_buffer_rsrc_t sbuf = buffer_of(a.xs, (int64_t)a.T * KB * 4);
+  auto token = [&](int i) { return a.perm[t.row0 + i] / a.k; };
+  f32x4_t acc[2][C::TN][C::TM];
+  tile_product<C>(
+      lds, wbuf, ws, 1, a.d, xbuf, sbuf, [&](int i) { return i < t.rows ? (uint32_t)token(i) * a.d : BUFFER_OUT; },
+      [&](int i) { return i < t.rows ? (uint32_t)token(i) * KB * 4 : BUFFER_OUT; }, acc);
+
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, quad = lane >> 4;
-  const int nt = blockIdx.x % n_tiles;
-  int e, row0, rows;
-  if (!find_tile(a.offsets, a.E, 16, blockIdx.x / n_tiles, &e, &row0, &rows)) return;
-  const int KB = bs_blocks(a.d), FB = bs_blocks(a.f);
-  const int n0 = nt * BS + wave * 16;
-  const bool rok = r < rows, nok = n0 + r < a.f;
-  const int64_t t = rok ? a.perm[row0 + r] / a.k : 0;
-  const uint8_t* xrow = a.xq + t * a.d;
-  const int64_t woff = ((int64_t)e * a.f + n0 + r) * a.d, soff = ((int64_t)e * FB + nt) * KB;
-  f32x4_t g = {0.0f, 0.0f, 0.0f, 0.0f}, u = g;
-  for (int kb = 0; kb < KB; kb++) {
-    const i32x8_t x = load_frag(xrow, rok, kb, a.d, quad);
-    const f32x4_t pg = mfma_block(load_frag(a.w_gate + woff, nok, kb, a.d, quad), x);
-    const f32x4_t pu = mfma_block(load_frag(a.w_up + woff, nok, kb, a.d, quad), x);
-    const float xsc = rok ? a.xs[t * KB + kb] : 0.0f;
-    const float sg = xsc * a.s_gate[soff + kb], su = xsc * a.s_up[soff + kb];
+  const int wn = wave % C::WN, wm = wave / C::WN;
+  uint32_t* smax = reinterpret_cast<uint32_t*>(lds);  // [WN][BM]
+  // (columns past f have zero weights: h = 0 there)
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      g[i] = __builtin_fmaf(pg[i], sg, g[i]);
-      u[i] = __builtin_fmaf(pu[i], su, u[i]);
-    }
-  }
-  float h[4];
-  uint32_t mx = 0;
+  for (int j = 0; j < C::TM; j++) {
+    uint32_t mx = 0;
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
-    h[i] = silu(g[i]) * u[i];
-    if (n0 + 4 * quad + i < a.f) mx = max(mx, abs_bits(h[i]));
+    for (int i = 0; i < C::TN; i++)
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        acc[0][i][j][q] = silu(acc[0][i][j][q]) * acc[1][i][j][q];
+        mx = max(mx, abs_bits(acc[0][i][j][q]));
+      }
+    mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16, 64));
+    mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32, 64));
+    if (quad == 0) smax[wn * C::BM + (wm * C::TM + j) * 16 + r] = mx;
   }
-  mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16, 64));
-  mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32, 64));
-  if (quad == 0) smax[wave][r] = mx;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < 8; w++) mx = max(mx, smax[w][r]);
-  if (!rok) return;
-  const float sc = bs_scale(mx);
-  const int64_t row = row0 + r;
-  if (n0 + 4 * quad < a.f)  // f is a multiple of 16
-    *reinterpret_cast<uint32_t*>(a.hq + row * a.f + n0 + 4 * quad) =
-        mx >= 0x7f800000u ? 0u : e4m3x4(h[0] / sc, h[1] / sc, h[2] / sc, h[3] / sc);
-  if (wave == 0 && quad == 0) a.hs[row * FB + nt] = sc;
+  for (int j = 0; j < C::TM; j++) {
+    const int i_row = (wm * C::TM + j) * 16 + r;
+    uint32_t mx = 0;
+#pragma unroll
+    for (int w = 0; w < C::WN; w++) mx = max(mx, smax[w * C::BM + i_row]);
+    if (i_row >= t.rows) continue;
+    const float sc = bs_scale(mx);
+    const int64_t row = t.row0 + i_row;
+#pragma unroll
+    for (int i = 0; i < C::TN; i++) {
+      const int n = n0 + (wn * C::TN + i) * 16 + 4 * quad;
+      const f32x4_t h = acc[0][i][j];
+      if (n < a.f)  // f is a multiple of 16
+        *reinterpret_cast<uint32_t*>(a.hq + row * a.f + n) =
+            mx >= 0x7f800000u ? 0u : e4m3x4(h[0] / sc, h[1] / sc, h[2] / sc, h[3] / sc);
+    }
+    if (wn == 0 && quad == 0) a.hs[row * FB + t.nt] = sc;
+  }
 }
 
-hipError_t launch_bs_gateup(const BsGateup& a, hipStream_t s) {
-  const int n_tiles = bs_blocks(a.f);
-  const int64_t tiles = max_tiles((int64_t)a.T * a.k, a.E, 16);
-  QMOE_LAUNCH(bs_gateup_kernel, dim3((unsigned)(tiles * n_tiles)), dim3(512), 0, s, a, n_tiles);
+template <class C>
+static hipError_t launch_gateup(const BsGateup& a, hipStream_t s) {
+  const int tiles = (int)max_tiles((int64_t)a.T * a.k, a.E, C::BM);
+  auto* k = bs_gateup_kernel<C>;
+  int per_cu, cus;
+  hipError_t e = launch_shape((const void*)k, C::THREADS, C::LDS, C::LDS, &per_cu, &cus);
+  if (e != hipSuccess) return e;
+  QMOE_LAUNCH(k, dim3((unsigned)((int64_t)tiles * bs_blocks(a.f))), dim3(C::THREADS), C::LDS, s, a, tiles);
   return hipGetLastError();
 }
 
+hipError_t launch_bs_gateup(const BsGateup& a, hipStream_t s) {
+  const int64_t n = (int64_t)a.T * a.k;
+  if (n <= 4 * (int64_t)a.E) return launch_gateup<Tile<8, 1, 1, 1, 4, 1, 2, true>>(a, s);
+  if (n <= 24 * (int64_t)a.E) return launch_gateup<Tile<8, 1, 1, 2, 4, 1, 2, true>>(a, s);
+  if (n <= 96 * (int64_t)a.E) return launch_gateup<Tile<8, 1, 1, 4, 3, 1, 2, true>>(a, s);
+  return launch_gateup<Tile<4, 2, 2, 4, 3, 1, 2, true>>(a, s);
+}
+
 // ye[r][n] = (D_e h_r)[n] for the bucket rows.
-__global__ __launch_bounds__(256) void bs_down_kernel(BsDown a, int n_tiles) {
-  const int lane = threadIdx.x & 63, r = lane & 15, quad = lane >> 4;
-  const int nt = blockIdx.x % n_tiles;
-  int e, row0, rows;
-  if (!find_tile(a.offsets, a.E, 16, blockIdx.x / n_tiles, &e, &row0, &rows)) return;
-  const int KB = bs_blocks(a.f), DB = bs_blocks(a.d);
-  const int n0 = nt * 64 + (threadIdx.x >> 6) * 16;
-  if (n0 >= a.d) return;
-  const bool rok = r < rows;
-  const int64_t row = row0 + (rok ? r : 0);
-  const int64_t woff = ((int64_t)e * a.d + n0 + r) * a.f, soff = ((int64_t)e * DB + n0 / BS) * KB;
-  f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int kb = 0; kb < KB; kb++) {
-    const f32x4_t p = mfma_block(load_frag(a.w_down + woff, n0 + r < a.d, kb, a.f, quad),
-                                 load_frag(a.hq + row * a.f, rok, kb, a.f, quad));
-    const float sc = a.hs[row * KB + kb] * a.s_down[soff + kb];
+template <class C>
+__global__ __launch_bounds__(C::THREADS, 2) void bs_down_kernel(BsDown a, int tiles) {
+  extern __shared__ __align__(1024) uint8_t lds[];
+  ExpertTile t;
+  if (!expert_tile(a.offsets, a.E, C::BM, tiles, &t)) return;
+  const int KB = bs_blocks(a.f), DB = bs_blocks(a.d), n0 = t.nt * C::BN;
+  const __amdgpu_buffer_rsrc_t wbuf[1] = {
+      buffer_of(a.w_down + ((int64_t)t.e * a.d + n0) * a.f, (int64_t)min(C::BN, a.d - n0) * a.f)};
+  const float* const ws[1] = {a.s_down + ((int64_t)t.e * DB + n0 / BS) * KB};
+  const __amdgpu_buffer_rsrc_t xbuf = buffer_of(a.hq + (int64_t)t.row0 * a.f, (int64_t)t.rows * a.f);
+  const __amdgpu_buffer_rsrc_t sbuf = buffer_of(a.hs + (int64_t)t.row0 * KB, (int64_t)t.rows * KB * 4);
+  f32x4_t acc[1][C::TN][C::TM];
+  tile_product<C>(
+      lds, wbuf, ws, DB - n0 / BS, a.f, xbuf, sbuf, [&](int i) { return i < t.rows ? (uint32_t)(i * a.f) : BUFFER_OUT; },
+      [&](int i) { return i < t.rows ? (uint32_t)(i * KB * 4) : BUFFER_OUT; }, acc);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, quad = lane >> 4;
+  const int wn = wave % C::WN, wm = wave / C::WN;
 #pragma unroll
-    for (int i = 0; i < 4; i++) acc[i] = __builtin_fmaf(p[i], sc, acc[i]);
+  for (int j = 0; j < C::TM; j++) {
+    const int i_row = (wm * C::TM + j) * 16 + r;
+    if (i_row >= t.rows) continue;
+    float* row = a.ye + (int64_t)(t.row0 + i_row) * a.d;
+#pragma unroll
+    for (int i = 0; i < C::TN; i++) {
+      const int n = n0 + (wn * C::TN + i) * 16 + 4 * quad;
+      store4(row + n, acc[0][i][j], a.d - n, true);  // d is a multiple of 16
+    }
   }
-  if (rok && n0 + 4 * quad < a.d) *reinterpret_cast<f32x4_t*>(a.ye + row * a.d + n0 + 4 * quad) = acc;
 }
 
 // y[t] = add[t] + sum_j wt[t][j] ye[pos[t k + j]], 4 outputs per thread.
@@ -113,13 +148,29 @@ __global__ __launch_bounds__(256) void bs_combine_kernel(BsDown a) {
 
 size_t bs_down_ws(int T, int k, int d) { return (size_t)T * k * d * 4; }
 
+template <class C>
+static hipError_t launch_down(const BsDown& a, hipStream_t s) {
+  const int tiles = (int)max_tiles((int64_t)a.T * a.k, a.E, C::BM);
+  auto* k = bs_down_kernel<C>;
+  int per_cu, cus;
+  hipError_t e = launch_shape((const void*)k, C::THREADS, C::LDS, C::LDS, &per_cu, &cus);
+  if (e != hipSuccess) return e;
+  QMOE_LAUNCH(k, dim3((unsigned)((int64_t)tiles * ((a.d + C::BN - 1) / C::BN))), dim3(C::THREADS), C::LDS, s, a, tiles);
+  return hipGetLastError();
+}
+
+static hipError_t launch_down_products(const BsDown& a, hipStream_t s) {
+  const int64_t n = (int64_t)a.T * a.k;
+  if (n <= 4 * (int64_t)a.E) return launch_down<Tile<8, 1, 1, 1, 4, 1, 1, true>>(a, s);
+  if (n <= 24 * (int64_t)a.E) return launch_down<Tile<8, 1, 2, 2, 4, 1, 1, true>>(a, s);
+  if (n <= 96 * (int64_t)a.E) return launch_down<Tile<8, 1, 2, 4, 3, 1, 1, true>>(a, s);
+  return launch_down<Tile<4, 2, 4, 4, 3, 1, 1, true>>(a, s);
+}
+
 hipError_t launch_bs_down(const BsDown& a, hipStream_t s) {
-  const int n_tiles = (a.d + 63) / 64;
-  const int64_t tiles = max_tiles((int64_t)a.T * a.k, a.E, 16);
   int pid = prof_begin("bs_down", s);
-  QMOE_LAUNCH(bs_down_kernel, dim3((unsigned)(tiles * n_tiles)), dim3(256), 0, s, a, n_tiles);
+  hipError_t e = launch_down_products(a, s);
   prof_end(pid, s);
-  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   pid = prof_begin("bs_combine", s);
   QMOE_LAUNCH(bs_combine_kernel, dim3((unsigned)(((int64_t)a.T * (a.d / 4) + 255) / 256)), dim3(256), 0, s, a);
