@@ -164,36 +164,49 @@ __device__ __forceinline__ void store4(uint16_t* p, f32x4_t v, int left, bool ve
   }
 }
 
-// The M tile of `bm` bucket rows that is the `tile`-th over all experts:
-// expert e, first row and row count.  false: there are fewer tiles.  Every
-// lane of a wave calls it with the same tile.
-__device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, int E, int bm, int tile, int* e_out,
-                                          int* row0, int* rows) {
-  const int lane = threadIdx.x & 63;
-  int base = 0;
-  for (int e0 = 0; e0 < E; e0 += 64) {
-    const int e = e0 + lane;
-    const int a = offsets[min(e, E)], b = offsets[min(e + 1, E)];
-    const int n = (b - a + bm - 1) / bm;
-    int incl = n;
+// The M tile of BM bucket rows that is the `tile`-th over all experts: expert,
+// first row and row count.  false: there are fewer tiles.  Every lane of a wave
+// calls it with the same tile; lane l counts the tiles of experts C l .. C l + C
+// - 1, all offsets requested at once.
+template <int BM>
+__device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, int E, int tile, int* e_out, int* row0,
+                                          int* rows) {
+  constexpr int MOST = MAX_EXPERTS / 64;
+  const int lane = threadIdx.x & 63, C = (E + 63) / 64, e0 = lane * C;
+  int off[MOST + 1];
+  off[0] = offsets[min(e0, E)];
 #pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-      const int o = __shfl_up(incl, s, 64);
-      if (lane >= s) incl += o;
-    }
-    const int total = __builtin_amdgcn_readlane(incl, 63);
-    if (tile < base + total) {
-      const uint64_t m = __ballot(tile < base + incl);
-      const int src = __builtin_ctzll(m);
-      const int first = __builtin_amdgcn_readlane(a, src) + (tile - base - __builtin_amdgcn_readlane(incl - n, src)) * bm;
-      *e_out = e0 + src;
-      *row0 = first;
-      *rows = min(bm, __builtin_amdgcn_readlane(b, src) - first);
-      return true;
-    }
-    base += total;
+  for (int i = 0; i < MOST; i++)
+    if (i < C) off[i + 1] = offsets[min(e0 + i + 1, E)];
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < MOST; i++)
+    if (i < C) n += (off[i + 1] - off[i] + BM - 1) / BM;
+  int incl = n;
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) {
+    const int o = __shfl_up(incl, s, 64);
+    if (lane >= s) incl += o;
   }
-  return false;
+  const uint64_t has = __ballot(tile < incl);
+  if (has == 0) return false;
+  int left = tile - (incl - n), e = e0, first = 0, count = 0;
+#pragma unroll
+  for (int i = 0; i < MOST; i++)
+    if (i < C) {
+      const int t = (off[i + 1] - off[i] + BM - 1) / BM;
+      if (left >= 0 && left < t) {
+        e = e0 + i;
+        first = off[i] + left * BM;
+        count = min(BM, off[i + 1] - first);
+      }
+      left -= t;
+    }
+  const int src = __builtin_ctzll(has);
+  *e_out = __builtin_amdgcn_readlane(e, src);
+  *row0 = __builtin_amdgcn_readlane(first, src);
+  *rows = __builtin_amdgcn_readlane(count, src);
+  return true;
 }
 
 // Upper bound on the number of M tiles of n rows in E buckets.

@@ -9,20 +9,21 @@ namespace qmoe {
 struct ExpertTile {
   int e, row0, rows, nt;
 };
-__device__ __forceinline__ bool expert_tile(const int32_t* offsets, int E, int bm, int tiles, ExpertTile* t) {
+template <int BM>
+__device__ __forceinline__ bool expert_tile(const int32_t* offsets, int E, int tiles, ExpertTile* t) {
   const int id = xcd_order(blockIdx.x, gridDim.x);
   t->nt = id / tiles;
-  return find_tile(offsets, E, bm, id - t->nt * tiles, &t->e, &t->row0, &t->rows);
+  return find_tile<BM>(offsets, E, id - t->nt * tiles, &t->e, &t->row0, &t->rows);
 }
 
 // A block owns BM bucket rows of one expert and one group of 128 hidden
 // columns, gate and up, so that the group's maximum stays in it.
 template <class C>
-__global__ __launch_bounds__(C::THREADS, 2) void bs_gateup_kernel(BsGateup a, int tiles) {
+__global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void bs_gateup_kernel(BsGateup a, int tiles) {
   static_assert(C::BN == BS && C::NMAT == 2, "one group of hidden columns");
   extern __shared__ __align__(1024) uint8_t lds[];
   ExpertTile t;
-  if (!expert_tile(a.offsets, a.E, C::BM, tiles, &t)) return;
+  if (!expert_tile<C::BM>(a.offsets, a.E, tiles, &t)) return;
   const int KB = bs_blocks(a.d), FB = bs_blocks(a.f), n0 = t.nt * BS;
   const int64_t woff = ((int64_t)t.e * a.f + n0) * a.d, soff = ((int64_t)t.e * FB + t.nt) * KB;
   const int64_t wbytes = (int64_t)min(BS, a.f - n0) * a.d;
@@ -87,20 +88,30 @@ static hipError_t launch_gateup(const BsGateup& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// The M tile, by the rows that an expert has on average (few enough tiles that
+// most experts are one, and where they are not, enough matrix work a weight
+// byte).  Measured, 384 experts x 4096 x 2048 unless given, us per call with
+// tiles of 16 / 32 / 48 / 128 rows:
+//   0.1 rows (8 tokens)      143 / 145 / 154 / 183   (1 token: 26 / 29 / 34 / 54)
+//   1 row (64 tokens)        687 / 681 / 681 / 912
+//   16 rows, uniform         1287 / 1111 .. 1365 / 1373 / 1548
+//   48 rows (128, crowded)   784 / 565 / 544 / 631
+//   96 rows (64, crowded)    645 / 405 / 358 / 388
+//   384 rows (16, 2048 x 512, crowded)  91 / 49 / 47 / 37
 hipError_t launch_bs_gateup(const BsGateup& a, hipStream_t s) {
-  const int64_t n = (int64_t)a.T * a.k;
-  if (n <= 4 * (int64_t)a.E) return launch_gateup<Tile<8, 1, 1, 1, 4, 1, 2, true>>(a, s);
-  if (n <= 24 * (int64_t)a.E) return launch_gateup<Tile<8, 1, 1, 2, 4, 1, 2, true>>(a, s);
-  if (n <= 96 * (int64_t)a.E) return launch_gateup<Tile<8, 1, 1, 4, 3, 1, 2, true>>(a, s);
+  const int64_t n = (int64_t)a.T * a.k, E = a.E;
+  if (n <= 4 * E) return launch_gateup<Tile<8, 1, 1, 1, 4, 1, 2, true>>(a, s);
+  if (n <= 32 * E) return launch_gateup<Tile<8, 1, 1, 2, 2, 1, 2, true>>(a, s);
+  if (n <= 160 * E) return launch_gateup<Tile<8, 1, 1, 3, 2, 1, 2, true>>(a, s);
   return launch_gateup<Tile<4, 2, 2, 4, 3, 1, 2, true>>(a, s);
 }
 
 // ye[r][n] = (D_e h_r)[n] for the bucket rows.
 template <class C>
-__global__ __launch_bounds__(C::THREADS, 2) void bs_down_kernel(BsDown a, int tiles) {
+__global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void bs_down_kernel(BsDown a, int tiles) {
   extern __shared__ __align__(1024) uint8_t lds[];
   ExpertTile t;
-  if (!expert_tile(a.offsets, a.E, C::BM, tiles, &t)) return;
+  if (!expert_tile<C::BM>(a.offsets, a.E, tiles, &t)) return;
   const int KB = bs_blocks(a.f), DB = bs_blocks(a.d), n0 = t.nt * C::BN;
   const __amdgpu_buffer_rsrc_t wbuf[1] = {
       buffer_of(a.w_down + ((int64_t)t.e * a.d + n0) * a.f, (int64_t)min(C::BN, a.d - n0) * a.f)};
@@ -159,11 +170,17 @@ static hipError_t launch_down(const BsDown& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// As for gate/up; tiles of 16 (128 outputs) / 32 / 48 / 128 rows (256 outputs):
+//   0.1 rows (8 tokens)   78 / 84 / 86 / 99
+//   4 rows                582 / 573 / 577 / 749
+//   16 rows               749 / 658 / 650 / 800
+//   64 rows, crowded      1726 / 1080 / 999 / 1139
+//   384 rows (64 experts) 1348 / 740 / 655 / 630
 static hipError_t launch_down_products(const BsDown& a, hipStream_t s) {
-  const int64_t n = (int64_t)a.T * a.k;
-  if (n <= 4 * (int64_t)a.E) return launch_down<Tile<8, 1, 1, 1, 4, 1, 1, true>>(a, s);
-  if (n <= 24 * (int64_t)a.E) return launch_down<Tile<8, 1, 2, 2, 4, 1, 1, true>>(a, s);
-  if (n <= 96 * (int64_t)a.E) return launch_down<Tile<8, 1, 2, 4, 3, 1, 1, true>>(a, s);
+  const int64_t n = (int64_t)a.T * a.k, E = a.E;
+  if (n <= 2 * E) return launch_down<Tile<8, 1, 1, 1, 4, 1, 1, true>>(a, s);
+  if (n <= 12 * E) return launch_down<Tile<8, 1, 2, 2, 2, 1, 1, true>>(a, s);
+  if (n <= 200 * E) return launch_down<Tile<8, 1, 2, 3, 2, 1, 1, true>>(a, s);
   return launch_down<Tile<4, 2, 4, 4, 3, 1, 1, true>>(a, s);
 }
 

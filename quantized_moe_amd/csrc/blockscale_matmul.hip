@@ -71,7 +71,7 @@ __global__ __launch_bounds__(512) void bs_matmul_rows_kernel(BsMatmul a) {
 }
 
 template <class C, typename OUT>
-__global__ __launch_bounds__(C::THREADS, 2) void bs_matmul_tile_kernel(BsMatmul a, int n_tiles, int m_tiles) {
+__global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void bs_matmul_tile_kernel(BsMatmul a, int n_tiles, int m_tiles) {
   extern __shared__ __align__(1024) uint8_t lds[];
   // an XCD (block id mod 8) takes a contiguous eighth of the tiles, in strips
   // of 4 M tiles so that neighbours in time share operands in its L2

@@ -21,24 +21,25 @@ struct Tile {
   static constexpr bool EXACT = EXACT_;
   static constexpr int WAVES = WN * WM, THREADS = 64 * WAVES * KS;
   static constexpr int BN = WN * TN * 16, BM = WM * TM * 16;
-  static constexpr int S_ROWS = BM < 64 ? 64 : BM;  // a copy of scales brings 64
+  static constexpr int S_ROWS = (BM + 63) / 64 * 64;  // a copy of scales brings 64
   static constexpr int W_BYTES = NMAT * BN * BS, X_BYTES = BM * BS, S_BYTES = S_ROWS * 4;
   static constexpr int STAGE = W_BYTES + X_BYTES + S_BYTES;
   static constexpr int NB = (BN + BS - 1) / BS;         // weight scale rows of a matrix's tile ...
   static constexpr int SCALES = KS * STAGES * STAGE;    // ... kept whole behind the stages
   static constexpr int LDS = SCALES + NMAT * NB * (BS_MAX_K / BS) * 4;
-  // copies of 8 rows per wave and block; where the rows are fewer than 8 per
-  // wave, some waves bring the same ones
+  // copies of 8 rows per wave and block; where the rows are not 8 (or 16, ...)
+  // per wave, some waves bring the same ones
   static constexpr int W_COPIES = BN / 8 / WAVES, X_UNITS = BM / 8;
-  static constexpr int X_COPIES = X_UNITS < WAVES ? 1 : X_UNITS / WAVES;
+  static constexpr int X_COPIES = (X_UNITS + WAVES - 1) / WAVES;
   static constexpr int COPIES = NMAT * W_COPIES + X_COPIES;
   static constexpr int TILE_ROWS = NMAT * TN;                           // tiles of 16 outputs of a wave
   static constexpr int SPREAD = TILE_ROWS > 1 ? TILE_ROWS / 2 : 1;      // those that copies go with
   static constexpr int PER_ROW = (COPIES + SPREAD - 1) / SPREAD;
+  // registers: where two blocks of 8 small waves fit a CU's LDS, they fit its registers too
+  static constexpr int WAVES_PER_SIMD = 2 * LDS <= 160 * 1024 && THREADS == 512 && TILE_ROWS * TM <= 6 ? 4 : 2;
   static_assert((KS - 1) * WAVES * 64 * TILE_ROWS * TM * 16 <= SCALES, "the groups' sums fit the stages");
   static_assert(S_ROWS % 64 == 0 && WAVES % (S_ROWS / 64) == 0, "scale copies");
-  static_assert(W_COPIES * 8 * WAVES == BN && (X_UNITS < WAVES ? WAVES % X_UNITS == 0 : X_UNITS % WAVES == 0),
-                "whole copies");
+  static_assert(W_COPIES * 8 * WAVES == BN, "whole copies");
   static_assert(TN * 16 <= BS && BS % (TN * 16) == 0, "one weight scale per wave, matrix and block");
   static_assert(LDS <= 160 * 1024, "LDS of a CU");
 };
