@@ -166,8 +166,8 @@ __device__ __forceinline__ void store4(uint16_t* p, f32x4_t v, int left, bool ve
 
 // The M tile of BM bucket rows that is the `tile`-th over all experts: expert,
 // first row and row count.  false: there are fewer tiles.  Every lane of a wave
-// calls it with the same tile; lane l counts the tiles of experts C l .. C l + C
-// - 1, all offsets requested at once.
+// calls it alike; lane l counts the tiles of experts C l .. C l + C - 1, all
+// offsets requested at once.
 template <int BM>
 __device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, int E, int tile, int* e_out, int* row0,
                                           int* rows) {

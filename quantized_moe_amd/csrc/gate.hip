@@ -26,118 +26,217 @@ __device__ __forceinline__ float exp32(float t) {
   return p * __uint_as_float((uint32_t)((int)n + 127) << 23);
 }
 
-// Keys order as (value descending, index ascending); 0 is "out".  A value in
-// (> -inf) has order bits above those of -inf, so its key is never 0.
-__device__ __forceinline__ uint64_t rank_key(float v, int i) {
-  return v > -INFINITY ? ((uint64_t)logit_order_bits(v) << 32) | (uint32_t)~i : 0ull;
+// 1 / x correctly rounded for x in [1, 2^117]: the hardware's reciprocal is off
+// by one unit at most, and a Newton step with its residual from a fused
+// multiply-add leaves the nearest fp32 number (checked for every significand).
+// 5 instructions where the general IEEE division takes 10.
+__device__ __forceinline__ float recip_exact(float x) {
+  float r = __builtin_amdgcn_rcpf(x);
+  r = __builtin_fmaf(__builtin_fmaf(-x, r, 1.0f), r, r);
+  return __builtin_fmaf(__builtin_fmaf(-x, r, 1.0f), r, r);
 }
 
-// One wave per token, the experts' values in LDS.
-template <int SLOTS>
-__global__ __launch_bounds__(64) void gate_kernel(GateLaunch a) {
-  __shared__ float sv[64 * SLOTS];
-  const int lane = threadIdx.x, t = blockIdx.x;
-  const int E = a.E, EG = E / a.n_groups;
+// The same bits as sigmoid32 (topk.hpp).
+__device__ __forceinline__ float sigmoid_score(float z) {
+  return recip_exact(1.0f + exp32(-fminf(fmaxf(z, -80.0f), 80.0f)));
+}
+
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ float dpp_fmax_step(float v) {
+  const int ninf = (int)0xff800000u;
+  return fmaxf(v, __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(ninf, (int)__float_as_uint(v), CTRL, ROW_MASK,
+                                                                        0xf, false)));
+}
+// Maximum over the wave, the same in every lane.
+__device__ __forceinline__ float wave_fmax(float v) {
+  v = dpp_fmax_step<0x111, 0xf>(v);
+  v = dpp_fmax_step<0x112, 0xf>(v);
+  v = dpp_fmax_step<0x114, 0xf>(v);
+  v = dpp_fmax_step<0x118, 0xf>(v);
+  v = dpp_fmax_step<0x142, 0xa>(v);
+  v = dpp_fmax_step<0x143, 0xc>(v);
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+__device__ __forceinline__ float read_lane(float v, int lane) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
+
+// A wave per token, four tokens per block; everything stays in registers.
+//
+// P = 2^LG lanes hold a group (all 64 the one group when no groups are chosen):
+// lane g P + p has experts g EG + p + P i, i < SLOTS, EG = E / groups.  A
+// group's two best are then a butterfly over its lanes, its rank a count over
+// the groups' values, and an expert that is out is a -inf in its slot.  Each
+// round of the top-k takes the wave maximum of the lanes' maxima (6 DPP steps)
+// and finds who has it by comparing every slot with it: the comparisons' lane
+// masks are scalars, so the lowest index (group, slot, lane) is found by the
+// scalar unit beside other waves' vector work.  Only what orders the experts is
+// computed for all of them; the chosen ones' scores are taken at the end.
+//
+// Bound by vector instructions: about 35 a score and 20 a round and token.
+template <int SLOTS, int ZDT>
+__global__ __launch_bounds__(256) void gate_kernel(GateLaunch a, int lg) {
+  __shared__ float terms[4][64 * 16];  // softmax terms of grouped experts, for their sum's order
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int t = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(wave);
+  if (t >= a.T) return;
   const bool pick_groups = a.top_groups < a.n_groups;
-  float z[SLOTS], s[SLOTS];
-  bool in[SLOTS];
+  const int G = pick_groups ? a.n_groups : 1, EG = a.E / G, P = 1 << lg;
+  const int g = lane >> lg, p = lane & (P - 1), e0 = g * EG + p;
+  const bool top2 = pick_groups && a.group_score == MOE_GROUP_TOP2_SUM;
+
+  float z[SLOTS];
+  const int64_t row = (int64_t)t * a.z_stride;
 #pragma unroll
   for (int i = 0; i < SLOTS; i++) {
-    const int e = min(lane + 64 * i, E - 1);
-    const int64_t at = (int64_t)t * a.z_stride + e;
-    z[i] = a.z_dtype == X_BF16 ? bf16_bits_to_float(static_cast<const uint16_t*>(a.z)[at])
-                               : static_cast<const float*>(a.z)[at];
-    in[i] = lane + 64 * i < E && z[i] > -0x1p127f;  // (false for NaN)
-    z[i] = in[i] ? fminf(z[i], 3.402823466e38f) : -INFINITY;
+    const bool own = g < G && p + P * i < EG;
+    const int64_t at = row + (own ? e0 + P * i : 0);
+    float v;
+    if constexpr (ZDT == X_BF16)
+      v = bf16_bits_to_float(static_cast<const uint16_t*>(a.z)[at]);
+    else
+      v = static_cast<const float*>(a.z)[at];
+    // (false for NaN)
+    z[i] = own && v > -0x1p127f ? fminf(v, 3.402823466e38f) : -INFINITY;
   }
-  if (a.score == MOE_SCORE_SIGMOID) {
-#pragma unroll
-    for (int i = 0; i < SLOTS; i++) s[i] = sigmoid32(z[i]);
-  } else {
-    float m = -INFINITY;
+
+  float m = 0.0f, total = 1.0f;  // softmax: the largest logit, the sum of the terms
+  if (a.score == MOE_SCORE_SOFTMAX) {
+    m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < SLOTS; i++) m = fmaxf(m, z[i]);
+    m = wave_fmax(m);
+  }
+  // a masked expert's term is 0 and its -inf stays
+  auto term = [&](float x) { return x > -INFINITY ? exp32(fmaxf(x - m, -80.0f)) : 0.0f; };
+  float v[SLOTS];
+  if (a.score == MOE_SCORE_SOFTMAX) {
+    float part = 0.0f;
 #pragma unroll
-    for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x, 64));
-    float p = 0.0f;
+    for (int i = 0; i < SLOTS; i++) v[i] = term(z[i]);
+    if (pick_groups) {  // partial e % 64 is another lane's
+#pragma unroll
+      for (int i = 0; i < SLOTS; i++)
+        if (g < G && p + P * i < EG) terms[wave][e0 + P * i] = v[i];
+      __builtin_amdgcn_wave_barrier();  // (a wave's LDS operations are in order)
+      for (int e = lane; e < a.E; e += 64) part = part + terms[wave][e];
+    } else {
+#pragma unroll
+      for (int i = 0; i < SLOTS; i++) part = part + v[i];
+    }
+#pragma unroll
+    for (int s = 32; s >= 1; s >>= 1) part = part + __shfl_xor(part, s, 64);
+    total = part;
+  }
+  auto score = [&](float x, float e) {  // e: its softmax term
+    return a.score == MOE_SCORE_SIGMOID ? sigmoid_score(x) : e / total;
+  };
+  if (a.bias || top2) {
 #pragma unroll
     for (int i = 0; i < SLOTS; i++) {
-      s[i] = in[i] ? exp32(fmaxf(z[i] - m, -80.0f)) : 0.0f;
-      p = p + s[i];
+      float s = score(z[i], v[i]);
+      if (a.bias) s = s + a.bias[g < G && p + P * i < EG ? e0 + P * i : 0];
+      v[i] = z[i] > -INFINITY && s > -INFINITY ? s : -INFINITY;
     }
+  } else {
 #pragma unroll
-    for (int x = 32; x >= 1; x >>= 1) p = p + __shfl_down(p, x, 64);
-    p = __shfl(p, 0, 64);
-#pragma unroll
-    for (int i = 0; i < SLOTS; i++) s[i] = s[i] / p;
+    for (int i = 0; i < SLOTS; i++) v[i] = z[i];
   }
-  float v[SLOTS];
-#pragma unroll
-  for (int i = 0; i < SLOTS; i++) {
-    const int e = min(lane + 64 * i, E - 1);
-    v[i] = a.bias ? s[i] + a.bias[e] : (pick_groups && a.group_score == MOE_GROUP_TOP2_SUM ? s[i] : z[i]);
-    if (!in[i] || !(v[i] > -INFINITY)) v[i] = -INFINITY;
-  }
+
   if (pick_groups) {
-#pragma unroll
-    for (int i = 0; i < SLOTS; i++) sv[lane + 64 * i] = v[i];
-    __syncthreads();
     float b1 = -INFINITY, b2 = -INFINITY;
-    if (lane < a.n_groups)
-      for (int i = 0; i < EG; i++) {
-        const float x = sv[lane * EG + i];
-        b2 = fmaxf(b2, fminf(b1, x));
-        b1 = fmaxf(b1, x);
-      }
-    if (a.group_score == MOE_GROUP_TOP2_SUM && b2 > -INFINITY) b1 = b1 + b2;
-    uint64_t key = rank_key(b1, lane), kept = 0;
-    for (int r = 0; r < a.top_groups; r++) {
-      const uint64_t best = wave_max_u64(key);
-      if (best == 0) break;
-      kept |= 1ull << (int)~(uint32_t)best;
-      if (key == best) key = 0;
+#pragma unroll
+    for (int i = 0; i < SLOTS; i++) {
+      b2 = fmaxf(b2, fminf(b1, v[i]));
+      b1 = fmaxf(b1, v[i]);
     }
+    for (int s = 1; s < P; s <<= 1) {
+      const float c1 = __shfl_xor(b1, s, 64), c2 = __shfl_xor(b2, s, 64);
+      b2 = fmaxf(fmaxf(b2, c2), fminf(b1, c1));
+      b1 = fmaxf(b1, c1);
+    }
+    if (top2 && b2 > -INFINITY) b1 = b1 + b2;
+    int before = 0;  // groups that come before this lane's
+    for (int h = 0; h < G; h++) {
+      const float c = read_lane(b1, h << lg);
+      before += c > b1 || (c == b1 && h < g);
+    }
+#pragma unroll
+    for (int i = 0; i < SLOTS; i++) v[i] = before < a.top_groups ? v[i] : -INFINITY;
+  }
+
+  int my_e = -1;
+  float my_z = -INFINITY;
+  for (int r = 0; r < a.k; r++) {
+    float b = v[0];
+#pragma unroll
+    for (int i = 1; i < SLOTS; i++) b = fmaxf(b, v[i]);
+    b = wave_fmax(b);
+    if (!(b > -INFINITY)) break;
+    uint64_t has[SLOTS], any = 0;
+#pragma unroll
+    for (int i = 0; i < SLOTS; i++) {
+      has[i] = __ballot(v[i] == b);  // (-0 == +0)
+      any |= has[i];
+    }
+    const int first = __builtin_ctzll(any) >> lg;  // the lowest group
+    const uint64_t lanes = (lg == 6 ? ~0ull : (1ull << P) - 1) << (first << lg);
+    int slot = 0;
+    uint64_t in_slot = 0;
+#pragma unroll
+    for (int i = SLOTS - 1; i >= 0; i--)
+      if (has[i] & lanes) {
+        slot = i;
+        in_slot = has[i] & lanes;
+      }
+    const int l = __builtin_ctzll(in_slot);
+    const int e = first * EG + (l & (P - 1)) + P * slot;
+    float ze = 0.0f;
 #pragma unroll
     for (int i = 0; i < SLOTS; i++)
-      if (!(kept >> ((lane + 64 * i) / EG) & 1)) v[i] = -INFINITY;
-  }
-  uint64_t key[SLOTS];
-#pragma unroll
-  for (int i = 0; i < SLOTS; i++) key[i] = rank_key(v[i], lane + 64 * i);
-  int my_e = -1;
-  float my_s = 0.0f, total = 0.0f;
-  for (int r = 0; r < a.k; r++) {
-    uint64_t best = 0;
-#pragma unroll
-    for (int i = 0; i < SLOTS; i++) best = key[i] > best ? key[i] : best;
-    best = wave_max_u64(best);
-    if (best == 0) break;
-    const int e = (int)~(uint32_t)best;
-    float se = 0.0f;
-#pragma unroll
-    for (int i = 0; i < SLOTS; i++) {
-      if (key[i] == best) key[i] = 0;
-      if (e >> 6 == i) se = s[i];
+      if (slot == i) {
+        ze = read_lane(z[i], l);
+        v[i] = lane == l ? -INFINITY : v[i];
+      }
+    if (lane == r) {
+      my_e = e;
+      my_z = ze;
     }
-    se = __shfl(se, e & 63, 64);
-    total = total + se;
-    if (lane == r) my_e = e, my_s = se;
   }
+  const float s = my_e >= 0 ? score(my_z, term(my_z)) : 0.0f;
+  float sum = 0.0f;
+  for (int r = 0; r < a.k; r++) sum = sum + read_lane(s, r);
   if (lane < a.k) {
-    const float w = a.renormalize ? (my_e >= 0 ? my_s / total : 0.0f) : my_s;
+    const float w = a.renormalize && my_e >= 0 ? s / sum : s;
     a.idx[(int64_t)t * a.k + lane] = my_e;
     a.wt[(int64_t)t * a.k + lane] = w * a.scale;
   }
 }
 
-hipError_t launch_gate(const GateLaunch& a, hipStream_t s) {
-  const dim3 grid((unsigned)a.T);
-  if (a.E <= 256)
-    QMOE_LAUNCH(gate_kernel<4>, grid, dim3(64), 0, s, a);
-  else if (a.E <= 512)
-    QMOE_LAUNCH(gate_kernel<8>, grid, dim3(64), 0, s, a);
+template <int SLOTS>
+static void launch_slots(const GateLaunch& a, int lg, hipStream_t s) {
+  const dim3 grid((unsigned)((a.T + 3) / 4));
+  if (a.z_dtype == X_BF16)
+    QMOE_LAUNCH((gate_kernel<SLOTS, X_BF16>), grid, dim3(256), 0, s, a, lg);
   else
-    QMOE_LAUNCH(gate_kernel<16>, grid, dim3(64), 0, s, a);
+    QMOE_LAUNCH((gate_kernel<SLOTS, X_F32>), grid, dim3(256), 0, s, a, lg);
+}
+
+hipError_t launch_gate(const GateLaunch& a, hipStream_t s) {
+  const int G = a.top_groups < a.n_groups ? a.n_groups : 1;
+  int lg = 6;
+  while ((G << lg) > 64) lg--;
+  const int slots = (a.E / G + (1 << lg) - 1) >> lg;  // at most 32
+  if (slots <= 4)
+    launch_slots<4>(a, lg, s);
+  else if (slots <= 6)
+    launch_slots<6>(a, lg, s);
+  else if (slots <= 8)
+    launch_slots<8>(a, lg, s);
+  else if (slots <= 16)
+    launch_slots<16>(a, lg, s);
+  else
+    launch_slots<32>(a, lg, s);
   return hipGetLastError();
 }
 
