@@ -3,6 +3,8 @@
 // scores decide selections near a tie, so each is rounded on its own.
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.hpp"
 #include "kernels.hpp"
 #include "topk.hpp"
@@ -41,20 +43,19 @@ __device__ __forceinline__ float sigmoid_score(float z) {
   return recip_exact(1.0f + exp32(-fminf(fmaxf(z, -80.0f), 80.0f)));
 }
 
-template <int CTRL, int ROW_MASK>
-__device__ __forceinline__ float dpp_fmax_step(float v) {
-  const int ninf = (int)0xff800000u;
-  return fmaxf(v, __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(ninf, (int)__float_as_uint(v), CTRL, ROW_MASK,
-                                                                        0xf, false)));
-}
-// Maximum over the wave, the same in every lane.
+// Maximum over the wave, the same in every lane.  Lanes that a step's shift
+// gives no source keep their value.  (Written out: from the builtins the
+// compiler makes a move and a maximum of each step.  A step reads other lanes'
+// results of the one before, which takes two wait states.)
 __device__ __forceinline__ float wave_fmax(float v) {
-  v = dpp_fmax_step<0x111, 0xf>(v);
-  v = dpp_fmax_step<0x112, 0xf>(v);
-  v = dpp_fmax_step<0x114, 0xf>(v);
-  v = dpp_fmax_step<0x118, 0xf>(v);
-  v = dpp_fmax_step<0x142, 0xa>(v);
-  v = dpp_fmax_step<0x143, 0xc>(v);
+  asm("s_nop 1\n\t"
+      "v_max_f32_dpp %0, %0, %0 row_shr:1 row_mask:0xf bank_mask:0xf\n\ts_nop 1\n\t"
+      "v_max_f32_dpp %0, %0, %0 row_shr:2 row_mask:0xf bank_mask:0xf\n\ts_nop 1\n\t"
+      "v_max_f32_dpp %0, %0, %0 row_shr:4 row_mask:0xf bank_mask:0xf\n\ts_nop 1\n\t"
+      "v_max_f32_dpp %0, %0, %0 row_shr:8 row_mask:0xf bank_mask:0xf\n\ts_nop 1\n\t"
+      "v_max_f32_dpp %0, %0, %0 row_bcast:15 row_mask:0xa bank_mask:0xf\n\ts_nop 1\n\t"
+      "v_max_f32_dpp %0, %0, %0 row_bcast:31 row_mask:0xc bank_mask:0xf\n\ts_nop 1"
+      : "+v"(v));
   return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 __device__ __forceinline__ float read_lane(float v, int lane) {
@@ -74,31 +75,35 @@ __device__ __forceinline__ float read_lane(float v, int lane) {
 // computed for all of them; the chosen ones' scores are taken at the end.
 //
 // Bound by vector instructions: about 35 a score and 20 a round and token.
-template <int SLOTS, int ZDT>
-__global__ __launch_bounds__(256) void gate_kernel(GateLaunch a, int lg) {
+template <int SLOTS, int ZDT, int LG>  // LG < 0: any other number of lanes
+__global__ __launch_bounds__(256) void gate_kernel(GateLaunch a, int lg_) {
   __shared__ float terms[4][64 * 16];  // softmax terms of grouped experts, for their sum's order
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int t = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(wave);
   if (t >= a.T) return;
-  const bool pick_groups = a.top_groups < a.n_groups;
+  const int lg = LG < 0 ? lg_ : LG;
+  const bool pick_groups = LG == 6 ? false : a.top_groups < a.n_groups;
   const int G = pick_groups ? a.n_groups : 1, EG = a.E / G, P = 1 << lg;
   const int g = lane >> lg, p = lane & (P - 1), e0 = g * EG + p;
   const bool top2 = pick_groups && a.group_score == MOE_GROUP_TOP2_SUM;
 
+  // slots that exist: i < n_own (unsigned offsets from a uniform row pointer)
+  const int n_own = g < G && p < EG ? (EG - p + P - 1) >> lg : 0;
+  using Z = typename std::conditional<ZDT == X_BF16, uint16_t, float>::type;
+  const Z* zrow = static_cast<const Z*>(a.z) + (int64_t)t * a.z_stride;
+  const uint32_t at = n_own > 0 ? e0 : 0;
   float z[SLOTS];
-  const int64_t row = (int64_t)t * a.z_stride;
 #pragma unroll
   for (int i = 0; i < SLOTS; i++) {
-    const bool own = g < G && p + P * i < EG;
-    const int64_t at = row + (own ? e0 + P * i : 0);
-    float v;
+    const Z v = zrow[i < n_own ? at + P * i : at];
     if constexpr (ZDT == X_BF16)
-      v = bf16_bits_to_float(static_cast<const uint16_t*>(a.z)[at]);
+      z[i] = bf16_bits_to_float(v);
     else
-      v = static_cast<const float*>(a.z)[at];
-    // (false for NaN)
-    z[i] = own && v > -0x1p127f ? fminf(v, 3.402823466e38f) : -INFINITY;
+      z[i] = v;
   }
+#pragma unroll
+  for (int i = 0; i < SLOTS; i++)  // (false for NaN)
+    z[i] = i < n_own && z[i] > -0x1p127f ? fminf(z[i], 3.402823466e38f) : -INFINITY;
 
   float m = 0.0f, total = 1.0f;  // softmax: the largest logit, the sum of the terms
   if (a.score == MOE_SCORE_SOFTMAX) {
@@ -117,7 +122,7 @@ __global__ __launch_bounds__(256) void gate_kernel(GateLaunch a, int lg) {
     if (pick_groups) {  // partial e % 64 is another lane's
 #pragma unroll
       for (int i = 0; i < SLOTS; i++)
-        if (g < G && p + P * i < EG) terms[wave][e0 + P * i] = v[i];
+        if (i < n_own) terms[wave][e0 + P * i] = v[i];
       __builtin_amdgcn_wave_barrier();  // (a wave's LDS operations are in order)
       for (int e = lane; e < a.E; e += 64) part = part + terms[wave][e];
     } else {
@@ -135,7 +140,7 @@ __global__ __launch_bounds__(256) void gate_kernel(GateLaunch a, int lg) {
 #pragma unroll
     for (int i = 0; i < SLOTS; i++) {
       float s = score(z[i], v[i]);
-      if (a.bias) s = s + a.bias[g < G && p + P * i < EG ? e0 + P * i : 0];
+      if (a.bias) s = s + a.bias[i < n_own ? at + P * i : at];
       v[i] = z[i] > -INFINITY && s > -INFINITY ? s : -INFINITY;
     }
   } else {
@@ -159,7 +164,7 @@ __global__ __launch_bounds__(256) void gate_kernel(GateLaunch a, int lg) {
     int before = 0;  // groups that come before this lane's
     for (int h = 0; h < G; h++) {
       const float c = read_lane(b1, h << lg);
-      before += c > b1 || (c == b1 && h < g);
+      before += h < g ? c >= b1 : c > b1;
     }
 #pragma unroll
     for (int i = 0; i < SLOTS; i++) v[i] = before < a.top_groups ? v[i] : -INFINITY;
@@ -213,30 +218,33 @@ __global__ __launch_bounds__(256) void gate_kernel(GateLaunch a, int lg) {
   }
 }
 
-template <int SLOTS>
+template <int SLOTS, int LG>
 static void launch_slots(const GateLaunch& a, int lg, hipStream_t s) {
   const dim3 grid((unsigned)((a.T + 3) / 4));
   if (a.z_dtype == X_BF16)
-    QMOE_LAUNCH((gate_kernel<SLOTS, X_BF16>), grid, dim3(256), 0, s, a, lg);
+    QMOE_LAUNCH((gate_kernel<SLOTS, X_BF16, LG>), grid, dim3(256), 0, s, a, lg);
   else
-    QMOE_LAUNCH((gate_kernel<SLOTS, X_F32>), grid, dim3(256), 0, s, a, lg);
+    QMOE_LAUNCH((gate_kernel<SLOTS, X_F32, LG>), grid, dim3(256), 0, s, a, lg);
+}
+
+template <int LG>
+static void launch_lanes(const GateLaunch& a, int lg, int slots, hipStream_t s) {
+  if (slots <= 4) return launch_slots<4, LG>(a, lg, s);
+  if (slots <= 6) return launch_slots<6, LG>(a, lg, s);
+  if (slots <= 8) return launch_slots<8, LG>(a, lg, s);
+  if (slots <= 16) return launch_slots<16, LG>(a, lg, s);
+  if constexpr (LG < 0) launch_slots<32, LG>(a, lg, s);
 }
 
 hipError_t launch_gate(const GateLaunch& a, hipStream_t s) {
   const int G = a.top_groups < a.n_groups ? a.n_groups : 1;
   int lg = 6;
   while ((G << lg) > 64) lg--;
-  const int slots = (a.E / G + (1 << lg) - 1) >> lg;  // at most 32
-  if (slots <= 4)
-    launch_slots<4>(a, lg, s);
-  else if (slots <= 6)
-    launch_slots<6>(a, lg, s);
-  else if (slots <= 8)
-    launch_slots<8>(a, lg, s);
-  else if (slots <= 16)
-    launch_slots<16>(a, lg, s);
+  const int slots = (a.E / G + (1 << lg) - 1) >> lg;  // at most 16 for powers of two, 32 for other G
+  if (lg == 6)  // no groups: the lanes' offsets are constants
+    launch_lanes<6>(a, lg, slots, s);
   else
-    launch_slots<32>(a, lg, s);
+    launch_lanes<-1>(a, lg, slots, s);
   return hipGetLastError();
 }
 
