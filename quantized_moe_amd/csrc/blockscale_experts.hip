@@ -189,7 +189,96 @@ __global__ __launch_bounds__(256) void bs_combine_kernel(BsDown a) {
   reinterpret_cast<f32x4_t*>(a.y)[i] = y;
 }
 
-size_t bs_down_ws(int T, int k, int d) { return (size_t)T * k * d * 4; }
+// Few tokens: one launch and no workspace.  A block owns 16 outputs of one
+// token; its 16 waves take equal stretches of the token's (route, K block)
+// pairs, straight from memory with U pairs requested at a time (all of them at
+// 6 routes of 2048 inputs: one round trip).  Every column of the matrix step
+// holds the same row.  A wave's sum of each route goes to LDS; they are added
+// in the order of the waves, then the routes weighted in their order.
+template <int U>
+__global__ __launch_bounds__(1024) void bs_down_token_kernel(BsDown a) {
+  constexpr int WAVES = 16;
+  __shared__ float part[TOPK_MAX_K][WAVES][16];
+  __shared__ float route_y[TOPK_MAX_K][16];
+  __shared__ int route_row[TOPK_MAX_K], route_e[TOPK_MAX_K];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, quad = lane >> 4;
+  const int n0 = blockIdx.x * 16, t = blockIdx.y, KB = bs_blocks(a.f), DB = bs_blocks(a.d);
+  for (int i = threadIdx.x; i < TOPK_MAX_K * WAVES * 16; i += 1024) (&part[0][0][0])[i] = 0.0f;
+  if (wave < a.k) {  // wave j finds route j's row and expert: the last with offsets[e] <= row
+    const int row = a.pos[t * a.k + wave];
+    int below = 0;
+#pragma unroll
+    for (int i = 0; i < MAX_EXPERTS / 64; i++)
+      if (64 * i < a.E) {
+        const int e = 64 * i + lane;
+        below += __popcll(__ballot(e < a.E && a.offsets[min(e, a.E - 1) + 1] <= row));
+      }
+    if (lane == 0) {
+      route_row[wave] = row < a.T * a.k ? row : -1;
+      route_e[wave] = min(below, a.E - 1);
+    }
+  }
+  __syncthreads();
+  const int pairs = a.k * KB, u0 = wave * pairs / WAVES, u1 = (wave + 1) * pairs / WAVES;
+  const i32x4_t zero = {0, 0, 0, 0};
+  f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int ub = u0; ub < u1; ub += U) {
+    i32x8_t w[U], x[U];
+    float sc[U];
+#pragma unroll
+    for (int i = 0; i < U; i++) {
+      const int u = min(ub + i, u1 - 1), j = u / KB, kb = u - j * KB;
+      const int row = __builtin_amdgcn_readfirstlane(route_row[j]), e = __builtin_amdgcn_readfirstlane(route_e[j]);
+      const bool on = ub + i < u1 && row >= 0;
+      const int k0 = kb * BS + 16 * quad;
+      const uint8_t* wp = a.w_down + ((int64_t)e * a.d + n0 + r) * a.f + k0;
+      const uint8_t* xp = a.hq + (int64_t)row * a.f + k0;
+      const bool in0 = on && k0 < a.f, in1 = on && k0 + 64 < a.f;
+      w[i] = join_pieces(in0 ? *reinterpret_cast<const i32x4_t*>(wp) : zero,
+                         in1 ? *reinterpret_cast<const i32x4_t*>(wp + 64) : zero);
+      x[i] = join_pieces(in0 ? *reinterpret_cast<const i32x4_t*>(xp) : zero,
+                         in1 ? *reinterpret_cast<const i32x4_t*>(xp + 64) : zero);
+      sc[i] = on ? a.hs[(int64_t)row * KB + kb] * a.s_down[((int64_t)e * DB + n0 / BS) * KB + kb] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < U; i++) {
+      const int u = ub + i, j = u / KB;
+      if (u >= u1) continue;
+      F16Block wf, xf;
+      wf.set(w[i]);
+      xf.set(x[i]);
+      const f32x4_t p = mfma_block(wf, xf);
+#pragma unroll
+      for (int q = 0; q < 4; q++) acc[q] = __builtin_fmaf(p[q], sc[i], acc[q]);
+      if (u + 1 == u1 || (u + 1) / KB != j) {  // the wave's last pair of this route
+        if (r == 0) *reinterpret_cast<f32x4_t*>(&part[j][wave][4 * quad]) = acc;
+        acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+    }
+  }
+  __syncthreads();
+  const int j = threadIdx.x >> 4, n = threadIdx.x & 15;
+  if (j < a.k) {
+    float s = 0.0f;
+#pragma unroll
+    for (int v = 0; v < WAVES; v++) s += part[j][v][n];
+    route_y[j][n] = s;
+  }
+  __syncthreads();
+  if (threadIdx.x < 16) {
+    const int64_t at = (int64_t)t * a.d + n0 + n;
+    float y = a.add ? a.add[at] : 0.0f;
+    for (int i = 0; i < a.k; i++)
+      if (route_row[i] >= 0) y = __builtin_fmaf(a.wt[t * a.k + i], route_y[i][n], y);
+    a.y[at] = y;
+  }
+}
+
+// (2 tokens: 27.6 us so, 25.6 us as products and a combine)
+constexpr int TOKEN_MAX_T = 1;
+
+size_t bs_down_ws(int T, int k, int d) { return T <= TOKEN_MAX_T ? 0 : (size_t)T * k * d * 4; }
 
 template <class C>
 static hipError_t launch_down(const BsDown& a, hipStream_t s) {
@@ -217,6 +306,12 @@ static hipError_t launch_down_products(const BsDown& a, hipStream_t s) {
 }
 
 hipError_t launch_bs_down(const BsDown& a, hipStream_t s) {
+  if (a.T <= TOKEN_MAX_T) {
+    const int pid = prof_begin("bs_down_token", s);
+    QMOE_LAUNCH(bs_down_token_kernel<6>, dim3(a.d / 16, a.T), dim3(1024), 0, s, a);
+    prof_end(pid, s);
+    return hipGetLastError();
+  }
   int pid = prof_begin("bs_down", s);
   hipError_t e = launch_down_products(a, s);
   prof_end(pid, s);
