@@ -265,11 +265,13 @@ def _need(fn: str, **tensors) -> None:
 def _rows_of(fn: str, name: str, t: torch.Tensor, dtypes) -> int:
     """Row stride (elements) of a 2-D tensor whose rows have no gaps."""
     if t.dtype not in dtypes:
-        raise TypeError(f"{fn}: {name} must be one of {dtypes}, not {t.dtype}")
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise TypeError(f"{fn}: {name} must be one of {tuple(dtypes)}, not {t.dtype}")
+    if t.dim() != 2:
         raise ValueError(f"{fn}: {name} must be 2-D with contiguous rows")
-    # (a single row's stride is free; torch leaves any number there)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    (rows, cols), (ld, step) = t.shape, t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{fn}: {name} must be 2-D with contiguous rows")
+    return ld if rows > 1 else cols  # (a single row's stride is free; torch leaves any number there)
 
 
 def scale_blocks(n: int) -> int:
@@ -278,7 +280,7 @@ def scale_blocks(n: int) -> int:
 
 
 _F8 = (torch.float8_e4m3fn, torch.uint8)
-_XDT = (torch.float32, torch.bfloat16)
+_XDT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 
 def gate(n_experts: int, top_k: int, score="sigmoid", n_groups=1, top_groups=1, group_score="max", renormalize=True,
@@ -302,26 +304,32 @@ def router_logits(w_router, x, z, stream=None) -> None:
 
 
 def gate_topk(gate: MoeGate, z, idx, wt, stream=None) -> None:
-    T, k = z.shape[0], gate.top_k
+    T, E = z.shape
+    k = gate.top_k
     stride = _rows_of("gate_topk", "z", z, _XDT)
-    if z.shape[1] != gate.n_experts:
-        raise ValueError(f"gate_topk: z has {z.shape[1]} logits per row, the gate {gate.n_experts} experts")
+    if E != gate.n_experts:
+        raise ValueError(f"gate_topk: z has {E} logits per row, the gate {gate.n_experts} experts")
     if not (_is(idx, _I32T, (T, k)) and _is(wt, _F32, (T, k))):
         _need("gate_topk", idx=(idx, torch.int32, (T, k)), wt=(wt, torch.float32, (T, k)))
-    _check(lib().moe_gate_topk(ctypes.byref(gate), _ptr(z), x_dtype_of(z), stride, T, _ptr(idx), _ptr(wt),
-                               _stream(stream)))
+    rc = lib().moe_gate_topk(ctypes.byref(gate), z.data_ptr(), _XDT[z.dtype], stride, T, idx.data_ptr(), wt.data_ptr(),
+                             _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def blockscale_quantize(x, q, s, stream=None) -> None:
     """x [M][K] to q (float8_e4m3fn or uint8) [M][K] and s [M][ceil(K / 128)]."""
     fn = "blockscale_quantize"
-    M, K = x.shape
     ldx, ldq = _rows_of(fn, "x", x, _XDT), _rows_of(fn, "q", q, _F8)
+    M, K = x.shape
     if q.shape != x.shape:
         raise ValueError(f"{fn}: q has shape {tuple(q.shape)}, needs {tuple(x.shape)}")
     if not _is(s, _F32, (M, (K + 127) // 128)):
         _need(fn, s=(s, torch.float32, (M, scale_blocks(K))))
-    _check(lib().moe_blockscale_quantize(_ptr(x), x_dtype_of(x), ldx, M, K, _ptr(q), ldq, _ptr(s), _stream(stream)))
+    rc = lib().moe_blockscale_quantize(x.data_ptr(), _XDT[x.dtype], ldx, M, K, q.data_ptr(), ldq, s.data_ptr(),
+                                       _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def blockscale_matmul_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -334,16 +342,18 @@ def blockscale_matmul(xq, xs, wq, ws, y, workspace=None, stream=None) -> None:
     """y [M][N] (float32 or bfloat16) = xq [M][K] times wq [N][K] transposed,
     with scales xs [M][ceil(K / 128)] and ws [ceil(N / 128)][ceil(K / 128)]."""
     fn = "blockscale_matmul"
+    ldx, ldy = _rows_of(fn, "xq", xq, _F8), _rows_of(fn, "y", y, _XDT)
     (M, K), N = xq.shape, wq.shape[0]
     KB, NB = (K + 127) // 128, (N + 127) // 128
-    ldx, ldy = _rows_of(fn, "xq", xq, _F8), _rows_of(fn, "y", y, _XDT)
     if y.shape != (M, N):
         raise ValueError(f"{fn}: y has shape {tuple(y.shape)}, needs {(M, N)}")
     if not (_is(xs, _F32, (M, KB)) and _is(wq, _U8, (N, K)) and _is(ws, _F32, (NB, KB))):
         _need(fn, xs=(xs, torch.float32, (M, KB)), wq=(wq, torch.uint8, (N, K)), ws=(ws, torch.float32, (NB, KB)))
-    n_ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().moe_blockscale_matmul(_ptr(xq), ldx, _ptr(xs), M, _ptr(wq), _ptr(ws), N, K, _ptr(y), x_dtype_of(y),
-                                       ldy, _ptr(workspace), n_ws, _stream(stream)))
+    wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    rc = lib().moe_blockscale_matmul(xq.data_ptr(), ldx, xs.data_ptr(), M, wq.data_ptr(), ws.data_ptr(), N, K,
+                                     y.data_ptr(), _XDT[y.dtype], ldy, wp, wn, _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def blockscale_gateup(xq, xs, k, offsets, perm, w_gate, s_gate, w_up, s_up, hq, hs, stream=None) -> None:
