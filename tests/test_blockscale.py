@@ -117,6 +117,24 @@ def test_quantize_is_exact(M, K, dtype):
 
 
 @gpu
+@pytest.mark.parametrize("exponent", [-126, -100, -81, -79, -40, 0, 60, 120])
+def test_quantize_divides_exactly(exponent):
+    """Groups of every size of scale; many quotients, among them values half way between two codes."""
+    rng = np.random.default_rng(exponent + 200)
+    M, K = 512, 1024
+    x = rng.standard_normal((M, K)).astype(np.float32)
+    x[: M // 2] = np.round(x[: M // 2] * 16) / 16 * 1.9375   # few significant bits: ties
+    x = (x * np.float32(2.0) ** exponent).astype(np.float32)
+    q, s = torch.empty(M, K, dtype=F8, device=DEV), torch.empty(M, nb(K), device=DEV)
+    lib.blockscale_quantize(torch.from_numpy(x).to(DEV), q, s)
+    b = x.reshape(M, -1, 128)
+    s_ref = np.maximum(np.abs(b).max(2), np.float32(2.0 ** -100)) / np.float32(448)
+    assert np.array_equal(s.cpu().numpy(), s_ref)
+    q_ref = torch.from_numpy((b / s_ref[:, :, None]).reshape(M, K)).to(F8)
+    assert torch.equal(down(q).view(torch.uint8), q_ref.view(torch.uint8))
+
+
+@gpu
 def test_quantize_non_finite_groups():
     x = torch.ones(4, 384)
     x[0, 5], x[1, 200], x[2, 300] = float("inf"), float("nan"), float("-inf")
