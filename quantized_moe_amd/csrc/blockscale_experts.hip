@@ -67,7 +67,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void bs_gateup_kerne
   f32x4_t acc[2][C::TN][C::TM];
   tile_product<C>(
       lds, wbuf, ws, 1, a.d, xbuf, sbuf, [&](int i) { return i < t.rows ? (uint32_t)token(i) * a.d : BUFFER_OUT; },
-      [&](int i) { return i < t.rows ? (uint32_t)token(i) * KB * 4 : BUFFER_OUT; }, acc);
+      [&](int i) { return i < t.rows ? (uint32_t)token(i) * KB * 4 : BUFFER_OUT; }, 0, KB, acc);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, quad = lane >> 4;
   const int wn = wave % C::WN, wm = wave / C::WN;
@@ -153,7 +153,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void bs_down_kernel(
   f32x4_t acc[1][C::TN][C::TM];
   tile_product<C>(
       lds, wbuf, ws, DB - n0 / BS, a.f, xbuf, sbuf, [&](int i) { return i < t.rows ? (uint32_t)(i * a.f) : BUFFER_OUT; },
-      [&](int i) { return i < t.rows ? (uint32_t)(i * KB * 4) : BUFFER_OUT; }, acc);
+      [&](int i) { return i < t.rows ? (uint32_t)(i * KB * 4) : BUFFER_OUT; }, 0, KB, acc);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, quad = lane >> 4;
   const int wn = wave % C::WN, wm = wave / C::WN;
 #pragma unroll

@@ -47,13 +47,13 @@ struct Tile {
 // acc[mat][i][j] = the wave's tiles.  wbuf: the tile's rows of each matrix,
 // K bytes apart; ws: the scales [ws_rows][KB] of their first block on; xbuf,
 // sbuf with xrow(i), srow(i): the byte offsets of row i's codes and scales
-// (BUFFER_OUT: no such row).  With KS > 1 the sums are group 0's; false for the
-// other groups' threads.
+// (BUFFER_OUT: no such row); K blocks kb0 <= kb < kb1 of the ones that K has.
+// With KS > 1 the sums are group 0's; false for the other groups' threads.
 template <class C, class XRow, class SRow>
 __device__ __forceinline__ bool tile_product(uint8_t* lds, const __amdgpu_buffer_rsrc_t (&wbuf)[C::NMAT],
                                              const float* const (&ws)[C::NMAT], int ws_rows, int K,
                                              __amdgpu_buffer_rsrc_t xbuf, __amdgpu_buffer_rsrc_t sbuf, XRow xrow,
-                                             SRow srow, f32x4_t (&acc)[C::NMAT][C::TN][C::TM]) {
+                                             SRow srow, int kb0, int kb1, f32x4_t (&acc)[C::NMAT][C::TN][C::TM]) {
   constexpr int WAVES = C::WAVES, TN = C::TN, TM = C::TM, KS = C::KS, ROWS = C::TILE_ROWS;
   const int lane = threadIdx.x & 63, block_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = block_wave / WAVES, wave = block_wave % WAVES;
@@ -119,21 +119,21 @@ __device__ __forceinline__ bool tile_product(uint8_t* lds, const __amdgpu_buffer
   // (blocks past the last: the last again, into a stage that nothing reads)
 #pragma unroll
   for (int b = 0; b < C::STAGES - 1; b++) {
-    const int kb = min(group + b * KS, KB - 1);
+    const int kb = min(kb0 + group + b * KS, kb1 - 1);
     cut_last(kb);
 #pragma unroll
     for (int i = 0; i < C::COPIES; i++) fetch(kb, b, i);
   }
   int stage = 0;
-  for (int k0 = 0; k0 < KB; k0 += KS) {
+  for (int k0 = kb0; k0 < kb1; k0 += KS) {
     const int kb = k0 + group;
     lds_landed<(C::STAGES - 2) * (C::COPIES + 1)>();
     const int fill = stage == 0 ? C::STAGES - 1 : stage - 1;
-    if (KS > 1 && kb >= KB) break;  // (the last round has no block for this group)
+    if (KS > 1 && kb >= kb1) break;  // (the last round has no block for this group)
     const uint8_t* st = stages + stage * C::STAGE;
     // The copies into the free stage are spread over the tile rows of this
     // block: all at once they fill the address queue and hold up the waves.
-    const int next = min(kb + (C::STAGES - 1) * KS, KB - 1);
+    const int next = min(kb + (C::STAGES - 1) * KS, kb1 - 1);
     cut_last(next);
     auto fetch_some = [&](int i) {
 #pragma unroll

@@ -176,7 +176,7 @@ def test_matmul(M, N, K, out):
 @pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("M,N,K", [(2090, 4100, 1040), (4097, 2050, 2064), (700, 640, 4112), (4000, 4200, 1040),
                                    (700, 5000, 144), (1030, 2300, 1168), (530, 4100, 1296), (33, 520, 1552), (1800, 1900, 16),
-                                   (3900, 3800, 272)])
+                                   (3900, 3800, 272), (100, 300, 8192), (40, 129, 4112), (250, 1999, 4096), (33, 1, 16384)])
 def test_matmul_many_tiles(M, N, K, out):
     """Several tiles of the largest kind in both directions, the last ones short."""
     rng = np.random.default_rng(M + N)
@@ -190,6 +190,22 @@ def test_matmul_many_tiles(M, N, K, out):
     err = (y.cpu().double()[rows] - ref).abs()
     assert (err <= tol).all(), float((err / tol).max())
     assert torch.isfinite(y).all()
+
+
+@gpu
+def test_matmul_of_a_shared_k_repeats_bitwise():
+    rng = np.random.default_rng(6)
+    M, N, K = 70, 500, 8208
+    (xq, xs), (wq, ws) = make_rows(rng, M, K), make_weight(rng, N, K)
+    args = [up(t) for t in (xq, xs, wq, ws)]
+    n = lib.blockscale_matmul_workspace_bytes(M, N, K)
+    assert n > 0
+    outs = []
+    for fill in (0x00, 0x7f, 0xff):  # whatever the workspace held before
+        y = torch.empty(M, N, device=DEV)
+        lib.blockscale_matmul(*args, y, torch.full((n,), fill, dtype=torch.uint8, device=DEV))
+        outs.append(y)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
 
 
 @gpu
