@@ -82,11 +82,11 @@ template <class C, typename OUT>
 __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void bs_matmul_tile_kernel(BsMatmul a, int n_tiles, int m_tiles) {
   extern __shared__ __align__(1024) uint8_t lds[];
   // an XCD (block id mod 8) takes a contiguous eighth of the tiles, in strips
-  // of 4 M tiles so that neighbours in time share operands in its L2
+  // of 8 M tiles so that neighbours in time share operands in its L2
   const int id = xcd_order(blockIdx.x, n_tiles * m_tiles);
-  const int strip = id / (4 * n_tiles), in_strip = id - strip * 4 * n_tiles;
-  const int strip_m = min(4, m_tiles - 4 * strip);
-  const int mt = 4 * strip + in_strip % strip_m, nt = in_strip / strip_m;
+  const int strip = id / (8 * n_tiles), in_strip = id - strip * 8 * n_tiles;
+  const int strip_m = min(8, m_tiles - 8 * strip);
+  const int mt = 8 * strip + in_strip % strip_m, nt = in_strip / strip_m;
   const int n0 = nt * C::BN, m0 = mt * C::BM;
   const int KB = bs_blocks(a.K);
   const int rows_n = min(C::BN, a.N - n0), rows_m = min(C::BM, a.M - m0);

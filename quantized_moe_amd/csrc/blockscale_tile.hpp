@@ -33,7 +33,7 @@ struct Tile {
   static constexpr int X_COPIES = (X_UNITS + WAVES - 1) / WAVES;
   static constexpr int COPIES = NMAT * W_COPIES + X_COPIES;
   static constexpr int TILE_ROWS = NMAT * TN;                           // tiles of 16 outputs of a wave
-  static constexpr int SPREAD = TILE_ROWS > 1 ? TILE_ROWS / 2 : 1;      // those that copies go with
+  static constexpr int SPREAD = !EXACT || TILE_ROWS == 1 ? TILE_ROWS : TILE_ROWS / 2;  // those that copies go with
   static constexpr int PER_ROW = (COPIES + SPREAD - 1) / SPREAD;
   // registers: where two blocks of 8 small waves fit a CU's LDS, they fit its registers too
   static constexpr int WAVES_PER_SIMD = 2 * LDS <= 160 * 1024 && THREADS == 512 && TILE_ROWS * TM <= 6 ? 4 : 2;
@@ -196,7 +196,11 @@ __device__ __forceinline__ bool tile_product(uint8_t* lds, const __amdgpu_buffer
         if (i + 1 < ROWS) w_next = wfrag(i + 1);
 #pragma unroll
         for (int j = 0; j < TM; j++) {
-          if (i < ROWS) p[i & 1][j] = mfma_block_e4m3(w, x[j]);
+          if (i < ROWS) {
+            __builtin_amdgcn_s_setprio(1);  // a wave with a matrix step ready goes before one that scales
+            p[i & 1][j] = mfma_block_e4m3(w, x[j]);
+            __builtin_amdgcn_s_setprio(0);
+          }
           if (i > 0) scale(i - 1, j);
           __builtin_amdgcn_sched_barrier(0);
         }
