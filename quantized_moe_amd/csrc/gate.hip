@@ -92,7 +92,7 @@ __global__ __launch_bounds__(256) void gate_kernel(GateLaunch a, int lg_) {
   using Z = typename std::conditional<ZDT == X_BF16, uint16_t, float>::type;
   const Z* zrow = static_cast<const Z*>(a.z) + (int64_t)t * a.z_stride;
   const uint32_t at = n_own > 0 ? e0 : 0;
-  float z[SLOTS];
+  float z[SLOTS], bias[SLOTS] = {};
 #pragma unroll
   for (int i = 0; i < SLOTS; i++) {
     const Z v = zrow[i < n_own ? at + P * i : at];
@@ -100,6 +100,10 @@ __global__ __launch_bounds__(256) void gate_kernel(GateLaunch a, int lg_) {
       z[i] = bf16_bits_to_float(v);
     else
       z[i] = v;
+  }
+  if (a.bias) {  // (requested with the logits: one wait)
+#pragma unroll
+    for (int i = 0; i < SLOTS; i++) bias[i] = a.bias[i < n_own ? at + P * i : at];
   }
 #pragma unroll
   for (int i = 0; i < SLOTS; i++)  // (false for NaN)
@@ -133,16 +137,20 @@ __global__ __launch_bounds__(256) void gate_kernel(GateLaunch a, int lg_) {
     for (int s = 32; s >= 1; s >>= 1) part = part + __shfl_xor(part, s, 64);
     total = part;
   }
-  auto score = [&](float x, float e) {  // e: its softmax term
-    return a.score == MOE_SCORE_SIGMOID ? sigmoid_score(x) : e / total;
-  };
   if (a.bias || top2) {
+    if (a.score == MOE_SCORE_SIGMOID) {
 #pragma unroll
-    for (int i = 0; i < SLOTS; i++) {
-      float s = score(z[i], v[i]);
-      if (a.bias) s = s + a.bias[i < n_own ? at + P * i : at];
-      v[i] = z[i] > -INFINITY && s > -INFINITY ? s : -INFINITY;
+      for (int i = 0; i < SLOTS; i++) v[i] = sigmoid_score(z[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < SLOTS; i++) v[i] = v[i] / total;
     }
+    if (a.bias) {
+#pragma unroll
+      for (int i = 0; i < SLOTS; i++) v[i] = v[i] + bias[i];
+    }
+#pragma unroll
+    for (int i = 0; i < SLOTS; i++) v[i] = z[i] > -INFINITY && v[i] > -INFINITY ? v[i] : -INFINITY;
   } else {
 #pragma unroll
     for (int i = 0; i < SLOTS; i++) v[i] = z[i];
@@ -208,7 +216,8 @@ __global__ __launch_bounds__(256) void gate_kernel(GateLaunch a, int lg_) {
       my_z = ze;
     }
   }
-  const float s = my_e >= 0 ? score(my_z, term(my_z)) : 0.0f;
+  const float chosen = a.score == MOE_SCORE_SIGMOID ? sigmoid_score(my_z) : term(my_z) / total;
+  const float s = my_e >= 0 ? chosen : 0.0f;
   float sum = 0.0f;
   for (int r = 0; r < a.k; r++) sum = sum + read_lane(s, r);
   if (lane < a.k) {
