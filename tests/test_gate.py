@@ -209,6 +209,41 @@ def test_agrees_with_the_sigmoid_router():
 
 
 @gpu
+def test_sigmoid_scores_have_the_defined_bits():
+    """Two million logits, one expert: the plain weight is the score, bit for bit."""
+    rng = np.random.default_rng(10)
+    g = lib.gate(1, 1, renormalize=False)
+    for i in range(32):
+        z = (rng.uniform(-85, 85, 65536) if i % 2 else 3 * rng.standard_normal(65536)).astype(f4)
+        if i == 0:
+            z[:8] = [0.0, -0.0, 80.0, -80.0, 81.0, -81.0, np.finfo(f4).max, -1e38]
+        zd = torch.from_numpy(z).to(DEV).view(-1, 1)
+        idx, wt = torch.empty(65536, 1, dtype=torch.int32, device=DEV), torch.empty(65536, 1, device=DEV)
+        lib.gate_topk(g, zd, idx, wt)
+        u = -np.clip(z, f4(-80), f4(80))
+        n = (u * f4(float.fromhex("0x1.715476p0")) + f4(1.5 * 2 ** 23)) - f4(1.5 * 2 ** 23)
+        r = (u - n * f4(float.fromhex("0x1.62e400p-1"))) - n * f4(float.fromhex("0x1.7f7d1cp-20"))
+        p = np.full_like(r, f4(float.fromhex("0x1.6c16c2p-10")))
+        for c in ("0x1.111112p-7", "0x1.555556p-5", "0x1.555556p-3", "0x1p-1", "0x1p0", "0x1p0"):
+            p = p * r + f4(float.fromhex(c))
+        want = f4(1) / (f4(1) + np.ldexp(p, n.astype(np.int32)))
+        assert (idx == 0).all()
+        assert np.array_equal(wt.cpu().numpy().ravel().view(np.uint32), want.view(np.uint32))
+
+
+@gpu
+def test_equal_values_in_one_lane_and_across():
+    """Few distinct logits: every round has equals in a lane's slots, in other lanes and in other groups."""
+    rng = np.random.default_rng(12)
+    for E, G, KG in ((384, 8, 3), (384, 1, 1), (96, 3, 2), (1000, 40, 7), (256, 4, 2)):
+        z = rng.integers(0, 4, (24, E)).astype(f4)
+        z[:6] += (rng.random((6, E)) < 0.02).astype(f4) * rng.random((6, E)).astype(f4)  # a few that are unique
+        for dtype in (torch.float32, torch.bfloat16):
+            for bias in (None, (rng.integers(0, 3, E) / 4).astype(f4)):
+                check(torch.from_numpy(z).to(dtype), 12, "sigmoid", G, KG, "top2", True, 1.0, bias)
+
+
+@gpu
 def test_streams_and_graph_replays():
     rng = np.random.default_rng(9)
     z = torch.from_numpy(rng.standard_normal((300, 100)).astype(f4)).to(DEV)
