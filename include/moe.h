@@ -523,8 +523,12 @@ int moe_gate_topk(const moe_gate* G, const void* z, int32_t z_dtype, int64_t z_s
  *
  * Products are summed in fp32: the dot products of one block of 128 on the
  * matrix units, then one fused multiply-add per block with the product of
- * the two scales.  A code or scale that is not a number makes the outputs
- * that it enters NaN.  Identical inputs give bitwise identical outputs.
+ * the two scales.  One exception: bf16 outputs of moe_blockscale_matmul with
+ * M > 32 and K >= 1024 take the dot products from the E4M3 matrix steps,
+ * which keep 14 bits below the largest of each 8 products (1.4e-5 of a
+ * typical dot product, where the output's own rounding is 2e-3).  A code or
+ * scale that is not a number makes the outputs that it enters NaN.
+ * Identical inputs give bitwise identical outputs.
  *
  * Limits: K (inputs) a multiple of 16 in [16, 16384]; N (outputs) in [1,
  * 65536] with N * K < 2^31; M in [0, 2^20] rows; q pointers 16-byte aligned,
@@ -581,7 +585,8 @@ int moe_blockscale_gateup(const uint8_t* xq, const float* xs, int32_t T, int32_t
  * and routes with pos = T*k (no place) add nothing; add [T][d] is nullable
  * (no term) and may be y itself.  hq [T*k][f], hs [T*k][ceil(f/128)]; w_down
  * [E][d][f] with scales [E][ceil(d/128)][ceil(f/128)]; y fp32 [T][d].
- * Workspace: moe_blockscale_down_workspace_bytes of the same T, k, d.
+ * Workspace: moe_blockscale_down_workspace_bytes of the same T, k, d (null
+ * if that is 0, as it is for one token): the routes' products in fp32.
  */
 int moe_blockscale_down_workspace_bytes(int32_t T, int32_t k, int32_t d, size_t* bytes);
 int moe_blockscale_down(const uint8_t* hq, const float* hs, int32_t T, int32_t k,

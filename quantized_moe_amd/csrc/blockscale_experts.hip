@@ -180,7 +180,7 @@ __global__ __launch_bounds__(256) void bs_combine_kernel(BsDown a) {
   if (a.add) y = reinterpret_cast<const f32x4_t*>(a.add)[i];
   for (int j = 0; j < a.k; j++) {
     const int p = a.pos[t * a.k + j];
-    if (p >= a.T * a.k) continue;  // a route without a place
+    if ((uint32_t)p >= (uint32_t)(a.T * a.k)) continue;  // a route without a place
     const float w = a.wt[t * a.k + j];
     const f32x4_t v = reinterpret_cast<const f32x4_t*>(a.ye)[(int64_t)p * d4 + c];
 #pragma unroll

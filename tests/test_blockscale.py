@@ -224,6 +224,25 @@ def test_matmul_nan_codes_and_scales_stay_in_their_rows():
     assert torch.equal(torch.isnan(y.cpu()), bad)
 
 
+@gpu
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,N,K", [(12, 300, 1040), (30, 300, 1040), (300, 600, 1040), (70, 500, 8208), (900, 1100, 2064),
+                                   (1100, 4100, 1040), (3500, 3900, 1040)])
+def test_matmul_nan_in_every_variant(M, N, K, out):
+    rng = np.random.default_rng(M)
+    (xq, xs), (wq, ws) = make_rows(rng, M, K), make_weight(rng, N, K)
+    xq.view(torch.uint8)[3, 1030] = 0x7f
+    xq.view(torch.uint8)[M - 1, 0] = 0xff
+    wq.view(torch.uint8)[150, K - 1] = 0xff
+    xs[7, 1] = float("nan")
+    y = torch.empty(M, N, dtype=out, device=DEV)
+    work = torch.empty(max(16, lib.blockscale_matmul_workspace_bytes(M, N, K)), dtype=torch.uint8, device=DEV)
+    lib.blockscale_matmul(up(xq), up(xs), up(wq), up(ws), y, work)
+    bad = torch.zeros(M, N, dtype=torch.bool)
+    bad[3], bad[7], bad[M - 1], bad[:, 150] = True, True, True, True
+    assert torch.equal(torch.isnan(y.cpu()), bad)
+
+
 # ----------------------------------------------------------------- experts ----
 EXPERTS = [
     # T, k, E, d, f, share of routes without an expert
