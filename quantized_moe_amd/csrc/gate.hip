@@ -4,6 +4,7 @@
 #include <math.h>
 
 #include <type_traits>
+#include <utility>
 
 #include "common.hpp"
 #include "kernels.hpp"
@@ -45,6 +46,11 @@ __device__ __forceinline__ float vmax3(float a, float b, float c) {
   asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
   return d;
 }
+__device__ __forceinline__ float vmed3(float a, float b, float c) {
+  float d;
+  asm("v_med3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
+  return d;
+}
 template <int N>
 __device__ __forceinline__ float max_of(const float (&v)[N]) {
   float b = v[0];
@@ -67,6 +73,17 @@ __device__ __forceinline__ float recip_exact(float x) {
 // The same bits as sigmoid32 (topk.hpp).
 __device__ __forceinline__ float sigmoid_score(float z) {
   return recip_exact(1.0f + exp32(-__builtin_amdgcn_fmed3f(z, -80.0f, 80.0f)));
+}
+
+// sigmoid_score within 2^-21: four instructions (two of them at a quarter of
+// the rate) where the exact steps take some 26.  Its argument's rounding moves
+// it by |z| s (1 - s) 2^-23 <= 2^-25, the exponential by s (1 - s) 2^-23, the
+// sum and the reciprocal by 2^-24 and 2^-23; the exact steps err by less than
+// 2^-22.
+__device__ __forceinline__ float sigmoid_near(float z) {
+  float s;  // (written out with the wait that other written-out instructions need after a reciprocal)
+  asm("v_rcp_f32 %0, %1\n\ts_nop 0" : "=v"(s) : "v"(1.0f + __builtin_amdgcn_exp2f(z * -0x1.715476p+0f)));
+  return s;
 }
 
 // Maximum over the wave, the same in every lane.  Lanes that a step's shift
@@ -108,23 +125,31 @@ __device__ __forceinline__ float read_lane(float v, int lane) {
 }
 __device__ __forceinline__ bool in_lanes(uint64_t mask) { return __builtin_amdgcn_inverse_ballot_w64(mask); }
 
+// f(0), f(1), ... as constants, until one is false.
+template <class F, int... R>
+__device__ __forceinline__ void each_until(F&& f, std::integer_sequence<int, R...>) {
+  (void)(f(std::integral_constant<int, R>{}) && ...);
+}
+
 // A wave per token, four tokens per block; everything stays in registers.
 //
 // P = 2^LG lanes hold a group (all 64 the one group when no groups are chosen):
 // lane g P + p has experts g EG + p + P i, i < SLOTS, EG = E / groups.  A
 // group's two best are then a butterfly over its lanes, its rank a count over
-// the groups' values, and an expert that is out is a -inf in its slot.  Each
-// round of the top-k takes the wave maximum of the lanes' maxima (6 DPP steps)
-// and compares every slot with it.  Nearly always one slot of one lane has it:
-// the comparisons' lane masks, which are scalars, show that, clear the slot and
-// name the lane; which slot it was, lane r finds for round r at the end, all
-// rounds at once.  Equal values take the scalar search for the lowest index
-// (group, slot, lane).  Only what orders the experts is computed for all of
-// them; the chosen ones' scores are taken at the end.
+// the groups' values, and an expert that is out is a -inf in its slot.
 //
-// Bound by vector instructions: about 30 a score and 25 a round and token.
-// Measured: 65536 tokens, 384 experts in 8 groups with a bias 59 us (100 MB of
-// logits: 21 us at a large copy's rate), 1 token 4.6 us.
+// Only what orders the experts is computed for all of them, and that first to
+// within a known error: a sigmoid in 4 instructions for the exact steps' 26, and
+// the value's lowest bits give way to its slot's number, so that a lane's values
+// are distinct and can be sorted.  If the groups that are kept and the best k + 1
+// values lie further apart than the errors, this is the exact scores' order; if
+// not (one token of some hundred), the token is done again with exact values.
+// The chosen experts' scores are always the exact steps'.
+//
+// Bound by vector instructions, 380 a token at 384 experts (100 in the 7 rounds,
+// 42 the scores, 24 the exact scores of the chosen).  Measured: 65536 tokens, 384
+// experts in 8 groups with a bias 43 us (60 us with exact values throughout; 100
+// MB of logits take 21 us at a large copy's rate); 1 token 5.2 us a call.
 //
 // FULL: every lane has an expert in every slot.
 template <int SLOTS, int ZDT, int LG, bool FULL>  // LG < 0: any other number of lanes
@@ -143,10 +168,10 @@ __global__ __launch_bounds__(256) void gate_kernel(GateLaunch a, int lg_, int gr
   using Z = typename std::conditional<ZDT == X_BF16, uint16_t, float>::type;
   const Z* zrow = static_cast<const Z*>(a.z) + (int64_t)t * a.z_stride;
   const uint32_t at = n_own > 0 ? e0 : 0;
-  float z[SLOTS], bias[SLOTS] = {};
+  float z[SLOTS], bias[SLOTS];
 #pragma unroll
   for (int i = 0; i < SLOTS; i++) {
-    const Z v = zrow[i < n_own ? at + P * i : at];
+    const Z v = FULL ? zrow[at + (int64_t)(P * i)] : zrow[i < n_own ? at + P * i : at];
     if constexpr (ZDT == X_BF16)
       z[i] = bf16_bits_to_float(v);
     else
@@ -154,11 +179,16 @@ __global__ __launch_bounds__(256) void gate_kernel(GateLaunch a, int lg_, int gr
   }
   if (a.bias) {  // (requested with the logits: one wait)
 #pragma unroll
-    for (int i = 0; i < SLOTS; i++) bias[i] = a.bias[i < n_own ? at + P * i : at];
+    for (int i = 0; i < SLOTS; i++) bias[i] = FULL ? a.bias[at + (int64_t)(P * i)] : a.bias[i < n_own ? at + P * i : at];
   }
 #pragma unroll
   for (int i = 0; i < SLOTS; i++)  // (false for NaN)
-    z[i] = i < n_own && z[i] > -0x1p127f ? vmin(z[i], 3.402823466e38f) : -INFINITY;
+    z[i] = i < n_own && z[i] > -0x1p127f ? z[i] : -INFINITY;
+  const bool plain = !(a.bias || top2);  // the values are the logits
+  if (plain || a.score == MOE_SCORE_SOFTMAX) {  // (sigmoid scores are the same)
+#pragma unroll
+    for (int i = 0; i < SLOTS; i++) z[i] = vmin(z[i], 3.402823466e38f);
+  }
 
   float m = 0.0f, total = 1.0f;  // softmax: the largest logit, the sum of the terms
   // a masked expert's term is 0 and its -inf stays
@@ -184,109 +214,257 @@ __global__ __launch_bounds__(256) void gate_kernel(GateLaunch a, int lg_, int gr
     }
     total = fold64(part);
   }
-  if (a.bias || top2) {
-    if (a.score == MOE_SCORE_SIGMOID) {
-#pragma unroll
-      for (int i = 0; i < SLOTS; i++) v[i] = sigmoid_score(z[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < SLOTS; i++) v[i] = v[i] / total;
-    }
-    if (a.bias) {
-#pragma unroll
-      for (int i = 0; i < SLOTS; i++) v[i] = vmax(v[i] + bias[i], -INFINITY);  // (NaN to -inf)
-    }
-#pragma unroll
-    for (int i = 0; i < SLOTS; i++) v[i] = z[i] > -INFINITY ? v[i] : -INFINITY;
-  } else {
-#pragma unroll
-    for (int i = 0; i < SLOTS; i++) v[i] = z[i];
-  }
-
-  if (pick_groups) {
-    float b1 = v[0], b2 = -INFINITY;
-#pragma unroll
-    for (int i = 1; i < SLOTS; i++) {
-      b2 = vmax(b2, vmin(b1, v[i]));
-      b1 = vmax(b1, v[i]);
-    }
-    auto merge = [&](float c1, float c2) {  // with another lane's two best
-      b2 = vmax3(b2, c2, vmin(b1, c1));
-      b1 = vmax(b1, c1);
-    };
+  int my_lane = -1, my_slot = -1;  // round `lane`'s expert
+  float my_v;
+  // (b1, b2), a lane's two best, to those of its group
+  auto merge_lanes = [&](float& b1, float& b2) __attribute__((always_inline)) {
     if constexpr (LG == 3) {
-      merge(dpp<0xb1>(b1), dpp<0xb1>(b2));    // quad_perm 1 0 3 2
-      merge(dpp<0x4e>(b1), dpp<0x4e>(b2));    // quad_perm 2 3 0 1
-      merge(dpp<0x141>(b1), dpp<0x141>(b2));  // row_half_mirror: the other quad
+      float t;
+#define QMOE_MERGE(STEP)                                                                                           \
+  asm("s_nop 1\n\tv_min_f32_dpp %0, %1, %1 " STEP " row_mask:0xf bank_mask:0xf\n\t"                                 \
+      "v_max_f32_dpp %1, %1, %1 " STEP " row_mask:0xf bank_mask:0xf\n\t"                                           \
+      "v_max_f32_dpp %2, %2, %2 " STEP " row_mask:0xf bank_mask:0xf"                                               \
+      : "=&v"(t), "+v"(b1), "+v"(b2));                                                                             \
+  b2 = vmax(b2, t);
+      QMOE_MERGE("quad_perm:[1,0,3,2]")
+      QMOE_MERGE("quad_perm:[2,3,0,1]")
+      QMOE_MERGE("row_half_mirror")  // the other quad
+#undef QMOE_MERGE
     } else {
-      for (int s = 1; s < P; s <<= 1) merge(__shfl_xor(b1, s, 64), __shfl_xor(b2, s, 64));
+      for (int s = 1; s < P; s <<= 1) {
+        const float c1 = __shfl_xor(b1, s, 64), c2 = __shfl_xor(b2, s, 64);
+        b2 = vmax3(b2, c2, vmin(b1, c1));
+        b1 = vmax(b1, c1);
+      }
     }
-    if (top2 && b2 > -INFINITY) b1 = b1 + b2;
-    int before = 0;  // groups that come before this lane's
-    for (int h = 0; h < G; h++) {
-      const float c = read_lane(b1, h << lg);
-      const int later = (h + 1) << lg;  // lanes of the groups after h: an equal value comes before theirs
-      const uint64_t tied = later < 64 ? __ballot(c >= b1) & (~0ull << later) : 0;
-      before += in_lanes(tied | __ballot(c > b1));
+  };
+  // Keys within near_err of the values, their lowest bits the slot: distinct in
+  // a lane, whose QUEUE largest are sorted once, so that a round is the wave
+  // maximum of the lanes' first and a step of one lane's queue.  False if the
+  // keys do not decide the order, or a lane's queue runs out.
+  // bf16 logits that are the values themselves have room for the expert's number
+  // (the lower first of equal ones): such keys are the exact order.
+  constexpr int SB = SLOTS <= 4 ? 4 : SLOTS <= 8 ? 8 : SLOTS <= 16 ? 16 : 32;  // slot numbers
+  constexpr int QUEUE = 4;
+  static_assert(SLOTS >= QUEUE, "every place is filled");
+  // 2^-21 of a score, (SB + 1) 2^-23 |v| of its sum's rounding and the slot's
+  // bits; a number also for -inf
+  auto near_err = [](float x) {
+    return (SB <= 16 ? 0x1p-18f : 0x1p-17f) * vmin(vmax(__builtin_fabsf(x), 1.0f), 3.402823466e38f);
+  };
+  const bool ordered = ZDT == X_BF16 && plain;
+  auto select_near = [&]() __attribute__((always_inline)) -> bool {
+    float key[SLOTS], q[QUEUE];
+    if (plain) {
+#pragma unroll
+      for (int i = 0; i < SLOTS; i++) key[i] = z[i];
+    } else {
+      if (a.score == MOE_SCORE_SIGMOID) {
+#pragma unroll
+        for (int i = 0; i < SLOTS; i++) key[i] = sigmoid_near(z[i]);
+      } else {
+        const float r = __builtin_amdgcn_rcpf(total);
+#pragma unroll
+        for (int i = 0; i < SLOTS; i++) key[i] = v[i] * r;
+      }
+      if (a.bias) {  // (NaN to -inf)
+#pragma unroll
+        for (int i = 0; i < SLOTS; i++) key[i] = vmed3(key[i] + bias[i], -INFINITY, 3.402823466e38f);
+      }
     }
-#pragma unroll
-    for (int i = 0; i < SLOTS; i++) v[i] = before < a.top_groups ? v[i] : -INFINITY;
-  }
-
-  float left[SLOTS];  // v without the chosen
-#pragma unroll
-  for (int i = 0; i < SLOTS; i++) left[i] = v[i];
-  int my_lane = -1, my_slot = -1;  // round `lane`'s expert, the slot if it is known
-  float my_v = 0.0f;
-  // a value was there twice: what is left of it is no sign of its slot any more
-  // (bf16 logits often are: they are searched without looking)
-  bool equals = ZDT == X_BF16;
-  for (int r = 0; r < a.k; r++) {
-    const float b = wave_fmax(max_of(left));
-    if (__float_as_uint(b) == 0xff800000u) break;  // (never NaN)
-    uint64_t has[SLOTS], any = 0, twice = 0;
 #pragma unroll
     for (int i = 0; i < SLOTS; i++) {
-      has[i] = __ballot(left[i] == b);  // (-0 == +0)
-      twice |= any & has[i];
-      any |= has[i];
+      const bool in = vmin(key[i], z[i]) > -INFINITY;
+      uint32_t b = __float_as_uint(key[i]);
+      if (ordered) {
+        b = __float_as_uint(key[i] + 0.0f);  // (-0 is 0)
+        const uint32_t e = e0 + P * i;
+        b = (b & ~1023u) | ((int)b < 0 ? e : 1023u - e);
+      } else {
+        b = (b & ~(SB - 1u)) | i;
+      }
+      key[i] = in ? __uint_as_float(b) : -INFINITY;
     }
-    int l = __builtin_ctzll(any);
-    const bool mine = in_lanes(1ull << r);
-    equals |= twice != 0 || (any & (any - 1)) != 0;
-    if (!equals) {
+    q[0] = key[0];
 #pragma unroll
-      for (int i = 0; i < SLOTS; i++) left[i] = in_lanes(has[i]) ? -INFINITY : left[i];
+    for (int j = 1; j < QUEUE; j++) q[j] = -INFINITY;
+#pragma unroll
+    for (int i = 1; i < SLOTS; i++) {  // into its place of the sorted queue
+#pragma unroll
+      for (int j = min(i, QUEUE - 1); j > 0; j--) q[j] = j == i ? vmin(q[j - 1], key[i]) : vmed3(q[j - 1], q[j], key[i]);
+      q[0] = vmax(q[0], key[i]);
+    }
+    if (pick_groups) {
+      float b1 = q[0], b2 = QUEUE > 1 ? q[1] : -INFINITY;
+      merge_lanes(b1, b2);
+      float err = ordered ? 0.0f : near_err(b1);
+      if (top2 && b2 > -INFINITY) {
+        err = err + near_err(b2);
+        b1 = b1 + b2;
+      }
+      const float most = b1 + err, least = b1 - err;
+      int before = -1;  // groups that may come before this lane's (not itself)
+      if constexpr (LG == 3) {  // each of a group's 8 lanes compares it with another one
+        const uint64_t m = __ballot(__shfl(most, p << 3, 64) >= least);
+        before += __builtin_popcount((uint32_t)(m >> (g << 3)) & 0xffu);
+      } else {
+        for (int h = 0; h < G; h++) before += in_lanes(__ballot(read_lane(most, h << lg) >= least));
+      }
+      const bool kept = before < a.top_groups;
+      if (!ordered && __popcll(__ballot(kept)) != a.top_groups << lg) return false;
+#pragma unroll
+      for (int j = 0; j < QUEUE; j++) q[j] = kept ? q[j] : -INFINITY;
+    }
+    my_lane = my_slot = -1;
+    my_v = -INFINITY;
+    uint64_t taken[QUEUE + 1] = {};  // lanes that have given that many
+    const int rounds = ordered ? a.k : a.k + 1;
+    bool decided = true;
+    auto round = [&](auto rc) __attribute__((always_inline)) -> bool {
+      constexpr int r = decltype(rc)::value;
+      if (r >= rounds) return false;
+      const uint32_t b = __float_as_uint(wave_fmax(q[0]));
+      if (b == 0xff800000u) return false;
+      const uint64_t has = __ballot(__float_as_uint(q[0]) == b);
+      uint64_t not_one = has & (has - 1);
+      if constexpr (SLOTS > QUEUE) {
+        not_one |= taken[QUEUE - 1] & has;
+#pragma unroll
+        for (int j = QUEUE - 1; j > 0; j--) taken[j] |= j == 1 ? has : taken[j - 1] & has;
+      }
+      decided = not_one == 0;
+      if (!decided) return false;
+      // (two wait states from a comparison or a read lane to these)
+      asm("s_nop 1\n\t"
+          "v_cndmask_b32 %0, %0, %1, %6\n\tv_cndmask_b32 %1, %1, %2, %6\n\t"
+          "v_cndmask_b32 %2, %2, %3, %6\n\tv_cndmask_b32 %3, %3, %9, %6\n\t"
+          "v_writelane_b32 %4, %7, %8\n\tv_writelane_b32 %5, %10, %8"
+          : "+v"(q[0]), "+v"(q[1]), "+v"(q[2]), "+v"(q[3]), "+v"(my_v), "+v"(my_lane)
+          : "s"(has), "s"(b), "n"(r), "v"(-INFINITY), "s"((int)__builtin_ctzll(has)));
+      return true;
+    };
+    each_until(round, std::make_integer_sequence<int, TOPK_MAX_K + 1>{});
+    if (!decided) return false;
+    if (ordered) {
+      const uint32_t b = __float_as_uint(my_v) & 1023u;
+      const int e = (int)__float_as_uint(my_v) < 0 ? b : 1023u - b;
+      my_slot = (e - (my_lane >> lg) * EG) >> lg;
     } else {
-      const int first = l >> lg;  // the lowest group
-      const uint64_t lanes = (~0ull >> (64 - P)) << (first << lg);
-      uint64_t in_slot = 0;
-      int slot = 0;
-#pragma unroll
-      for (int i = SLOTS - 1; i >= 0; i--)
-        if (has[i] & lanes) {
-          slot = i;
-          in_slot = has[i] & lanes;
-        }
-      l = __builtin_ctzll(in_slot);
-#pragma unroll
-      for (int i = 0; i < SLOTS; i++) left[i] = slot == i && lane == l ? -INFINITY : left[i];
-      my_slot = mine ? slot : my_slot;
+      const float next = __shfl_down(my_v, 1, 64);  // each of the k against the next
+      const bool apart = my_lane < 0 || my_v - next > near_err(my_v) + near_err(next);
+      if (__ballot(lane < a.k && !apart)) return false;
+      my_slot = __float_as_uint(my_v) & (SB - 1u);
     }
-    my_lane = mine ? l : my_lane;
-    my_v = mine ? b : my_v;
-  }
-  // The slot (where it was the only one with that value) and the logit.
+    return true;
+  };
+  // Any values: each round compares every slot with the wave's largest.  Nearly
+  // always one slot of one lane has it: the comparisons' lane masks, which are
+  // scalars, show that, clear the slot and name the lane; which slot it was, lane
+  // r finds for round r at the end, all rounds at once.  Equal values take the
+  // scalar search for the lowest index (group, slot, lane).
+  auto select_any = [&]() __attribute__((always_inline)) {
+    if (!plain) {
+      if (a.score == MOE_SCORE_SIGMOID) {
+#pragma unroll
+        for (int i = 0; i < SLOTS; i++) v[i] = sigmoid_score(z[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < SLOTS; i++) v[i] = v[i] / total;
+      }
+      if (a.bias) {
+#pragma unroll
+        for (int i = 0; i < SLOTS; i++) v[i] = vmax(v[i] + bias[i], -INFINITY);  // (NaN to -inf)
+      }
+#pragma unroll
+      for (int i = 0; i < SLOTS; i++) v[i] = z[i] > -INFINITY ? v[i] : -INFINITY;
+    } else {
+#pragma unroll
+      for (int i = 0; i < SLOTS; i++) v[i] = z[i];
+    }
+
+    if (pick_groups) {
+      float b1 = v[0], b2 = -INFINITY;
+#pragma unroll
+      for (int i = 1; i < SLOTS; i++) {
+        b2 = vmax(b2, vmin(b1, v[i]));
+        b1 = vmax(b1, v[i]);
+      }
+      merge_lanes(b1, b2);
+      if (top2 && b2 > -INFINITY) b1 = b1 + b2;
+      int before = 0;  // groups that come before this lane's
+      for (int h = 0; h < G; h++) {
+        const float c = read_lane(b1, h << lg);
+        const int later = (h + 1) << lg;  // lanes of the groups after h: an equal value comes before theirs
+        const uint64_t tied = later < 64 ? __ballot(c >= b1) & (~0ull << later) : 0;
+        before += in_lanes(tied | __ballot(c > b1));
+      }
+#pragma unroll
+      for (int i = 0; i < SLOTS; i++) v[i] = before < a.top_groups ? v[i] : -INFINITY;
+    }
+
+    float left[SLOTS];  // v without the chosen
+#pragma unroll
+    for (int i = 0; i < SLOTS; i++) left[i] = v[i];
+    my_lane = my_slot = -1;
+    my_v = -INFINITY;
+    // a value was there twice: what is left of it is no sign of its slot any more
+    // (bf16 logits often are: they are searched without looking)
+    bool equals = ZDT == X_BF16;
+    for (int r = 0; r < a.k; r++) {
+      const float b = wave_fmax(max_of(left));
+      if (__float_as_uint(b) == 0xff800000u) break;  // (never NaN)
+      uint64_t has[SLOTS], any = 0, twice = 0;
+#pragma unroll
+      for (int i = 0; i < SLOTS; i++) {
+        has[i] = __ballot(left[i] == b);  // (-0 == +0)
+        twice |= any & has[i];
+        any |= has[i];
+      }
+      int l = __builtin_ctzll(any);
+      const bool mine = in_lanes(1ull << r);
+      equals |= twice != 0 || (any & (any - 1)) != 0;
+      if (!equals) {
+#pragma unroll
+        for (int i = 0; i < SLOTS; i++) left[i] = in_lanes(has[i]) ? -INFINITY : left[i];
+      } else {
+        const int first = l >> lg;  // the lowest group
+        const uint64_t lanes = (~0ull >> (64 - P)) << (first << lg);
+        uint64_t in_slot = 0;
+        int slot = 0;
+#pragma unroll
+        for (int i = SLOTS - 1; i >= 0; i--)
+          if (has[i] & lanes) {
+            slot = i;
+            in_slot = has[i] & lanes;
+          }
+        l = __builtin_ctzll(in_slot);
+#pragma unroll
+        for (int i = 0; i < SLOTS; i++) left[i] = slot == i && lane == l ? -INFINITY : left[i];
+        my_slot = mine ? slot : my_slot;
+      }
+      my_lane = mine ? l : my_lane;
+      my_v = mine ? b : my_v;
+    }
+    const int from = my_lane < 0 ? lane : my_lane;
+#pragma unroll
+    for (int i = 0; i < SLOTS; i++) {
+      const float vi = __shfl(v[i], from, 64);
+      if (my_slot < 0 && my_lane >= 0 && vi == my_v) my_slot = i;
+    }
+  };
+  // Queues do not last where fewer lanes are left than rounds: 32768 tokens, 16 of
+  // 1024 experts in one of 8 groups 96 us without and 119 us with them; 16 of 512
+  // in one of 4 groups (16 lanes) 57 and 55 us, 8 of 384 in 2 of 8 groups 31 and
+  // 23 us, 6 of 384 by bf16 logits' sums, where ties are common, 38 and 32 us.
+  const int lanes_kept = (pick_groups ? a.top_groups : 1) << lg;
+  const bool try_near = SLOTS <= QUEUE || a.k <= lanes_kept;
+  if (!try_near || !select_near()) select_any();
   float my_z = -INFINITY;
   const int from = my_lane < 0 ? lane : my_lane;
 #pragma unroll
   for (int i = 0; i < SLOTS; i++) {
-    const float vi = __shfl(v[i], from, 64), zi = __shfl(z[i], from, 64);
-    const bool is = my_slot < 0 ? vi == my_v : my_slot == i;
-    if (is && my_lane >= 0) {
-      my_slot = i;
-      my_z = zi;
-    }
+    const float zi = __shfl(z[i], from, 64);
+    my_z = my_slot == i ? zi : my_z;
   }
   const int my_e = my_lane < 0 ? -1 : (my_lane >> lg) * EG + (my_lane & (P - 1)) + P * my_slot;
   const float chosen = a.score == MOE_SCORE_SIGMOID ? sigmoid_score(my_z) : term(my_z) / total;

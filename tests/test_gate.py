@@ -244,6 +244,40 @@ def test_equal_values_in_one_lane_and_across():
 
 
 @gpu
+@pytest.mark.parametrize("E,k,G,KG", [(384, 6, 8, 4), (384, 6, 1, 1), (256, 8, 8, 4), (100, 4, 10, 6), (1024, 16, 1, 1),
+                                      (1024, 8, 4, 2), (48, 3, 3, 2)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_values_a_few_units_apart(E, k, G, KG, score):
+    """Values that differ by a few of their last bits, in a token's best, its groups or both; biases of every size."""
+    rng = np.random.default_rng(E + k + G)
+    base = rng.integers(-2, 3, (20, E)).astype(f4)
+    z = (base * (1 + rng.integers(-3, 4, (20, E)) * f4(2.0 ** -23))).astype(f4)
+    z[10:] += (rng.random((10, E)) * 1e-5).astype(f4)
+    tiny = (rng.integers(-4, 5, E) * 2.0 ** -24).astype(f4)
+    for bias in (None, tiny, tiny + f4(1000.0), (rng.choice([-1e6, 1e6], E) + rng.random(E)).astype(f4),
+                 rng.choice([3e38, -3e38, 2e30, 1.0, math.inf, -math.inf], E).astype(f4),
+                 (rng.standard_normal(E) * 1e-3).astype(f4)):
+        for gs in ("max", "top2"):
+            check(torch.from_numpy(z), k, score, G, KG, gs, True, 1.0, bias)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_best_experts_crowd_in_one_place(dtype):
+    """The best values at distances of 8, 16, 32 and 64 experts, the ones that share registers."""
+    rng = np.random.default_rng(14)
+    for E, k, G, KG in ((384, 6, 1, 1), (1024, 16, 1, 1), (384, 6, 8, 4), (1000, 8, 2, 1), (960, 5, 8, 5)):
+        z = (0.01 * rng.standard_normal((24, E))).astype(f4)
+        for t in range(24):
+            step = (8, 16, 32, 64)[t % 4]
+            at = np.arange(rng.integers(0, step), E, step)
+            at = at[: rng.integers(3, 9)]
+            z[t, at] += 2 + 0.25 * rng.permutation(len(at)).astype(f4)
+        for bias in (None, (0.01 * rng.standard_normal(E)).astype(f4)):
+            check(torch.from_numpy(z).to(dtype), k, "sigmoid", G, KG, "max", True, 1.0, bias)
+
+
+@gpu
 def test_streams_and_graph_replays():
     rng = np.random.default_rng(9)
     z = torch.from_numpy(rng.standard_normal((300, 100)).astype(f4)).to(DEV)
