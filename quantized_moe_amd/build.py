@@ -1,8 +1,10 @@
-"""Build libqmoe.so (the HIP library) in-tree for gfx950.
+"""Build libqmoe.so (the HIP library) in-tree for gfx950, and the Python calls on it.
 
 Each .hip source is compiled separately (the router and gate files with
 floating-point contraction off, so their fixed fp32 steps are exactly what the
 source says), then linked into one shared library next to this file.
+_calls.so, the Python module of the gate and block-scaled operators, is host
+code that reads torch tensors and calls that library.
 """
 from __future__ import annotations
 
@@ -10,12 +12,14 @@ import concurrent.futures
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libqmoe.so")
 PROBE_OUT = os.path.join(HERE, "libqmoe_probe.so")  # measurement probes (not the layer's ABI)
+CALLS_OUT = os.path.join(HERE, "_calls.so")
 OBJ = os.path.join(HERE, "_build")
 ARCH = "gfx950"
 
@@ -53,14 +57,43 @@ def _link(objs, out, libs=()):
     os.replace(tmp, out)
 
 
+def _compile_calls() -> str:
+    import torch
+
+    t = os.path.dirname(torch.__file__)
+    obj = os.path.join(OBJ, "calls.o")
+    cmd = ["g++", "-c", os.path.join(CSRC, "calls.cpp"), "-o", obj, "-O2", "-std=c++17", "-fPIC", "-Wall",
+           "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(t, "include"), "-isystem", "/opt/rocm/include",
+           "-isystem", sysconfig.get_path("include")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for calls.cpp:\n" + r.stdout + r.stderr)
+    return obj
+
+
+def _link_calls(obj: str) -> None:
+    import torch
+
+    tmp = CALLS_OUT + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", HERE, "-l:libqmoe.so", "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
+    os.replace(tmp, CALLS_OUT)
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(OBJ, exist_ok=True)
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(10, os.cpu_count() or 1)) as ex:
+        calls = ex.submit(_compile_calls)
         objs = list(ex.map(_compile, SOURCES + PROBE_SOURCES))
     _link(objs[:len(SOURCES)], OUT, LIBS)
     _link(objs[len(SOURCES):], PROBE_OUT)
+    _link_calls(calls.result())
     if verbose:
-        print(f"built {OUT} and {PROBE_OUT}")
+        print(f"built {OUT}, {PROBE_OUT} and {CALLS_OUT}")
     return OUT
 
 

@@ -241,18 +241,31 @@ _SCORES = {"sigmoid": MOE_SCORE_SIGMOID, "softmax": MOE_SCORE_SOFTMAX}
 _GROUP_SCORES = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2_SUM}
 
 
-_F32, _BF16, _I32T, _U8, _E4M3 = torch.float32, torch.bfloat16, torch.int32, torch.uint8, torch.float8_e4m3fn
+_calls = None
 
 
-def _is(t, dtype, shape) -> bool:
-    """What the C call takes for granted about a tensor's storage: its dtype,
-    its size, no gaps.  Codes (dtype uint8) may be float8_e4m3fn."""
-    d = t.dtype
-    return (d is dtype or (dtype is _U8 and d is _E4M3)) and t.shape == shape and t.is_contiguous()
+def _load_calls():
+    """The compiled calls (csrc/calls.cpp): they check their tensors and give
+    the status, or None if a tensor is not as the call needs it; the functions
+    below then say which."""
+    global _calls
+    lib()
+    if not os.path.exists(os.path.join(_HERE, "_calls.so")):
+        raise RuntimeError(f"{_HERE}/_calls.so is not built; run __graft_entry__.build() first")
+    from . import _calls as module
+    _calls = module
+    return module
+
+
+def _not_on_gpu(fn: str, workspace=None) -> None:
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError(f"{fn}: the workspace must be contiguous")
+    raise ValueError(f"{fn}: every tensor must be in GPU memory")
 
 
 def _need(fn: str, **tensors) -> None:
-    """Raises for the first (tensor, dtype, shape) that is not as _is() asks."""
+    """Raises for the first (tensor, dtype, shape) whose storage is not as the C
+    call takes it: the dtype (codes, uint8, may be float8_e4m3fn), the size, no gaps."""
     for name, (t, dtype, shape) in tensors.items():
         if t.dtype != dtype and not (dtype == torch.uint8 and t.dtype == torch.float8_e4m3fn):
             raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
@@ -304,30 +317,29 @@ def router_logits(w_router, x, z, stream=None) -> None:
 
 
 def gate_topk(gate: MoeGate, z, idx, wt, stream=None) -> None:
-    T, E = z.shape
-    k = gate.top_k
-    stride = _rows_of("gate_topk", "z", z, _XDT)
-    if E != gate.n_experts:
-        raise ValueError(f"gate_topk: z has {E} logits per row, the gate {gate.n_experts} experts")
-    if not (_is(idx, _I32T, (T, k)) and _is(wt, _F32, (T, k))):
-        _need("gate_topk", idx=(idx, torch.int32, (T, k)), wt=(wt, torch.float32, (T, k)))
-    rc = lib().moe_gate_topk(ctypes.byref(gate), z.data_ptr(), _XDT[z.dtype], stride, T, idx.data_ptr(), wt.data_ptr(),
-                             _stream(stream))
+    rc = (_calls or _load_calls()).gate_topk(gate, z, idx, wt, stream)
+    if rc is None:
+        T, E = z.shape
+        _rows_of("gate_topk", "z", z, _XDT)
+        if E != gate.n_experts:
+            raise ValueError(f"gate_topk: z has {E} logits per row, the gate {gate.n_experts} experts")
+        _need("gate_topk", idx=(idx, torch.int32, (T, gate.top_k)), wt=(wt, torch.float32, (T, gate.top_k)))
+        _not_on_gpu("gate_topk")
     if rc:
         _check(rc)
 
 
 def blockscale_quantize(x, q, s, stream=None) -> None:
     """x [M][K] to q (float8_e4m3fn or uint8) [M][K] and s [M][ceil(K / 128)]."""
-    fn = "blockscale_quantize"
-    ldx, ldq = _rows_of(fn, "x", x, _XDT), _rows_of(fn, "q", q, _F8)
-    M, K = x.shape
-    if q.shape != x.shape:
-        raise ValueError(f"{fn}: q has shape {tuple(q.shape)}, needs {tuple(x.shape)}")
-    if not _is(s, _F32, (M, (K + 127) // 128)):
+    rc = (_calls or _load_calls()).quantize(x, q, s, stream)
+    if rc is None:
+        fn = "blockscale_quantize"
+        _rows_of(fn, "x", x, _XDT), _rows_of(fn, "q", q, _F8)
+        M, K = x.shape
+        if q.shape != x.shape:
+            raise ValueError(f"{fn}: q has shape {tuple(q.shape)}, needs {tuple(x.shape)}")
         _need(fn, s=(s, torch.float32, (M, scale_blocks(K))))
-    rc = lib().moe_blockscale_quantize(x.data_ptr(), _XDT[x.dtype], ldx, M, K, q.data_ptr(), ldq, s.data_ptr(),
-                                       _stream(stream))
+        _not_on_gpu(fn)
     if rc:
         _check(rc)
 
@@ -341,17 +353,16 @@ def blockscale_matmul_workspace_bytes(M: int, N: int, K: int) -> int:
 def blockscale_matmul(xq, xs, wq, ws, y, workspace=None, stream=None) -> None:
     """y [M][N] (float32 or bfloat16) = xq [M][K] times wq [N][K] transposed,
     with scales xs [M][ceil(K / 128)] and ws [ceil(N / 128)][ceil(K / 128)]."""
-    fn = "blockscale_matmul"
-    ldx, ldy = _rows_of(fn, "xq", xq, _F8), _rows_of(fn, "y", y, _XDT)
-    (M, K), N = xq.shape, wq.shape[0]
-    KB, NB = (K + 127) // 128, (N + 127) // 128
-    if y.shape != (M, N):
-        raise ValueError(f"{fn}: y has shape {tuple(y.shape)}, needs {(M, N)}")
-    if not (_is(xs, _F32, (M, KB)) and _is(wq, _U8, (N, K)) and _is(ws, _F32, (NB, KB))):
+    rc = (_calls or _load_calls()).matmul(xq, xs, wq, ws, y, workspace, stream)
+    if rc is None:
+        fn = "blockscale_matmul"
+        _rows_of(fn, "xq", xq, _F8), _rows_of(fn, "y", y, _XDT)
+        (M, K), N = xq.shape, wq.shape[0]
+        KB, NB = scale_blocks(K), scale_blocks(N)
+        if y.shape != (M, N):
+            raise ValueError(f"{fn}: y has shape {tuple(y.shape)}, needs {(M, N)}")
         _need(fn, xs=(xs, torch.float32, (M, KB)), wq=(wq, torch.uint8, (N, K)), ws=(ws, torch.float32, (NB, KB)))
-    wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
-    rc = lib().moe_blockscale_matmul(xq.data_ptr(), ldx, xs.data_ptr(), M, wq.data_ptr(), ws.data_ptr(), N, K,
-                                     y.data_ptr(), _XDT[y.dtype], ldy, wp, wn, _stream(stream))
+        _not_on_gpu(fn, workspace)
     if rc:
         _check(rc)
 
@@ -359,21 +370,19 @@ def blockscale_matmul(xq, xs, wq, ws, y, workspace=None, stream=None) -> None:
 def blockscale_gateup(xq, xs, k, offsets, perm, w_gate, s_gate, w_up, s_up, hq, hs, stream=None) -> None:
     """hq [T*k][f], hs [T*k][ceil(f / 128)]: the bucket rows' silu(gate) * up,
     requantised; offsets and perm as bucket() writes them."""
-    fn = "blockscale_gateup"
-    (T, d), (E, f, _) = xq.shape, w_gate.shape
-    R, DB, FB = T * k, scale_blocks(d), scale_blocks(f)
-    if not (_is(xq, _U8, (T, d)) and _is(xs, _F32, (T, DB)) and _is(offsets, _I32T, (E + 1,))
-            and _is(perm, _I32T, (R,)) and _is(w_gate, _U8, (E, f, d)) and _is(s_gate, _F32, (E, FB, DB))
-            and _is(w_up, _U8, (E, f, d)) and _is(s_up, _F32, (E, FB, DB)) and _is(hq, _U8, (R, f))
-            and _is(hs, _F32, (R, FB))):
+    rc = (_calls or _load_calls()).gateup(xq, xs, k, offsets, perm, w_gate, s_gate, w_up, s_up, hq, hs, stream)
+    if rc is None:
+        fn = "blockscale_gateup"
+        (T, d), (E, f, _) = xq.shape, w_gate.shape
+        R, DB, FB = T * k, scale_blocks(d), scale_blocks(f)
         _need(fn, xq=(xq, torch.uint8, (T, d)), xs=(xs, torch.float32, (T, DB)),
               offsets=(offsets, torch.int32, (E + 1,)), perm=(perm, torch.int32, (R,)),
               w_gate=(w_gate, torch.uint8, (E, f, d)), s_gate=(s_gate, torch.float32, (E, FB, DB)),
               w_up=(w_up, torch.uint8, (E, f, d)), s_up=(s_up, torch.float32, (E, FB, DB)),
               hq=(hq, torch.uint8, (R, f)), hs=(hs, torch.float32, (R, FB)))
-    _check(lib().moe_blockscale_gateup(_ptr(xq), _ptr(xs), T, k, _ptr(offsets), _ptr(perm), E, _ptr(w_gate),
-                                       _ptr(s_gate), _ptr(w_up), _ptr(s_up), f, d, _ptr(hq), _ptr(hs),
-                                       _stream(stream)))
+        _not_on_gpu(fn)
+    if rc:
+        _check(rc)
 
 
 def blockscale_down_workspace_bytes(T: int, k: int, d: int) -> int:
@@ -384,22 +393,20 @@ def blockscale_down_workspace_bytes(T: int, k: int, d: int) -> int:
 
 def blockscale_down(hq, hs, wt, offsets, pos, w_down, s_down, y, workspace, add=None, stream=None) -> None:
     """y [T][d] = add + the weighted sum of each token's experts' down products."""
-    fn = "blockscale_down"
-    (T, k), (E, d, f) = wt.shape, w_down.shape
-    R, DB, FB = T * k, scale_blocks(d), scale_blocks(f)
-    if not (_is(hq, _U8, (R, f)) and _is(hs, _F32, (R, FB)) and _is(wt, _F32, (T, k))
-            and _is(offsets, _I32T, (E + 1,)) and _is(pos, _I32T, (R,)) and _is(w_down, _U8, (E, d, f))
-            and _is(s_down, _F32, (E, DB, FB)) and _is(y, _F32, (T, d))):
+    rc = (_calls or _load_calls()).down(hq, hs, wt, offsets, pos, w_down, s_down, y, workspace, add, stream)
+    if rc is None:
+        fn = "blockscale_down"
+        (T, k), (E, d, f) = wt.shape, w_down.shape
+        R, DB, FB = T * k, scale_blocks(d), scale_blocks(f)
         _need(fn, hq=(hq, torch.uint8, (R, f)), hs=(hs, torch.float32, (R, FB)), wt=(wt, torch.float32, (T, k)),
               offsets=(offsets, torch.int32, (E + 1,)), pos=(pos, torch.int32, (R,)),
               w_down=(w_down, torch.uint8, (E, d, f)), s_down=(s_down, torch.float32, (E, DB, FB)),
               y=(y, torch.float32, (T, d)))
-    if add is not None and not _is(add, _F32, (T, d)):
-        _need(fn, add=(add, torch.float32, (T, d)))
-    n_ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().moe_blockscale_down(_ptr(hq), _ptr(hs), T, k, _ptr(wt), _ptr(offsets), _ptr(pos), E, _ptr(w_down),
-                                     _ptr(s_down), d, f, _ptr(add), _ptr(y), _ptr(workspace), n_ws,
-                                     _stream(stream)))
+        if add is not None:
+            _need(fn, add=(add, torch.float32, (T, d)))
+        _not_on_gpu(fn, workspace)
+    if rc:
+        _check(rc)
 
 
 def profile_enable(on: bool) -> None:
