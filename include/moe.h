@@ -586,7 +586,7 @@ int moe_blockscale_gateup(const uint8_t* xq, const float* xs, int32_t T, int32_t
  * (no term) and may be y itself.  hq [T*k][f], hs [T*k][ceil(f/128)]; w_down
  * [E][d][f] with scales [E][ceil(d/128)][ceil(f/128)]; y fp32 [T][d].
  * Workspace: moe_blockscale_down_workspace_bytes of the same T, k, d (null
- * if that is 0, as it is for one token): the routes' products in fp32.
+ * if that is 0, as it is for one and two tokens): the routes' products in fp32.
  */
 int moe_blockscale_down_workspace_bytes(int32_t T, int32_t k, int32_t d, size_t* bytes);
 int moe_blockscale_down(const uint8_t* hq, const float* hs, int32_t T, int32_t k,

@@ -189,94 +189,110 @@ __global__ __launch_bounds__(256) void bs_combine_kernel(BsDown a) {
   reinterpret_cast<f32x4_t*>(a.y)[i] = y;
 }
 
-// Few tokens: one launch and no workspace.  A block owns 16 outputs of one
-// token; its 16 waves take equal stretches of the token's (route, K block)
-// pairs, straight from memory with U pairs requested at a time (all of them at
-// 6 routes of 2048 inputs: one round trip).  Every column of the matrix step
-// holds the same row.  A wave's sum of each route goes to LDS; they are added
-// in the order of the waves, then the routes weighted in their order.
+// One or two tokens: one launch and no workspace.  A block owns 16 outputs of
+// one token; its 16 waves share the K blocks (and, where those are fewer, the
+// routes), straight from memory with U routes requested at a time: one round trip
+// at 8 routes of 2048 inputs.  Column j of the matrix steps' activations is route
+// j's row, for all routes at once; of the product with route j's weights column j
+// is kept, so that a lane needs its own route's scales only and one accumulator
+// serves every route.  The waves' sums are added in their order, then the routes
+// weighted in theirs.  Bound by the weights, after two loads in a row (positions
+// and offsets, then weights).
 template <int U>
 __global__ __launch_bounds__(1024) void bs_down_token_kernel(BsDown a) {
   constexpr int WAVES = 16;
-  __shared__ float part[TOPK_MAX_K][WAVES][16];
-  __shared__ float route_y[TOPK_MAX_K][16];
-  __shared__ int route_row[TOPK_MAX_K], route_e[TOPK_MAX_K];
+  static_assert(TOPK_MAX_K == 16, "a column of the matrix step for each route");
+  __shared__ f32x4_t part[WAVES][16][4];  // [wave][route][output / 4]
+  __shared__ float route_y[16][16];
+  __shared__ int route_row[16], route_e[16];
+  __shared__ float route_wt[16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, quad = lane >> 4;
   const int n0 = blockIdx.x * 16, t = blockIdx.y, KB = bs_blocks(a.f), DB = bs_blocks(a.d);
-  for (int i = threadIdx.x; i < TOPK_MAX_K * WAVES * 16; i += 1024) (&part[0][0][0])[i] = 0.0f;
+  const int64_t out = (int64_t)t * a.d + n0 + r;
+  const float add = a.add && threadIdx.x < 16 ? a.add[out] : 0.0f;  // (requested early, as the weights of the routes)
+  int row = -1, below = 0;
+  float wt = 0.0f;
   if (wave < a.k) {  // wave j finds route j's row and expert: the last with offsets[e] <= row
-    const int row = a.pos[t * a.k + wave];
-    int below = 0;
+    constexpr int MOST = MAX_EXPERTS / 64;
+    row = a.pos[t * a.k + wave];
+    wt = a.wt[t * a.k + wave];
+    const __amdgpu_buffer_rsrc_t ends = buffer_of(a.offsets + 1, (int64_t)a.E * 4);
+    int end[MOST];
 #pragma unroll
-    for (int i = 0; i < MAX_EXPERTS / 64; i++)
-      if (64 * i < a.E) {
-        const int e = 64 * i + lane;
-        below += __popcll(__ballot(e < a.E && a.offsets[min(e, a.E - 1) + 1] <= row));
-      }
-    if (lane == 0) {
-      route_row[wave] = row < a.T * a.k ? row : -1;
-      route_e[wave] = min(below, a.E - 1);
-    }
+    for (int i = 0; i < MOST; i++) end[i] = __float_as_int(buffer_load4(ends, (64 * i + lane) * 4));  // all at once
+#pragma unroll
+    for (int i = 0; i < MOST; i++) below += __popcll(__ballot(64 * i + lane < a.E && end[i] <= row));
+  }
+  if (lane == 0) {
+    route_row[wave] = row < a.T * a.k ? row : -1;
+    route_e[wave] = min(below, a.E - 1);
+    route_wt[wave] = wt;
   }
   __syncthreads();
-  const int pairs = a.k * KB, u0 = wave * pairs / WAVES, u1 = (wave + 1) * pairs / WAVES;
-  const i32x4_t zero = {0, 0, 0, 0};
+  row = route_row[r];
+  const int e = route_e[r];
+  const uint32_t valid = (uint32_t)__ballot(row >= 0) & 0xffffu;
+  const int64_t x_row = max(row, 0);
+  const uint8_t* xp = a.hq + x_row * a.f;
+  const float *hp = a.hs + x_row * KB, *sp = a.s_down + ((int64_t)e * DB + n0 / BS) * KB;
+  const int G = KB >= WAVES ? 1 : WAVES / KB;  // groups of waves that share the routes
+  const int g = KB >= WAVES ? 0 : wave / KB;
   f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int ub = u0; ub < u1; ub += U) {
-    i32x8_t w[U], x[U];
-    float sc[U];
-#pragma unroll
-    for (int i = 0; i < U; i++) {
-      const int u = min(ub + i, u1 - 1), j = u / KB, kb = u - j * KB;
-      const int row = __builtin_amdgcn_readfirstlane(route_row[j]), e = __builtin_amdgcn_readfirstlane(route_e[j]);
-      const bool on = ub + i < u1 && row >= 0;
+  for (int jb = g; jb < (g < G ? a.k : 0); jb += G * U)
+    for (int kb = KB >= WAVES ? wave : wave - g * KB; kb < KB; kb += WAVES) {
       const int k0 = kb * BS + 16 * quad;
-      const uint8_t* wp = a.w_down + ((int64_t)e * a.d + n0 + r) * a.f + k0;
-      const uint8_t* xp = a.hq + (int64_t)row * a.f + k0;
-      const bool in0 = on && k0 < a.f, in1 = on && k0 + 64 < a.f;
-      w[i] = join_pieces(in0 ? *reinterpret_cast<const i32x4_t*>(wp) : zero,
-                         in1 ? *reinterpret_cast<const i32x4_t*>(wp + 64) : zero);
-      x[i] = join_pieces(in0 ? *reinterpret_cast<const i32x4_t*>(xp) : zero,
-                         in1 ? *reinterpret_cast<const i32x4_t*>(xp + 64) : zero);
-      sc[i] = on ? a.hs[(int64_t)row * KB + kb] * a.s_down[((int64_t)e * DB + n0 / BS) * KB + kb] : 0.0f;
-    }
+      const bool in0 = k0 < a.f, in1 = k0 + 64 < a.f;  // past f: some code of the row, times 0
+      const int c0 = in0 ? k0 : 0, c1 = in1 ? k0 + 64 : 0;
+      i32x8_t w[U];
 #pragma unroll
-    for (int i = 0; i < U; i++) {
-      const int u = ub + i, j = u / KB;
-      if (u >= u1) continue;
-      F16Block wf, xf;
-      wf.set(w[i]);
-      xf.set(x[i]);
-      const f32x4_t p = mfma_block(wf, xf);
+      for (int i = 0; i < U; i++) {
+        const int j = jb + G * i;
+        const bool on = valid >> j & 1;  // (else a buffer of no bytes)
+        const int64_t at = ((int64_t)__builtin_amdgcn_readlane(e, j & 15) * a.d + n0) * a.f;
+        const __amdgpu_buffer_rsrc_t wbuf = buffer_of(a.w_down + at, on ? 16 * a.f : 0);
+        w[i] = join_pieces(buffer_load16(wbuf, r * a.f + c0), buffer_load16(wbuf, r * a.f + c1));
+      }
+      const i32x4_t zero = {0, 0, 0, 0};
+      const i32x4_t x0 = *reinterpret_cast<const i32x4_t*>(xp + c0), x1 = *reinterpret_cast<const i32x4_t*>(xp + c1);
+      const float hs = hp[kb], ws = sp[kb];
+      __builtin_amdgcn_sched_barrier(0);  // (else the loads go between the matrix steps, to save registers)
+      const float sc = hs * ws;
+      F16Block xf;
+      xf.set(join_pieces(in0 ? x0 : zero, in1 ? x1 : zero));
 #pragma unroll
-      for (int q = 0; q < 4; q++) acc[q] = __builtin_fmaf(p[q], sc[i], acc[q]);
-      if (u + 1 == u1 || (u + 1) / KB != j) {  // the wave's last pair of this route
-        if (r == 0) *reinterpret_cast<f32x4_t*>(&part[j][wave][4 * quad]) = acc;
-        acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int i = 0; i < U; i++) {
+        const int j = jb + G * i;
+        F16Block wf;
+        wf.set(w[i]);
+        const f32x4_t p = mfma_block(wf, xf);
+#pragma unroll
+        for (int q = 0; q < 4; q++) acc[q] = r == j ? __builtin_fmaf(p[q], sc, acc[q]) : acc[q];
       }
     }
-  }
+  part[wave][r][quad] = acc;  // (0 for the routes of other groups)
   __syncthreads();
   const int j = threadIdx.x >> 4, n = threadIdx.x & 15;
   if (j < a.k) {
-    float s = 0.0f;
+    float s = part[0][j][n >> 2][n & 3];
 #pragma unroll
-    for (int v = 0; v < WAVES; v++) s += part[j][v][n];
+    for (int v = 1; v < WAVES; v++) s += part[v][j][n >> 2][n & 3];
     route_y[j][n] = s;
   }
   __syncthreads();
   if (threadIdx.x < 16) {
-    const int64_t at = (int64_t)t * a.d + n0 + n;
-    float y = a.add ? a.add[at] : 0.0f;
-    for (int i = 0; i < a.k; i++)
-      if (route_row[i] >= 0) y = __builtin_fmaf(a.wt[t * a.k + i], route_y[i][n], y);
-    a.y[at] = y;
+    float y = add;
+#pragma unroll
+    for (int i = 0; i < TOPK_MAX_K; i++)
+      y = valid >> i & 1 ? __builtin_fmaf(route_wt[i], route_y[i][n], y) : y;
+    a.y[out] = y;
   }
 }
 
-// (2 tokens: 27.6 us so, 25.6 us as products and a combine)
-constexpr int TOKEN_MAX_T = 1;
+// Measured so / as products and a combine: 6 of 384 experts x 2048 x 4096, 1
+// token 11.4 us, 2 tokens 22.3 / 25.9; 4 of 64 x 1408 x 2048, 2 tokens 8.0 / 11.7;
+// but 4 tokens 45.1 / 44.9 and, where they share experts (16), 32.0 / 19.3.
+constexpr int TOKEN_MAX_T = 2;
 
 size_t bs_down_ws(int T, int k, int d) { return T <= TOKEN_MAX_T ? 0 : (size_t)T * k * d * 4; }
 
