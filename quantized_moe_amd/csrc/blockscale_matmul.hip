@@ -200,8 +200,12 @@ static hipError_t launch_rows(const BsMatmul& a, hipStream_t s) {
 //   M 32, 32 outputs a block instead of 16: 11.1 and 9.9, at N = K = 8192 22.6 and 30.2
 //   M 128 (64 tiles of 128 x 64): 20.2 / 17.2 on them, 15.2 / 12.0 on 64 x 64
 //   M 1000, N 1100, K 2064 (144): 15.3 / 12.3 on 128 x 64, 19.3 / 16.5 on 64 x 64
-//     (288: a second round of few), fp16 13.5 on 64 x 96 (198); 700 x 1500 x
+//     (288: a second round of few), fp16 13.0 on 64 x 96 (198); 700 x 1500 x
 //     1040 9.6 and 8.3, but M 512 (384 tiles of 64 x 96) 23.5 and 34.3
+//   fp16 64 x 64 and 64 x 96 with three groups and two stages, and with two
+//     groups: 512 x 2048 x 4096 14.8 and 15.4, 512 x 1024 x 1040 6.4 and 7.0, 64 x
+//     4096 x 2048 8.7 and 9.3; 64 x 96 13.0 and 13.6, 1500 x 700 x 8192 30.9 and 32.7
+//     (E4M3 steps, 64 x 64: 14.2 and 12.3)
 //   M 512 (128 tiles of 128 x 128): 32.0 / 24.4 on them, 22.6 / 18.2 on 128 x 64
 //   M 1024 (256): 34.6 (two groups) / 26.0 (four stages) on 128 x 128, 38.4 /
 //     32.6 with one group and two stages, 42.6 / 29.1 on 128 x 64
@@ -230,10 +234,10 @@ static hipError_t launch_matmul(const BsMatmul& a, hipStream_t s) {
   if (tiles(128, 128) >= 192) return launch_tile<2, 2, 4, 4, 2, 2, true, OUT>(a, s);
   if (tiles(128, 64) >= 128) {
     // one round of 64 x 96 tiles where they are enough for the CUs but not more
-    if (tiles(64, 96) <= 256) return launch_tile<2, 2, 2, 3, 2, 2, true, OUT>(a, s);
+    if (tiles(64, 96) <= 256) return launch_tile<2, 2, 2, 3, 2, 3, true, OUT>(a, s);
     return launch_tile<2, 2, 4, 2, 3, 2, true, OUT>(a, s);
   }
-  return launch_tile<2, 2, 2, 2, 3, 2, true, OUT>(a, s, parts);
+  return launch_tile<2, 2, 2, 2, 2, 3, true, OUT>(a, s, parts);
 }
 
 hipError_t launch_bs_matmul(const BsMatmul& a, hipStream_t s) {
