@@ -164,50 +164,58 @@ __device__ __forceinline__ void store4(uint16_t* p, f32x4_t v, int left, bool ve
   }
 }
 
-// The M tile of BM bucket rows that is the `tile`-th over all experts: expert,
-// first row and row count.  false: there are fewer tiles.  Every lane of a wave
-// calls it alike; lane l counts the tiles of experts C l .. C l + C - 1, all
+// The M tiles of BM bucket rows over all experts.  Every lane of a wave makes
+// the calls alike; lane l counts the tiles of experts C l .. C l + C - 1, all
 // offsets requested at once.
 template <int BM>
-__device__ __forceinline__ bool find_tile(const int32_t* __restrict__ offsets, int E, int tile, int* e_out, int* row0,
-                                          int* rows) {
-  constexpr int MOST = MAX_EXPERTS / 64;
-  const int lane = threadIdx.x & 63, C = (E + 63) / 64, e0 = lane * C;
-  int off[MOST + 1];
-  off[0] = offsets[min(e0, E)];
+struct TileScan {
+  static constexpr int MOST = MAX_EXPERTS / 64;
+  int off[MOST + 1], C, e0, before, upto;  // tiles before the lane's experts, and with them
+
+  __device__ __forceinline__ TileScan(const int32_t* __restrict__ offsets, int E) {
+    const int lane = threadIdx.x & 63;
+    C = (E + 63) / 64;
+    e0 = lane * C;
+    off[0] = offsets[min(e0, E)];
 #pragma unroll
-  for (int i = 0; i < MOST; i++)
-    if (i < C) off[i + 1] = offsets[min(e0 + i + 1, E)];
-  int n = 0;
+    for (int i = 0; i < MOST; i++)
+      if (i < C) off[i + 1] = offsets[min(e0 + i + 1, E)];
+    int n = 0;
 #pragma unroll
-  for (int i = 0; i < MOST; i++)
-    if (i < C) n += (off[i + 1] - off[i] + BM - 1) / BM;
-  int incl = n;
+    for (int i = 0; i < MOST; i++)
+      if (i < C) n += (off[i + 1] - off[i] + BM - 1) / BM;
+    upto = n;
 #pragma unroll
-  for (int s = 1; s < 64; s <<= 1) {
-    const int o = __shfl_up(incl, s, 64);
-    if (lane >= s) incl += o;
-  }
-  const uint64_t has = __ballot(tile < incl);
-  if (has == 0) return false;
-  int left = tile - (incl - n), e = e0, first = 0, count = 0;
-#pragma unroll
-  for (int i = 0; i < MOST; i++)
-    if (i < C) {
-      const int t = (off[i + 1] - off[i] + BM - 1) / BM;
-      if (left >= 0 && left < t) {
-        e = e0 + i;
-        first = off[i] + left * BM;
-        count = min(BM, off[i + 1] - first);
-      }
-      left -= t;
+    for (int s = 1; s < 64; s <<= 1) {
+      const int o = __shfl_up(upto, s, 64);
+      if (lane >= s) upto += o;
     }
-  const int src = __builtin_ctzll(has);
-  *e_out = __builtin_amdgcn_readlane(e, src);
-  *row0 = __builtin_amdgcn_readlane(first, src);
-  *rows = __builtin_amdgcn_readlane(count, src);
-  return true;
-}
+    before = upto - n;
+  }
+  __device__ __forceinline__ int tiles() const { return __builtin_amdgcn_readlane(upto, 63); }
+  // Tile `tile`'s expert, first row and row count.  false: there are fewer.
+  __device__ __forceinline__ bool find(int tile, int* e_out, int* row0, int* rows) const {
+    const uint64_t has = __ballot(tile < upto);
+    if (has == 0) return false;
+    int left = tile - before, e = e0, first = 0, count = 0;
+#pragma unroll
+    for (int i = 0; i < MOST; i++)
+      if (i < C) {
+        const int t = (off[i + 1] - off[i] + BM - 1) / BM;
+        if (left >= 0 && left < t) {
+          e = e0 + i;
+          first = off[i] + left * BM;
+          count = min(BM, off[i + 1] - first);
+        }
+        left -= t;
+      }
+    const int src = __builtin_ctzll(has);
+    *e_out = __builtin_amdgcn_readlane(e, src);
+    *row0 = __builtin_amdgcn_readlane(first, src);
+    *rows = __builtin_amdgcn_readlane(count, src);
+    return true;
+  }
+};
 
 // Upper bound on the number of M tiles of n rows in E buckets.
 inline int64_t max_tiles(int64_t n, int E, int bm) {
