@@ -575,3 +575,76 @@ def test_binding_checks_shapes_and_dtypes():
 
 class _NoStream:
     cuda_stream = None
+
+
+def test_binding_refuses_host_memory():
+    x, q, s = torch.zeros(4, 256), torch.zeros(4, 256, dtype=torch.uint8), torch.zeros(4, 2)
+    w, ws, y = torch.zeros(64, 256, dtype=torch.uint8), torch.zeros(1, 2), torch.zeros(4, 64)
+    with pytest.raises(ValueError, match="GPU memory"):
+        lib.blockscale_quantize(x, q, s, stream=_NoStream)
+    with pytest.raises(ValueError, match="GPU memory"):
+        lib.blockscale_matmul(q, s, w, ws, y, stream=_NoStream)
+
+
+@gpu
+def test_binding_names_what_is_wrong_on_the_gpu_too():
+    f = lambda *n: torch.zeros(*n, device=DEV)  # noqa: E731
+    u8 = lambda *n: torch.zeros(*n, dtype=torch.uint8, device=DEV)  # noqa: E731
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32, device=DEV)  # noqa: E731
+    x, q, s, w, ws, y = f(4, 256), u8(4, 256), f(4, 2), u8(64, 256), f(1, 2), f(4, 64)
+    with pytest.raises(TypeError, match="x must be"):
+        lib.blockscale_quantize(x.half(), q, s)
+    with pytest.raises(ValueError, match="s has shape"):
+        lib.blockscale_quantize(x, q, s[:3])
+    with pytest.raises(lib.MoeError, match="ldx"):
+        lib.blockscale_quantize(f(4, 258)[:, :256], q, s)  # rows not 16 bytes apart: the library's own check
+    with pytest.raises(ValueError, match="contiguous rows"):
+        lib.blockscale_matmul(u8(256, 4).t(), s, w, ws, y)
+    with pytest.raises(TypeError, match="xs must be"):
+        lib.blockscale_matmul(q, s.double(), w, ws, y)
+    with pytest.raises(ValueError, match="wq must be contiguous"):
+        lib.blockscale_matmul(q, s, u8(64, 512)[:, :256], ws, y)
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        lib.blockscale_matmul(q, s, w, ws, y, u8(64, 64)[:, ::2])
+    with pytest.raises(ValueError, match="GPU memory"):
+        lib.blockscale_matmul(q, s.cpu(), w, ws, y)
+    wg, sg, hq, hs = u8(8, 128, 256), f(8, 1, 2), u8(8, 128), f(8, 1)
+    with pytest.raises(ValueError, match="offsets has shape"):
+        lib.blockscale_gateup(q, s, 2, i32(8), i32(8), wg, sg, wg, sg, hq, hs)
+    with pytest.raises(TypeError, match="pos must be"):
+        lib.blockscale_down(hq, hs, f(4, 2), i32(9), f(8), u8(8, 256, 128), f(8, 2, 1), f(4, 256), None)
+    with pytest.raises(ValueError, match="add has shape"):
+        lib.blockscale_down(hq, hs, f(4, 2), i32(9), i32(8), u8(8, 256, 128), f(8, 2, 1), f(4, 256), u8(65536), add=f(4, 255))
+    with pytest.raises(TypeError, match="arguments"):
+        lib._load_calls().matmul(q, s)
+    with pytest.raises(AttributeError):
+        lib.blockscale_quantize(x, q, s, stream=7)
+
+
+@gpu
+def test_two_tokens_that_share_an_expert_and_lose_routes():
+    """The one-launch down product at its largest batch: 2 tokens, 16 routes of which some have no place."""
+    rng = np.random.default_rng(21)
+    T, k, E, d, f = 2, 16, 20, 80, 1424
+    idx = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    idx[0, 3] = idx[1, 0] = idx[1, 15] = -1
+    offsets, perm, pos = (t.to(DEV) for t in buckets(torch.from_numpy(idx), E)[-3:])
+    hq, hs = make_rows(rng, T * k, f)
+    wq, ws = make_weight(rng, d, f, E)
+    wt = torch.from_numpy(rng.random((T, k)).astype(np.float32))
+    y = torch.full((T, d), float("nan"), device=DEV)
+    assert lib.blockscale_down_workspace_bytes(T, k, d) == 0
+    lib.blockscale_down(up(hq), up(hs), up(wt), offsets, pos, up(wq), up(ws), y, None)
+    ref, mag = torch.zeros(T, d, dtype=torch.float64), torch.zeros(T, d, dtype=torch.float64)
+    p = pos.cpu().tolist()
+    for t in range(T):
+        for j in range(k):
+            e = int(idx[t, j])
+            if e < 0:
+                continue
+            r = p[t * k + j]
+            a, b = product(values_rows(hq[r: r + 1], hs[r: r + 1]), values_weight(wq[e], ws[e]))
+            ref[t] += wt[t, j].double() * a[0]
+            mag[t] += wt[t, j].double() * b[0]
+    tol = (SUM(f) + (k + 2) * 2.0 ** -24) * mag
+    assert ((y.cpu().double() - ref).abs() <= tol).all()
