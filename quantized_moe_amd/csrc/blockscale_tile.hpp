@@ -99,15 +99,7 @@ __device__ __forceinline__ bool tile_product(uint8_t* lds, const __amdgpu_buffer
   };
 
   const int wn = wave % C::WN, wm = wave / C::WN;
-  // The weight scales of the whole tile are staged once: loads of them in the
-  // loop would wait for the copies in flight (one counter counts both).
   float* wsc_all = reinterpret_cast<float*>(lds + C::SCALES);  // [mat][NB][KB]
-#pragma unroll
-  for (int mat = 0; mat < C::NMAT; mat++)
-    for (int i = threadIdx.x; i < C::NB * KB; i += C::THREADS) {
-      const int b = C::NB == 1 ? 0 : min(i / KB, ws_rows - 1);
-      wsc_all[mat * C::NB * KB + i] = ws[mat][b * KB + (C::NB == 1 ? i : i % KB)];
-    }
   const float* wsr = wsc_all + (wn * TN * 16) / BS * KB;
   const int swz0 = (quad ^ (r & 7)) * 16, swz1 = ((quad + 4) ^ (r & 7)) * 16;
   auto frag = [&](const uint8_t* tile, int row) {  // the lane's 32 bytes of the tile's row (row % 8 == r % 8)
@@ -124,6 +116,15 @@ __device__ __forceinline__ bool tile_product(uint8_t* lds, const __amdgpu_buffer
 #pragma unroll
     for (int i = 0; i < C::COPIES; i++) fetch(kb, b, i);
   }
+  // The weight scales of the whole tile are staged once: loads of them in the
+  // loop would wait for the copies in flight (one counter counts both).  Here they
+  // wait for the first stages', which the first step needs anyway.
+#pragma unroll
+  for (int mat = 0; mat < C::NMAT; mat++)
+    for (int i = threadIdx.x; i < C::NB * KB; i += C::THREADS) {
+      const int b = C::NB == 1 ? 0 : min(i / KB, ws_rows - 1);
+      wsc_all[mat * C::NB * KB + i] = ws[mat][b * KB + (C::NB == 1 ? i : i % KB)];
+    }
   int stage = 0;
   for (int k0 = kb0; k0 < kb1; k0 += KS) {
     const int kb = k0 + group;
