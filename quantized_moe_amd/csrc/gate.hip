@@ -14,11 +14,14 @@
 
 namespace qmoe {
 
-// e^t for t in [-80, 80]: the steps of sigmoid32 (include/moe.h).
+// e^t for t in [-80, 80]: the steps of sigmoid32 (include/moe.h).  Two of them
+// in fewer instructions with the same bits: n ln2_hi has 22 bits at most, so a
+// fused multiply-add rounds as the product and the difference do; and the sum
+// with 1.5 2^23 ends in n, which is added to p's exponent (p 2^n is normal).
 __device__ __forceinline__ float exp32(float t) {
   const float kf = t * 0x1.715476p+0f;
-  const float n = (kf + 0x1.8p+23f) - 0x1.8p+23f;
-  const float r = (t - n * 0x1.62e400p-1f) - n * 0x1.7f7d1cp-20f;
+  const float shifted = kf + 0x1.8p+23f, n = shifted - 0x1.8p+23f;
+  const float r = __builtin_fmaf(-n, 0x1.62e400p-1f, t) - n * 0x1.7f7d1cp-20f;
   float p = 0x1.6c16c2p-10f;
   p = p * r + 0x1.111112p-7f;
   p = p * r + 0x1.555556p-5f;
@@ -26,7 +29,7 @@ __device__ __forceinline__ float exp32(float t) {
   p = p * r + 0.5f;
   p = p * r + 1.0f;
   p = p * r + 1.0f;
-  return __builtin_amdgcn_ldexpf(p, (int)n);  // p 2^n, a normal number
+  return __uint_as_float((__float_as_uint(shifted) << 23) + __float_as_uint(p));
 }
 
 // Maxima and minima of numbers (the compiler, which must allow for signalling
