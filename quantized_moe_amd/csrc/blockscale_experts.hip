@@ -132,15 +132,19 @@ static hipError_t launch_gateup(const BsGateup& a, hipStream_t s) {
 // tiles of 16 / 32 / 48 / 128 rows:
 //   0.1 rows (8 tokens)      143 / 145 / 154 / 183   (1 token: 26 / 29 / 34 / 54)
 //   1 row (64 tokens)        687 / 681 / 681 / 912
-//   16 rows, uniform         1287 / 1111 .. 1365 / 1373 / 1548
+//   11 rows                  1177 / 1184 / 1305 / -
+//   16 rows, uniform         1294 / 1125 / 1122 / 1548;  24 rows (256): - / 815 / 741 / -
 //   48 rows (128, crowded)   784 / 565 / 544 / 631
 //   96 rows (64, crowded)    645 / 405 / 358 / 388
 //   384 rows (16, 2048 x 512, crowded)  91 / 49 / 47 / 37
+// 48 rows on four waves, each with twice the outputs, for eight: fewer reads of
+// LDS and conversions a matrix step (48 rows crowded 502 -> 486, 24 rows 752 ->
+// 741); 32 rows on four: 538 for 561 crowded, but 1211 for 1184 at 11 rows.
 hipError_t launch_bs_gateup(const BsGateup& a, hipStream_t s) {
   const int64_t n = (int64_t)a.T * a.k, E = a.E;
   if (n <= 4 * E) return launch_gateup<Tile<8, 1, 1, 1, 4, 1, 2, true>>(a, s);
-  if (n <= 32 * E) return launch_gateup<Tile<8, 1, 1, 2, 2, 1, 2, true>>(a, s);
-  if (n <= 160 * E) return launch_gateup<Tile<8, 1, 1, 3, 2, 1, 2, true>>(a, s);
+  if (n <= 16 * E) return launch_gateup<Tile<8, 1, 1, 2, 2, 1, 2, true>>(a, s);
+  if (n <= 160 * E) return launch_gateup<Tile<4, 1, 2, 3, 2, 1, 2, true>>(a, s);
   return launch_gateup<Tile<4, 2, 2, 4, 3, 1, 2, true>>(a, s);
 }
 
@@ -319,11 +323,14 @@ static hipError_t launch_down(const BsDown& a, hipStream_t s) {
 //   16 rows               749 / 658 / 650 / 800
 //   64 rows, crowded      1726 / 1080 / 999 / 1139
 //   384 rows (64 experts) 1348 / 740 / 655 / 630
+// 48 rows on four waves for eight: 64 rows, crowded 993 -> 952, uniform 970 -> 960
+// (64 rows x 128 outputs, three blocks a CU: 965 and 926, but 56 for 48 at 500
+// tokens over 64 experts x 1408 x 2000).
 static hipError_t launch_down_products(const BsDown& a, hipStream_t s) {
   const int64_t n = (int64_t)a.T * a.k, E = a.E;
   if (n <= 2 * E) return launch_down<Tile<8, 1, 1, 1, 4, 1, 1, true>>(a, s);
   if (n <= 12 * E) return launch_down<Tile<8, 1, 2, 2, 2, 1, 1, true>>(a, s);
-  if (n <= 200 * E) return launch_down<Tile<8, 1, 2, 3, 2, 1, 1, true>>(a, s);
+  if (n <= 200 * E) return launch_down<Tile<4, 1, 4, 3, 2, 1, 1, true>>(a, s);
   return launch_down<Tile<4, 2, 4, 4, 3, 1, 1, true>>(a, s);
 }
 
