@@ -258,7 +258,7 @@ __global__ __launch_bounds__(1024) void bs_down_token_kernel(BsDown a) {
 #pragma unroll
       for (int i = 0; i < U; i++) {
         const int j = jb + G * i;
-        const bool on = valid >> j & 1;  // (else a buffer of no bytes)
+        const bool on = j < a.k && (valid >> (j & 15) & 1);  // (else a buffer of no bytes)
         const int64_t at = ((int64_t)__builtin_amdgcn_readlane(e, j & 15) * a.d + n0) * a.f;
         const __amdgpu_buffer_rsrc_t wbuf = buffer_of(a.w_down + at, on ? 16 * a.f : 0);
         w[i] = join_pieces(buffer_load16(wbuf, r * a.f + c0), buffer_load16(wbuf, r * a.f + c1));

@@ -622,12 +622,14 @@ def test_binding_names_what_is_wrong_on_the_gpu_too():
 
 
 @gpu
-def test_two_tokens_that_share_an_expert_and_lose_routes():
-    """The one-launch down product at its largest batch: 2 tokens, 16 routes of which some have no place."""
+@pytest.mark.parametrize("T,k,f", [(2, 16, 1424), (1, 16, 16), (2, 5, 128), (1, 16, 272), (2, 7, 1040), (1, 9, 2064),
+                                   (2, 16, 4112)])
+def test_two_tokens_that_share_an_expert_and_lose_routes(T, k, f):
+    """The one-launch down product: one and two tokens, routes of which some have no place, few blocks and many."""
     rng = np.random.default_rng(21)
-    T, k, E, d, f = 2, 16, 20, 80, 1424
+    E, d = 20, 80
     idx = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
-    idx[0, 3] = idx[1, 0] = idx[1, 15] = -1
+    idx[0, 3] = idx[T - 1, 0] = idx[T - 1, k - 1] = -1
     offsets, perm, pos = (t.to(DEV) for t in buckets(torch.from_numpy(idx), E)[-3:])
     hq, hs = make_rows(rng, T * k, f)
     wq, ws = make_weight(rng, d, f, E)
