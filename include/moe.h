@@ -521,14 +521,11 @@ int moe_gate_topk(const moe_gate* G, const void* z, int32_t z_dtype, int64_t z_s
  * [E][NB][KB].  These are the layouts in which 8-bit checkpoints of the
  * layer's family come, so nothing is repacked.
  *
- * Products are summed in fp32: the dot products of one block of 128 on the
- * matrix units, then one fused multiply-add per block with the product of
- * the two scales.  One exception: bf16 outputs of moe_blockscale_matmul with
- * M > 32 and K >= 1024 take the dot products from the E4M3 matrix steps,
- * which keep 14 bits below the largest of each 8 products (1.4e-5 of a
- * typical dot product, where the output's own rounding is 2e-3).  A code or
- * scale that is not a number makes the outputs that it enters NaN.
- * Identical inputs give bitwise identical outputs.
+ * Products are summed in fp32, bf16 outputs too: the dot products of one
+ * block of 128 on the matrix units (the codes as fp16, which holds them
+ * exactly), then one fused multiply-add per block with the product of the
+ * two scales.  A code or scale that is not a number makes the outputs that it
+ * enters NaN.  Identical inputs give bitwise identical outputs.
  *
  * Limits: K (inputs) a multiple of 16 in [16, 16384]; N (outputs) in [1,
  * 65536] with N * K < 2^31; M in [0, 2^20] rows; q pointers 16-byte aligned,

@@ -3,10 +3,10 @@
 // Matrix-unit step: a block of 128 inputs is 16 x 16 dot products that leave
 // the matrix unit on their own and meet the product of their two scales in one
 // fused multiply-add.  The E4M3 codes enter as fp16, which holds each exactly,
-// through 16x16x32 steps whose sums are full fp32 (measured: 1.2e-8 of the
-// result per block).  The unit's own E4M3 steps align groups of eight products
-// to the largest and drop what lies 14 bits below it (measured: 1.4e-5 of the
-// result): too coarse for fp32 outputs.
+// through 16x16x32 steps whose sums are fp32.  The unit's own E4M3 steps, twice
+// as fast, drop what lies some 14 bits below the largest of eight products: where
+// large ones cancel, what is left of the sum is lost (2064 whole-number products
+// with the sum -316 gave -208), so no product uses them.
 // The operands are taken as (weights, activations): the result's 16 columns
 // (lane % 16) are activation rows, so a lane needs one activation scale per
 // tile, and its 4 values are 4 consecutive outputs of that row (rows 4 (lane /
@@ -71,12 +71,6 @@ __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v
 
 // One output value, fp32 or bf16 (nearest even).
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
-
-// E4M3 bytes on the matrix unit's own E4M3 step (see above for its sums).
-__device__ __forceinline__ f32x4_t mfma_block_e4m3(i32x8_t w, i32x8_t x) {
-  const f32x4_t z = {0.0f, 0.0f, 0.0f, 0.0f};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, z, 0, 0, 0, 127, 0, 127);  // unit scales 2^0
-}
 
 // One lane's operand of a block as fp16, converted once and used for several
 // tiles.

@@ -142,10 +142,10 @@ static hipError_t launch_gateup(const BsGateup& a, hipStream_t s) {
 // 741); 32 rows on four: 538 for 561 crowded, but 1211 for 1184 at 11 rows.
 hipError_t launch_bs_gateup(const BsGateup& a, hipStream_t s) {
   const int64_t n = (int64_t)a.T * a.k, E = a.E;
-  if (n <= 4 * E) return launch_gateup<Tile<8, 1, 1, 1, 4, 1, 2, true>>(a, s);
-  if (n <= 16 * E) return launch_gateup<Tile<8, 1, 1, 2, 2, 1, 2, true>>(a, s);
-  if (n <= 160 * E) return launch_gateup<Tile<4, 1, 2, 3, 2, 1, 2, true>>(a, s);
-  return launch_gateup<Tile<4, 2, 2, 4, 3, 1, 2, true>>(a, s);
+  if (n <= 4 * E) return launch_gateup<Tile<8, 1, 1, 1, 4, 1, 2>>(a, s);
+  if (n <= 16 * E) return launch_gateup<Tile<8, 1, 1, 2, 2, 1, 2>>(a, s);
+  if (n <= 160 * E) return launch_gateup<Tile<4, 1, 2, 3, 2, 1, 2>>(a, s);
+  return launch_gateup<Tile<4, 2, 2, 4, 3, 1, 2>>(a, s);
 }
 
 // ye[r][n] = (D_e h_r)[n] for the bucket rows.
@@ -328,10 +328,10 @@ static hipError_t launch_down(const BsDown& a, hipStream_t s) {
 // tokens over 64 experts x 1408 x 2000).
 static hipError_t launch_down_products(const BsDown& a, hipStream_t s) {
   const int64_t n = (int64_t)a.T * a.k, E = a.E;
-  if (n <= 2 * E) return launch_down<Tile<8, 1, 1, 1, 4, 1, 1, true>>(a, s);
-  if (n <= 12 * E) return launch_down<Tile<8, 1, 2, 2, 2, 1, 1, true>>(a, s);
-  if (n <= 200 * E) return launch_down<Tile<4, 1, 4, 3, 2, 1, 1, true>>(a, s);
-  return launch_down<Tile<4, 2, 4, 4, 3, 1, 1, true>>(a, s);
+  if (n <= 2 * E) return launch_down<Tile<8, 1, 1, 1, 4, 1, 1>>(a, s);
+  if (n <= 12 * E) return launch_down<Tile<8, 1, 2, 2, 2, 1, 1>>(a, s);
+  if (n <= 200 * E) return launch_down<Tile<4, 1, 4, 3, 2, 1, 1>>(a, s);
+  return launch_down<Tile<4, 2, 4, 4, 3, 1, 1>>(a, s);
 }
 
 hipError_t launch_bs_down(const BsDown& a, hipStream_t s) {

@@ -170,9 +170,9 @@ size_t bs_matmul_ws(int M, int N, int K) {
   return s > 1 ? (size_t)s * M * N * 4 : 0;
 }
 
-template <int WN, int WM, int TN, int TM, int ST, int KS, bool EXACT, typename OUT>
+template <int WN, int WM, int TN, int TM, int ST, int KS, typename OUT>
 static hipError_t launch_tile(const BsMatmul& a, hipStream_t s, int parts = 1) {
-  using C = Tile<WN, WM, TN, TM, ST, KS, 1, EXACT>;
+  using C = Tile<WN, WM, TN, TM, ST, KS, 1>;
   const int n_tiles = (a.N + C::BN - 1) / C::BN, m_tiles = (a.M + C::BM - 1) / C::BM;
   auto* k = bs_matmul_tile_kernel<C, OUT>;
   int per_cu, cus;
@@ -195,49 +195,35 @@ static hipError_t launch_rows(const BsMatmul& a, hipStream_t s) {
 
 // The variant: by rows, then the largest tile of which there are enough for
 // the 256 CUs.  Measured on both sides of each step, N = K = 4096 unless
-// given (us, fp16 steps / E4M3 steps):
-//   M 32: rows 9.8, 64 x 64 tiles 14.9 / 12.1;   64: rows 15.3, tiles 14.9 / 12.1
+// given (us):
+//   M 32: rows 9.8, 64 x 64 tiles 14.9;   64: rows 15.3, tiles 14.9
 //   M 32, 32 outputs a block instead of 16: 11.1 and 9.9, at N = K = 8192 22.6 and 30.2
-//   M 128 (64 tiles of 128 x 64): 20.2 / 17.2 on them, 15.2 / 12.0 on 64 x 64
-//   M 1000, N 1100, K 2064 (144): 15.3 / 12.3 on 128 x 64, 19.3 / 16.5 on 64 x 64
-//     (288: a second round of few), fp16 13.0 on 64 x 96 (198); 700 x 1500 x
-//     1040 9.6 and 8.3, but M 512 (384 tiles of 64 x 96) 23.5 and 34.3
-//   fp16 64 x 64 and 64 x 96 with three groups and two stages, and with two
-//     groups: 512 x 2048 x 4096 14.8 and 15.4, 512 x 1024 x 1040 6.4 and 7.0, 64 x
+//   M 128 (64 tiles of 128 x 64): 20.2 on them, 15.2 on 64 x 64
+//   M 1000, N 1100, K 2064 (144): 15.3 on 128 x 64, 19.3 on 64 x 64 (288: a
+//     second round of few), 13.0 on 64 x 96 (198); 700 x 1500 x 1040 9.6 and
+//     8.3, but M 512 (384 tiles of 64 x 96) 23.5 and 34.3
+//   64 x 64 and 64 x 96 with three groups and two stages, and with two groups:
+//     512 x 2048 x 4096 14.8 and 15.4, 512 x 1024 x 1040 6.4 and 7.0, 64 x
 //     4096 x 2048 8.7 and 9.3; 64 x 96 13.0 and 13.6, 1500 x 700 x 8192 30.9 and 32.7
-//     (E4M3 steps, 64 x 64: 14.2 and 12.3)
-//   M 512 (128 tiles of 128 x 128): 32.0 / 24.4 on them, 22.6 / 18.2 on 128 x 64
-//   M 1024 (256): 34.6 (two groups) / 26.0 (four stages) on 128 x 128, 38.4 /
-//     32.6 with one group and two stages, 42.6 / 29.1 on 128 x 64
-//   M 2048 (512; 128 of 256 x 256): 71.0 / 42.9 with one group and two stages,
-//     66.9 / 53.6 with two groups; 256 x 256 E4M3 61
-//   M 4096 (1024; 256 of 256 x 256): 123 / 82.8 on 128 x 128, 132 with two
-//     groups; 256 x 256 E4M3 71.4
-// The E4M3 steps round a sum by 1.4e-5 of it, bf16 by 2e-3: they serve bf16
-// outputs, and sums of eight blocks or more, where the errors average out.
+//   M 512 (128 tiles of 128 x 128): 32.0 on them, 22.6 on 128 x 64
+//   M 1024 (256): 34.6 on 128 x 128 with two groups, 38.4 with one group and
+//     two stages, 42.6 on 128 x 64
+//   M 2048 (512): 71.0 with one group and two stages, 66.9 with two groups
+//   M 4096 (1024): 123 on 128 x 128, 132 with two groups
 template <typename OUT>
 static hipError_t launch_matmul(const BsMatmul& a, hipStream_t s) {
   if (a.M <= 16) return launch_rows<1, 1, 4, OUT>(a, s);
   if (a.M <= 32) return a.N >= 6144 ? launch_rows<2, 2, 2, OUT>(a, s) : launch_rows<1, 2, 2, OUT>(a, s);
   auto tiles = [&](int bn, int bm) { return tile_count(a.M, a.N, bm, bn); };
   const int parts = split_k(a.M, a.N, a.K);
-  if constexpr (sizeof(OUT) == 2) {
-    if (a.K >= 8 * BS) {
-      if (tiles(256, 256) >= 192) return launch_tile<2, 4, 8, 4, 2, 1, false, OUT>(a, s);
-      if (tiles(128, 128) >= 384) return launch_tile<2, 2, 4, 4, 2, 1, false, OUT>(a, s);
-      if (tiles(128, 128) >= 192) return launch_tile<2, 2, 4, 4, 4, 1, false, OUT>(a, s);
-      if (tiles(128, 64) >= 128) return launch_tile<2, 2, 4, 2, 3, 1, false, OUT>(a, s);
-      return launch_tile<2, 2, 2, 2, 3, 2, false, OUT>(a, s, parts);
-    }
-  }
-  if (tiles(128, 128) >= 768) return launch_tile<2, 2, 4, 4, 2, 1, true, OUT>(a, s);
-  if (tiles(128, 128) >= 192) return launch_tile<2, 2, 4, 4, 2, 2, true, OUT>(a, s);
+  if (tiles(128, 128) >= 768) return launch_tile<2, 2, 4, 4, 2, 1, OUT>(a, s);
+  if (tiles(128, 128) >= 192) return launch_tile<2, 2, 4, 4, 2, 2, OUT>(a, s);
   if (tiles(128, 64) >= 128) {
     // one round of 64 x 96 tiles where they are enough for the CUs but not more
-    if (tiles(64, 96) <= 256) return launch_tile<2, 2, 2, 3, 2, 3, true, OUT>(a, s);
-    return launch_tile<2, 2, 4, 2, 3, 2, true, OUT>(a, s);
+    if (tiles(64, 96) <= 256) return launch_tile<2, 2, 2, 3, 2, 3, OUT>(a, s);
+    return launch_tile<2, 2, 4, 2, 3, 2, OUT>(a, s);
   }
-  return launch_tile<2, 2, 2, 2, 2, 3, true, OUT>(a, s, parts);
+  return launch_tile<2, 2, 2, 2, 2, 3, OUT>(a, s, parts);
 }
 
 hipError_t launch_bs_matmul(const BsMatmul& a, hipStream_t s) {

@@ -14,11 +14,9 @@ namespace qmoe {
 // KS groups of such waves share the K blocks (group g takes blocks g, g + KS,
 // ...), each with stages of its own, and add their sums in the order of the
 // groups: where tiles are few, a CU has more waves and half the steps.
-// EXACT: fp16 steps (fp32 sums); else the unit's E4M3 steps, twice as fast.
-template <int WN_, int WM_, int TN_, int TM_, int ST, int KS_, int NMAT_, bool EXACT_>
+template <int WN_, int WM_, int TN_, int TM_, int ST, int KS_, int NMAT_>
 struct Tile {
   static constexpr int WN = WN_, WM = WM_, TN = TN_, TM = TM_, STAGES = ST, KS = KS_, NMAT = NMAT_;
-  static constexpr bool EXACT = EXACT_;
   static constexpr int WAVES = WN * WM, THREADS = 64 * WAVES * KS;
   static constexpr int BN = WN * TN * 16, BM = WM * TM * 16;
   static constexpr int S_ROWS = (BM + 63) / 64 * 64;  // a copy of scales brings 64
@@ -33,7 +31,7 @@ struct Tile {
   static constexpr int X_COPIES = (X_UNITS + WAVES - 1) / WAVES;
   static constexpr int COPIES = NMAT * W_COPIES + X_COPIES;
   static constexpr int TILE_ROWS = NMAT * TN;                           // tiles of 16 outputs of a wave
-  static constexpr int SPREAD = !EXACT || TILE_ROWS == 1 ? TILE_ROWS : TILE_ROWS / 2;  // those that copies go with
+  static constexpr int SPREAD = TILE_ROWS == 1 ? 1 : TILE_ROWS / 2;     // those that copies go with
   static constexpr int PER_ROW = (COPIES + SPREAD - 1) / SPREAD;
   // registers: where two blocks of 8 small waves fit a CU's LDS, they fit its registers too
   static constexpr int WAVES_PER_SIMD = 2 * LDS <= 160 * 1024 && THREADS == 512 && TILE_ROWS * TM <= 6 ? 4 : 2;
@@ -152,61 +150,37 @@ __device__ __forceinline__ bool tile_product(uint8_t* lds, const __amdgpu_buffer
       for (int j = 0; j < TM; j++) sc[mat][j] = xsc[j * 16 + r] * wsc;
     }
     // Tile row i is multiplied while row i - 1's sums are scaled: one matrix
-    // step, then the four multiply-adds that run in its shadow; with fp16
-    // steps also a part of the next row's conversion.
+    // step, then the four multiply-adds that run in its shadow and a part of
+    // the next row's conversion.
     f32x4_t p[2][TM];
     auto scale = [&](int i, int j) {
 #pragma unroll
       for (int q = 0; q < 4; q++)
         acc[i / TN][i % TN][j][q] = __builtin_fmaf(p[i & 1][j][q], sc[i / TN][j], acc[i / TN][i % TN][j][q]);
     };
-    if constexpr (C::EXACT) {
-      F16Block x[TM], w;
-      i32x8_t raw = wfrag(0);
+    F16Block x[TM], w;
+    i32x8_t raw = wfrag(0);
 #pragma unroll
-      for (int j = 0; j < TM; j++) x[j].set(frag(xt, j * 16));
-      w.set(raw);
+    for (int j = 0; j < TM; j++) x[j].set(frag(xt, j * 16));
+    w.set(raw);
 #pragma unroll
-      for (int i = 0; i <= ROWS; i++) {
-        fetch_some(i);
-        F16Block w_next;
-        if (i + 1 < ROWS) raw = wfrag(i + 1);
+    for (int i = 0; i <= ROWS; i++) {
+      fetch_some(i);
+      F16Block w_next;
+      if (i + 1 < ROWS) raw = wfrag(i + 1);
 #pragma unroll
-        for (int j = 0; j < TM; j++) {
-          if (i < ROWS) p[i & 1][j] = mfma_block(w, x[j]);
-          if (i + 1 < ROWS && (j > 0 || TM == 1)) {
-            constexpr int D = TM > 1 ? TM - 1 : 1;
-            const int s0 = TM > 1 ? 4 * (j - 1) / D : 0, s1 = TM > 1 ? 4 * j / D : 4;
+      for (int j = 0; j < TM; j++) {
+        if (i < ROWS) p[i & 1][j] = mfma_block(w, x[j]);
+        if (i + 1 < ROWS && (j > 0 || TM == 1)) {
+          constexpr int D = TM > 1 ? TM - 1 : 1;
+          const int s0 = TM > 1 ? 4 * (j - 1) / D : 0, s1 = TM > 1 ? 4 * j / D : 4;
 #pragma unroll
-            for (int s = s0; s < s1; s++) w_next.s[s] = e4m3_to_f16(raw[2 * s], raw[2 * s + 1]);
-          }
-          if (i > 0) scale(i - 1, j);
-          __builtin_amdgcn_sched_barrier(0);
+          for (int s = s0; s < s1; s++) w_next.s[s] = e4m3_to_f16(raw[2 * s], raw[2 * s + 1]);
         }
-        w = w_next;
+        if (i > 0) scale(i - 1, j);
+        __builtin_amdgcn_sched_barrier(0);
       }
-    } else {
-      i32x8_t x[TM];
-#pragma unroll
-      for (int j = 0; j < TM; j++) x[j] = frag(xt, j * 16);
-      i32x8_t w = wfrag(0);
-#pragma unroll
-      for (int i = 0; i <= ROWS; i++) {
-        fetch_some(i);
-        i32x8_t w_next = w;
-        if (i + 1 < ROWS) w_next = wfrag(i + 1);
-#pragma unroll
-        for (int j = 0; j < TM; j++) {
-          if (i < ROWS) {
-            __builtin_amdgcn_s_setprio(1);  // a wave with a matrix step ready goes before one that scales
-            p[i & 1][j] = mfma_block_e4m3(w, x[j]);
-            __builtin_amdgcn_s_setprio(0);
-          }
-          if (i > 0) scale(i - 1, j);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        w = w_next;
-      }
+      w = w_next;
     }
     stage = stage + 1 == C::STAGES ? 0 : stage + 1;
   }
