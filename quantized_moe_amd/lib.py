@@ -301,6 +301,8 @@ def gate(n_experts: int, top_k: int, score="sigmoid", n_groups=1, top_groups=1, 
     """A gate's description for gate_topk (it keeps the bias tensor alive)."""
     if bias is not None:
         _need("gate", bias=(bias, torch.float32, (n_experts,)))
+        if not bias.is_cuda:
+            _not_on_gpu("gate")
     g = MoeGate(abi_version=MOE_ABI_VERSION, n_experts=n_experts, top_k=top_k, score=_SCORES[score],
                 n_groups=n_groups, top_groups=top_groups, group_score=_GROUP_SCORES[group_score],
                 renormalize=1 if renormalize else 0, scale=scale, bias=_ptr(bias))
@@ -313,6 +315,8 @@ def router_logits(w_router, x, z, stream=None) -> None:
     T = x.shape[0]
     _need("router_logits", w_router=(w_router, torch.float32, (E, d)), x=(x, x.dtype, (T, d)),
           z=(z, torch.float32, (T, E)))
+    if not (w_router.is_cuda and x.is_cuda and z.is_cuda):
+        _not_on_gpu("router_logits")
     _check(lib().moe_router_logits(_ptr(w_router), E, d, _ptr(x), x_dtype_of(x), T, _ptr(z), _stream(stream)))
 
 
