@@ -3,14 +3,15 @@
 // A decode step makes these calls for one token, where the kernels take 3 to 5
 // us: checks and marshalling in Python (3 to 5 us a call) would be what such a
 // call costs, here they take some 0.3 us.  Each function checks what the library
-// takes for granted about its tensors (dtype, shape, strides, memory of the GPU)
-// and calls the entry point of the same name; it returns the status, or None if
+// takes for granted about its tensors (dtype, shape, strides, memory of the
+// current GPU, a stream of it) and calls the entry point of the same name; it returns the status, or None if
 // a tensor is not as it should be (the Python side then says which).
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 
 #include <climits>
@@ -20,11 +21,20 @@
 
 namespace {
 
-// A tensor in GPU memory, or null.
+// The current device, which the library launches on: asked for once a call, and
+// only if there is a tensor of a GPU.  -1: not asked yet.
+thread_local int current = -1;
+int current_device() {
+  if (current < 0) current = c10::hip::current_device();
+  return current;
+}
+
+// A tensor in the current GPU's memory, or null.
 const at::Tensor* tensor(PyObject* o) {
   if (!THPVariable_Check(o)) return nullptr;
   const at::Tensor& t = THPVariable_Unpack(o);
-  return t.defined() && t.layout() == at::kStrided && t.is_cuda() ? &t : nullptr;
+  if (!t.defined() || t.layout() != at::kStrided || !t.is_cuda()) return nullptr;
+  return t.get_device() == current_device() ? &t : nullptr;
 }
 
 bool is_codes(at::ScalarType t) { return t == at::kFloat8_e4m3fn || t == at::kByte; }
@@ -83,6 +93,33 @@ bool workspace_of(PyObject* o, void** p, size_t* bytes) {
   return true;
 }
 
+// The value of attribute `name`, or null (no error) where there is none.
+PyObject* attribute(PyObject* o, const char* name) {
+  PyObject* v = PyObject_GetAttrString(o, name);
+  if (!v) PyErr_Clear();
+  return v;
+}
+
+// Not a stream of another device (an object that names no device is taken).
+bool stream_here(PyObject* o) {
+  if (o == Py_None) return true;
+  PyObject* v = attribute(o, "device_index");
+  if (!v) return true;
+  const long index = PyLong_Check(v) ? PyLong_AsLong(v) : current_device();
+  Py_DECREF(v);
+  return index == current_device();
+}
+
+// A gate's bias, which the description holds by address, is of this device (a
+// description that gate() did not make keeps no tensor to look at).
+bool bias_here(PyObject* gate) {
+  PyObject* v = attribute(gate, "bias_tensor");
+  if (!v) return true;
+  const bool here = v == Py_None || tensor(v);
+  Py_DECREF(v);
+  return here;
+}
+
 // None: torch's current stream; else an object with torch.cuda.Stream's handle.
 bool stream_of(PyObject* o, void** s) {
   if (o == Py_None) {
@@ -112,6 +149,7 @@ PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
     PyErr_Format(PyExc_TypeError, "%d arguments needed, not %zd", N, n);
     return nullptr;
   }
+  current = -1;
   try {
     return F(a);
   } catch (const std::exception& e) {
@@ -131,7 +169,8 @@ PyObject* gate_topk(PyObject* const* a) {
   Rows z;
   void *idx, *wt, *s;
   if (!sized || !rows_of(a[1], &z) || float_type(z.type) < 0 || z.cols != g.n_experts ||
-      !whole(a[2], at::kInt, {z.rows, g.top_k}, &idx) || !whole(a[3], at::kFloat, {z.rows, g.top_k}, &wt))
+      !whole(a[2], at::kInt, {z.rows, g.top_k}, &idx) || !whole(a[3], at::kFloat, {z.rows, g.top_k}, &wt) ||
+      (g.bias && !bias_here(a[0])) || !stream_here(a[4]))
     Py_RETURN_NONE;
   if (!stream_of(a[4], &s)) return nullptr;
   return call([&] {
@@ -144,7 +183,7 @@ PyObject* quantize(PyObject* const* a) {
   Rows x, q;
   void *sc, *s;
   if (!rows_of(a[0], &x) || float_type(x.type) < 0 || !rows_of(a[1], &q) || !is_codes(q.type) || q.rows != x.rows ||
-      q.cols != x.cols || !whole(a[2], at::kFloat, {x.rows, blocks(x.cols)}, &sc))
+      q.cols != x.cols || !whole(a[2], at::kFloat, {x.rows, blocks(x.cols)}, &sc) || !stream_here(a[3]))
     Py_RETURN_NONE;
   if (!stream_of(a[3], &s)) return nullptr;
   return call([&] {
@@ -164,7 +203,8 @@ PyObject* matmul(PyObject* const* a) {
     Py_RETURN_NONE;
   const int64_t N = w[0], K = x.cols;
   if (!whole(a[1], at::kFloat, {x.rows, blocks(K)}, &xs) || !whole(a[2], at::kByte, {N, K}, &wq) ||
-      !whole(a[3], at::kFloat, {blocks(N), blocks(K)}, &ws) || !workspace_of(a[5], &work, &work_bytes))
+      !whole(a[3], at::kFloat, {blocks(N), blocks(K)}, &ws) || !workspace_of(a[5], &work, &work_bytes) ||
+      !stream_here(a[6]))
     Py_RETURN_NONE;
   if (!stream_of(a[6], &s)) return nullptr;
   return call([&] {
@@ -186,7 +226,8 @@ PyObject* gateup(PyObject* const* a) {
       !whole(a[3], at::kInt, {E + 1}, &offsets) || !whole(a[4], at::kInt, {R}, &perm) ||
       !whole(a[5], at::kByte, {E, f, d}, &wg) || !whole(a[6], at::kFloat, {E, FB, DB}, &sg) ||
       !whole(a[7], at::kByte, {E, f, d}, &wu) || !whole(a[8], at::kFloat, {E, FB, DB}, &su) ||
-      !whole(a[9], at::kByte, {R, f}, &hq) || !whole(a[10], at::kFloat, {R, FB}, &hs))
+      !whole(a[9], at::kByte, {R, f}, &hq) || !whole(a[10], at::kFloat, {R, FB}, &hs) ||
+      !stream_here(a[11]))
     Py_RETURN_NONE;
   if (!stream_of(a[11], &s)) return nullptr;
   return call([&] {
@@ -208,7 +249,8 @@ PyObject* down(PyObject* const* a) {
       !whole(a[2], at::kFloat, {T, k}, &wt) || !whole(a[3], at::kInt, {E + 1}, &offsets) ||
       !whole(a[4], at::kInt, {R}, &pos) || !whole(a[5], at::kByte, {E, d, f}, &wd) ||
       !whole(a[6], at::kFloat, {E, DB, FB}, &sd) || !whole(a[7], at::kFloat, {T, d}, &y) ||
-      !workspace_of(a[8], &work, &work_bytes) || (a[9] != Py_None && !whole(a[9], at::kFloat, {T, d}, &add)))
+      !workspace_of(a[8], &work, &work_bytes) || (a[9] != Py_None && !whole(a[9], at::kFloat, {T, d}, &add)) ||
+      !stream_here(a[10]))
     Py_RETURN_NONE;
   if (!stream_of(a[10], &s)) return nullptr;
   return call([&] {

@@ -257,10 +257,21 @@ def _load_calls():
     return module
 
 
-def _not_on_gpu(fn: str, workspace=None) -> None:
+def _not_here(fn: str, *tensors, workspace=None) -> None:
+    """Raises for tensors whose shapes and dtypes are right, but not the place."""
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError(f"{fn}: the workspace must be contiguous")
-    raise ValueError(f"{fn}: every tensor must be in GPU memory")
+    if not all(t.is_cuda for t in (*tensors, workspace) if t is not None):
+        raise ValueError(f"{fn}: every tensor must be in GPU memory")
+    raise ValueError(f"{fn}: every tensor and the stream must be of the current device, cuda:{torch.cuda.current_device()}")
+
+
+def _check_here(fn: str, stream, *tensors) -> None:
+    if not all(t.is_cuda for t in tensors):
+        _not_here(fn, *tensors)
+    here = torch.cuda.current_device()
+    if any(t.get_device() != here for t in tensors) or getattr(stream, "device_index", here) != here:
+        _not_here(fn, *tensors)
 
 
 def _need(fn: str, **tensors) -> None:
@@ -302,7 +313,7 @@ def gate(n_experts: int, top_k: int, score="sigmoid", n_groups=1, top_groups=1, 
     if bias is not None:
         _need("gate", bias=(bias, torch.float32, (n_experts,)))
         if not bias.is_cuda:
-            _not_on_gpu("gate")
+            _not_here("gate", bias)
     g = MoeGate(abi_version=MOE_ABI_VERSION, n_experts=n_experts, top_k=top_k, score=_SCORES[score],
                 n_groups=n_groups, top_groups=top_groups, group_score=_GROUP_SCORES[group_score],
                 renormalize=1 if renormalize else 0, scale=scale, bias=_ptr(bias))
@@ -315,8 +326,7 @@ def router_logits(w_router, x, z, stream=None) -> None:
     T = x.shape[0]
     _need("router_logits", w_router=(w_router, torch.float32, (E, d)), x=(x, x.dtype, (T, d)),
           z=(z, torch.float32, (T, E)))
-    if not (w_router.is_cuda and x.is_cuda and z.is_cuda):
-        _not_on_gpu("router_logits")
+    _check_here("router_logits", stream, w_router, x, z)
     _check(lib().moe_router_logits(_ptr(w_router), E, d, _ptr(x), x_dtype_of(x), T, _ptr(z), _stream(stream)))
 
 
@@ -328,7 +338,7 @@ def gate_topk(gate: MoeGate, z, idx, wt, stream=None) -> None:
         if E != gate.n_experts:
             raise ValueError(f"gate_topk: z has {E} logits per row, the gate {gate.n_experts} experts")
         _need("gate_topk", idx=(idx, torch.int32, (T, gate.top_k)), wt=(wt, torch.float32, (T, gate.top_k)))
-        _not_on_gpu("gate_topk")
+        _not_here("gate_topk", z, idx, wt)
     if rc:
         _check(rc)
 
@@ -343,7 +353,7 @@ def blockscale_quantize(x, q, s, stream=None) -> None:
         if q.shape != x.shape:
             raise ValueError(f"{fn}: q has shape {tuple(q.shape)}, needs {tuple(x.shape)}")
         _need(fn, s=(s, torch.float32, (M, scale_blocks(K))))
-        _not_on_gpu(fn)
+        _not_here(fn, x, q, s)
     if rc:
         _check(rc)
 
@@ -366,7 +376,7 @@ def blockscale_matmul(xq, xs, wq, ws, y, workspace=None, stream=None) -> None:
         if y.shape != (M, N):
             raise ValueError(f"{fn}: y has shape {tuple(y.shape)}, needs {(M, N)}")
         _need(fn, xs=(xs, torch.float32, (M, KB)), wq=(wq, torch.uint8, (N, K)), ws=(ws, torch.float32, (NB, KB)))
-        _not_on_gpu(fn, workspace)
+        _not_here(fn, xq, xs, wq, ws, y, workspace=workspace)
     if rc:
         _check(rc)
 
@@ -384,7 +394,7 @@ def blockscale_gateup(xq, xs, k, offsets, perm, w_gate, s_gate, w_up, s_up, hq, 
               w_gate=(w_gate, torch.uint8, (E, f, d)), s_gate=(s_gate, torch.float32, (E, FB, DB)),
               w_up=(w_up, torch.uint8, (E, f, d)), s_up=(s_up, torch.float32, (E, FB, DB)),
               hq=(hq, torch.uint8, (R, f)), hs=(hs, torch.float32, (R, FB)))
-        _not_on_gpu(fn)
+        _not_here(fn, xq, xs, offsets, perm, w_gate, s_gate, w_up, s_up, hq, hs)
     if rc:
         _check(rc)
 
@@ -408,7 +418,7 @@ def blockscale_down(hq, hs, wt, offsets, pos, w_down, s_down, y, workspace, add=
               y=(y, torch.float32, (T, d)))
         if add is not None:
             _need(fn, add=(add, torch.float32, (T, d)))
-        _not_on_gpu(fn, workspace)
+        _not_here(fn, hq, hs, wt, offsets, pos, w_down, s_down, y, add, workspace=workspace)
     if rc:
         _check(rc)
 

@@ -30,3 +30,45 @@ def test_layer_refuses_host_memory():
                                        max_tokens=4)
     with pytest.raises(ValueError, match="GPU memory"):
         layer.forward(torch.zeros(3, 256), torch.zeros(3, 256), stream=_NoStream)
+
+
+@pytest.mark.gpu
+def test_streams_of_another_device_are_refused():
+    """A launch on another device's stream would read this device's memory from there."""
+    dev = "cuda:0"
+
+    class Elsewhere:  # (its handle is this device's default stream: the calls would run)
+        cuda_stream = 0
+        device_index = 1
+
+    def f(*n):
+        return torch.zeros(*n, device=dev)
+
+    def u8(*n):
+        return torch.zeros(*n, dtype=torch.uint8, device=dev)
+
+    def i32(*n):
+        return torch.zeros(*n, dtype=torch.int32, device=dev)
+
+    g = lib.gate(8, 2, bias=f(8))
+    w, x, z, idx, wt, y, y2 = f(8, 256), f(4, 256), f(4, 8), i32(4, 2), f(4, 2), f(4, 128), f(4, 256)
+    xq, xs, hq, hs, offsets, perm, pos = u8(4, 256), f(4, 2), u8(8, 128), f(8, 1), i32(9), i32(8), i32(8)
+    wg, sg, wd, sd = u8(8, 128, 256), f(8, 1, 2), u8(8, 256, 128), f(8, 2, 1)
+    work = u8(lib.blockscale_down_workspace_bytes(4, 2, 256))
+    calls = [
+        lambda s: lib.router_logits(w, x, z, stream=s),
+        lambda s: lib.gate_topk(g, z, idx, wt, stream=s),
+        lambda s: lib.blockscale_quantize(x, xq, xs, stream=s),
+        lambda s: lib.blockscale_matmul(xq, xs, wg[0], sg[0], y, stream=s),
+        lambda s: lib.blockscale_gateup(xq, xs, 2, offsets, perm, wg, sg, wg, sg, hq, hs, stream=s),
+        lambda s: lib.blockscale_down(hq, hs, wt, offsets, pos, wd, sd, y2, work, stream=s),
+    ]
+    side = torch.cuda.Stream()
+    for call in calls:
+        torch.cuda.synchronize()
+        with pytest.raises(ValueError, match="current device, cuda:0"):
+            call(Elsewhere)
+        call(side)
+        torch.cuda.synchronize()
+        call(None)
+    torch.cuda.synchronize()
