@@ -90,20 +90,25 @@ __device__ __forceinline__ f32x4_t mfma_block(const F16Block& w, const F16Block&
 
 // Asynchronous copies from a buffer straight into LDS: lane l's 16 (or 4)
 // bytes at off + soff land at LDS byte address lds + 16 l (4 l); a lane whose
-// off is outside the buffer gets zeros.  Written out because the compiler cannot tell the LDS buffers of
-// a pipeline apart and would wait for every copy in flight before each read of
-// LDS.  They have no output registers; the waits are lds_landed() below.  (m0
-// holds the address; nothing else in these kernels uses m0.)
+// off is outside the buffer gets zeros.  Written out because the compiler cannot
+// tell the LDS buffers of a pipeline apart and would wait for every copy in
+// flight before each read of LDS.  They have no output registers; the waits are
+// lds_landed() below.  m0 holds the address (the compiler, which sets it anew
+// before each use of its own, notes that it is not preserved).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void lds_copy16(__amdgpu_buffer_rsrc_t r, uint32_t lds, uint32_t off, uint32_t soff) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                ::"s"(lds), "v"(off), "s"(r), "s"(soff)
-               : "memory");
+               : "memory", "m0");
 }
 __device__ __forceinline__ void lds_copy4(__amdgpu_buffer_rsrc_t r, uint32_t lds, uint32_t off, uint32_t soff) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
                ::"s"(lds), "v"(off), "s"(r), "s"(soff)
-               : "memory");
+               : "memory", "m0");
 }
+#pragma clang diagnostic pop
+
 // All but the N youngest copies of this wave have landed, its reads of LDS are
 // done, and so it is for every wave of the block.
 template <int N>
