@@ -528,9 +528,9 @@ int moe_gate_topk(const moe_gate* G, const void* z, int32_t z_dtype, int64_t z_s
  * enters NaN.  Identical inputs give bitwise identical outputs.
  *
  * Limits: K (inputs) a multiple of 16 in [16, 16384]; N (outputs) in [1,
- * 65536] with N * K < 2^31; M in [0, 2^20] rows; q pointers 16-byte aligned,
- * their row strides multiples of 16 bytes; outputs, scales and int32 arrays
- * 16-byte aligned.  M = 0 and T = 0 are valid no-ops.
+ * 65536]; M in [0, 2^20] rows; q pointers 16-byte aligned, their row strides
+ * multiples of 16 bytes; outputs, scales and int32 arrays 16-byte aligned.
+ * M = 0 and T = 0 are valid no-ops.
  */
 
 /*

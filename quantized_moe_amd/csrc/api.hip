@@ -989,10 +989,9 @@ static int check_bs_rows(const char* fn, int M) {
   return MOE_OK;
 }
 
-static int check_bs_outputs(const char* fn, int N, int K) {
+static_assert((int64_t)BS_MAX_N * BS_MAX_K < (int64_t(1) << 31), "weights are addressed with 31-bit byte offsets");
+static int check_bs_outputs(const char* fn, int N) {
   if (N < 1 || N > BS_MAX_N) return fail(MOE_ERR_INVALID_ARG, "%s: N %d not in [1, %d]", fn, N, BS_MAX_N);
-  if ((int64_t)N * K >= (int64_t(1) << 31))
-    return fail(MOE_ERR_INVALID_ARG, "%s: N %d by K %d is not below 2^31 weights", fn, N, K);
   return MOE_OK;
 }
 
@@ -1030,7 +1029,7 @@ extern "C" int moe_blockscale_matmul_workspace_bytes(int32_t M, int32_t N, int32
   const char* fn = "moe_blockscale_matmul_workspace_bytes";
   if (!bytes) return fail(MOE_ERR_INVALID_ARG, "%s: bytes is null", fn);
   int rc;
-  if ((rc = check_bs_rows(fn, M)) || (rc = check_bs_k(fn, "K", K)) || (rc = check_bs_outputs(fn, N, K))) return rc;
+  if ((rc = check_bs_rows(fn, M)) || (rc = check_bs_k(fn, "K", K)) || (rc = check_bs_outputs(fn, N))) return rc;
   *bytes = bs_matmul_ws(M, N, K);
   return ok();
 }
@@ -1040,7 +1039,7 @@ extern "C" int moe_blockscale_matmul(const uint8_t* xq, int64_t ldx, const float
                                      void* workspace, size_t workspace_bytes, void* stream) {
   const char* fn = "moe_blockscale_matmul";
   int rc;
-  if ((rc = check_bs_rows(fn, M)) || (rc = check_bs_k(fn, "K", K)) || (rc = check_bs_outputs(fn, N, K))) return rc;
+  if ((rc = check_bs_rows(fn, M)) || (rc = check_bs_k(fn, "K", K)) || (rc = check_bs_outputs(fn, N))) return rc;
   if (y_dtype != MOE_F32 && y_dtype != MOE_BF16)
     return fail(MOE_ERR_UNSUPPORTED, "%s: unknown output dtype %d", fn, y_dtype);
   if (ldx < K || ldx % 16 != 0 || ldx > BS_MAX_LDX)

@@ -72,3 +72,32 @@ def test_streams_of_another_device_are_refused():
         torch.cuda.synchronize()
         call(None)
     torch.cuda.synchronize()
+
+
+def test_largest_weight_is_taken():
+    """65536 x 16384, every weight below 2^31 bytes: no limit besides those of N and K."""
+    assert lib.blockscale_matmul_workspace_bytes(4, 65536, 16384) == 0
+    for n, k in ((65537, 16384), (65536, 16400)):
+        with pytest.raises(lib.MoeError, match="N 65537|K 16400"):
+            lib.blockscale_matmul_workspace_bytes(4, n, k)
+
+
+def test_workspaces_that_are_needed_and_not():
+    """Few outputs of a long K take partial sums, the routed products of three tokens on their rows; else nothing."""
+    P = 1 << 40  # a pointer that is never dereferenced: every call below is refused
+    L = lib.lib()
+    for M, N, K in ((64, 64, 16384), (300, 128, 16384), (33, 1, 4096)):
+        need = lib.blockscale_matmul_workspace_bytes(M, N, K)
+        assert need > 0 and need % (4 * M * N) == 0
+        args = (P, K, P, M, P, P, N, K, P, 0, N)
+        assert L.moe_blockscale_matmul(*args, P, need - 1, None) == lib.MOE_ERR_WORKSPACE
+        assert L.moe_blockscale_matmul(*args, None, need, None) == lib.MOE_ERR_INVALID_ARG
+    for M, N, K in ((1, 64, 16384), (32, 64, 16384), (64, 64, 3968), (4096, 4096, 16384)):
+        assert lib.blockscale_matmul_workspace_bytes(M, N, K) == 0
+    for T in (1, 2):
+        assert lib.blockscale_down_workspace_bytes(T, 6, 4096) == 0
+    need = lib.blockscale_down_workspace_bytes(3, 2, 256)
+    assert need == 3 * 2 * 256 * 4
+    args = (P, P, 3, 2, P, P, P, 8, P, P, 256, 256, None, P)
+    assert L.moe_blockscale_down(*args, P, need - 1, None) == lib.MOE_ERR_WORKSPACE
+    assert L.moe_blockscale_down(*args, None, need, None) == lib.MOE_ERR_INVALID_ARG
