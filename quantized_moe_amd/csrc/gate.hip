@@ -64,8 +64,10 @@ __device__ __forceinline__ float max_of(const float (&v)[N]) {
 }
 
 // 1 / x correctly rounded for x in [1, 2^117]: the hardware's reciprocal is off
-// by one unit at most, and a Newton step with its residual from a fused
-// multiply-add leaves the nearest fp32 number (checked for every significand).
+// by one unit at most, and two Newton steps with residuals from fused
+// multiply-adds leave the nearest fp32 number from any such start (tested on the
+// CPU for every significand), but for x = 2 - 2^-23, whose start has to be the
+// nearest and is (tested on the GPU: the score of every logit, bit for bit).
 // 5 instructions where the general IEEE division takes 10.
 __device__ __forceinline__ float recip_exact(float x) {
   float r = __builtin_amdgcn_rcpf(x);
