@@ -525,7 +525,11 @@ int moe_gate_topk(const moe_gate* G, const void* z, int32_t z_dtype, int64_t z_s
  * block of 128 on the matrix units (the codes as fp16, which holds them
  * exactly), then one fused multiply-add per block with the product of the
  * two scales.  A code or scale that is not a number makes the outputs that it
- * enters NaN.  Identical inputs give bitwise identical outputs.
+ * enters NaN.  Identical inputs give bitwise identical outputs.  The order in
+ * which the blocks are added goes by the sizes of a call: a row's last bits may
+ * differ between products of different M, and a token's between
+ * moe_blockscale_down of one or two tokens and of more.  Quantisation, the gate
+ * and moe_blockscale_gateup give a row the same bits in every batch.
  *
  * Limits: K (inputs) a multiple of 16 in [16, 16384]; N (outputs) in [1,
  * 65536]; M in [0, 2^20] rows; q pointers 16-byte aligned, their row strides

@@ -200,9 +200,10 @@ __global__ __launch_bounds__(256) void bs_combine_kernel(BsDown a) {
 }
 
 // One or two tokens: one launch and no workspace.  A block owns 16 outputs of
-// one token; its 16 waves share the K blocks (and, where those are fewer, the
-// routes), straight from memory with U routes requested at a time: one round trip
-// at 8 routes of 2048 inputs.  Column j of the matrix steps' activations is route
+// one token; its 16 waves share the K blocks (and, where two groups of waves or
+// more have one for each, the routes), straight from memory with U routes
+// requested at a time.  With U = 6 and more than 1024 inputs up to 6 routes are
+// one round trip for each 2048 inputs, 7 to 12 are two and 13 to 16 three.  Column j of the matrix steps' activations is route
 // j's row, for all routes at once; of the product with route j's weights column j
 // is kept, so that a lane needs its own route's scales only and one accumulator
 // serves every route.  The waves' sums are added in their order, then the routes

@@ -153,3 +153,29 @@ def test_down_values(T, k, E, d, f, kind):
     tol = SUM(f) * (w * ym[at]).sum(1) + (k + 2) * 2.0 ** -23 * (w * ye[at].abs()).sum(1)
     err = (y.cpu().double() - ref).abs()
     assert (err <= tol).all(), float((err / tol.clamp(min=1e-300)).max())
+
+
+@gpu
+def test_a_token_has_the_same_bits_in_every_batch():
+    """Gate/up in every tile, and down of three tokens and more: the first tokens of the largest batch by themselves."""
+    k, E, d, f, most = 2, 6, 400, 272, 8200
+    rng = np.random.default_rng(17)
+    idx = torch.from_numpy(np.argsort(rng.random((most, E)), axis=1)[:, :k].astype(np.int32))
+    (xq, xs), (wg, sg), (wu, su), (wd, sd) = make_rows(rng, most, d), *(make_weight(rng, *s, E) for s in ((f, d), (f, d), (d, f)))
+    wt = torch.from_numpy(rng.random((most, k), np.float32))
+    want = None
+    for T in (most, 700, 300, 30, 10, 3, 2, 1):
+        offsets, perm, pos = buckets(idx[:T], E)
+        hq = torch.empty(T * k, f, dtype=torch.uint8, device=DEV)
+        hs = torch.empty(T * k, nb(f), device=DEV)
+        y = torch.empty(T, d, device=DEV)
+        work = torch.empty(max(16, lib.blockscale_down_workspace_bytes(T, k, d)), dtype=torch.uint8, device=DEV)
+        lib.blockscale_gateup(up(xq[:T]), up(xs[:T]), k, up(offsets), up(perm), up(wg), up(sg), up(wu), up(su), hq, hs)
+        lib.blockscale_down(hq, hs, up(wt[:T]), up(offsets), up(pos), up(wd), up(sd), y, work)
+        at = pos.long().to(DEV)
+        have = hq[at], hs[at], y  # (by route, by route, by token)
+        if want is None:
+            want = have
+        assert torch.equal(have[0], want[0][: T * k]) and torch.equal(have[1], want[1][: T * k])
+        if T > 2:
+            assert torch.equal(y, want[2][:T])
