@@ -29,9 +29,10 @@ def quantize_weight(w: torch.Tensor):
 class BlockScaleLayer:
     """y = sum_j wt_j * expert_j(x) (+ shared(x)) for up to max_tokens tokens.
 
-    w_router fp32 [E][d]; gate: a lib.gate() description; each of w_gate, w_up
-    [E][f][d] and w_down [E][d][f] a (codes, scales) pair as quantize_weight
-    returns it; shared: None or such pairs of one expert, (gate, up, down) of
+    w_router fp32 [E][d], d a power of two in [256, 8192] (router_logits' limits);
+    gate: a lib.gate() description; each of w_gate, w_up [E][f][d] and w_down
+    [E][d][f] a (codes, scales) pair as quantize_weight returns it; shared: None or
+    such pairs of one expert, (gate, up, down) of
     [f_s][d], [f_s][d], [d][f_s].  Buffers are allocated here, once; forward
     allocates nothing and its calls can be captured into a graph.  One call at
     a time: calls on several streams need a layer object each.

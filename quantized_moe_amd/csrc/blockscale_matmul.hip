@@ -194,22 +194,25 @@ static hipError_t launch_rows(const BsMatmul& a, hipStream_t s) {
 }
 
 // The variant: by rows, then the largest tile of which there are enough for
-// the 256 CUs.  Measured on both sides of each step, N = K = 4096 unless
-// given (us):
-//   M 32: rows 9.8, 64 x 64 tiles 14.9;   64: rows 15.3, tiles 14.9
+// the 256 CUs.  Measured on both sides of each step, N = K = 4096 and fp32
+// outputs unless given (us; bf16 outputs take up to 4 % less):
+//   M 32: rows 9.9;  33: 64 x 64 tiles 9.8;  64: rows 15.3, tiles 10.4
 //   M 32, 32 outputs a block instead of 16: 11.1 and 9.9, at N = K = 8192 22.6 and 30.2
-//   M 128 (64 tiles of 128 x 64): 20.2 on them, 15.2 on 64 x 64
+//   M 128 (64 tiles of 128 x 64): 20.2 on them, 15.2 on 64 x 64, whose K is
+//     shared besides: 12.6
 //   M 1000, N 1100, K 2064 (144): 15.3 on 128 x 64, 19.3 on 64 x 64 (288: a
 //     second round of few), 13.0 on 64 x 96 (198); 700 x 1500 x 1040 9.6 and
 //     8.3, but M 512 (384 tiles of 64 x 96) 23.5 and 34.3
 //   64 x 64 and 64 x 96 with three groups and two stages, and with two groups:
 //     512 x 2048 x 4096 14.8 and 15.4, 512 x 1024 x 1040 6.4 and 7.0, 64 x
 //     4096 x 2048 8.7 and 9.3; 64 x 96 13.0 and 13.6, 1500 x 700 x 8192 30.9 and 32.7
-//   M 512 (128 tiles of 128 x 128): 32.0 on them, 22.6 on 128 x 64
+//   M 512 (128 tiles of 128 x 128): 32.0 on them, 21.9 to 22.6 on 128 x 64
 //   M 1024 (256): 34.6 on 128 x 128 with two groups, 38.4 with one group and
 //     two stages, 42.6 on 128 x 64
 //   M 2048 (512): 71.0 with one group and two stages, 66.9 with two groups
 //   M 4096 (1024): 123 on 128 x 128, 132 with two groups
+//   M = N = K = 8192 to bf16: 914 to 927 (1.2 PFLOP/s; the library's 16-bit
+//     product of 8192^3, without scales, reaches 1.46)
 template <typename OUT>
 static hipError_t launch_matmul(const BsMatmul& a, hipStream_t s) {
   if (a.M <= 16) return launch_rows<1, 1, 4, OUT>(a, s);
