@@ -178,10 +178,14 @@ static hipError_t launch_tile(const BsMatmul& a, hipStream_t s, int parts = 1) {
   int per_cu, cus;
   hipError_t e = launch_shape((const void*)k, C::THREADS, C::LDS, C::LDS, &per_cu, &cus);
   if (e != hipSuccess) return e;
+  int pid = prof_begin("bs_matmul", s);
   QMOE_LAUNCH(k, dim3((unsigned)(n_tiles * m_tiles), parts), dim3(C::THREADS), C::LDS, s, a, n_tiles, m_tiles);
+  prof_end(pid, s);
   if (parts > 1) {
     if ((e = hipGetLastError()) != hipSuccess) return e;
+    pid = prof_begin("bs_matmul_sum", s);
     QMOE_LAUNCH(bs_matmul_sum_kernel<OUT>, dim3((unsigned)(((int64_t)a.M * a.N + 255) / 256)), dim3(256), 0, s, a, parts);
+    prof_end(pid, s);
   }
   return hipGetLastError();
 }
@@ -189,7 +193,9 @@ static hipError_t launch_tile(const BsMatmul& a, hipStream_t s, int parts = 1) {
 template <int TN, int TM, int U, typename OUT>
 static hipError_t launch_rows(const BsMatmul& a, hipStream_t s) {
   auto* k = bs_matmul_rows_kernel<TN, TM, U, OUT>;
+  const int pid = prof_begin("bs_matmul", s);
   QMOE_LAUNCH(k, dim3((a.N + 16 * TN - 1) / (16 * TN)), dim3(512), 0, s, a);
+  prof_end(pid, s);
   return hipGetLastError();
 }
 
@@ -230,10 +236,7 @@ static hipError_t launch_matmul(const BsMatmul& a, hipStream_t s) {
 }
 
 hipError_t launch_bs_matmul(const BsMatmul& a, hipStream_t s) {
-  const int pid = prof_begin("bs_matmul", s);
-  const hipError_t e = a.y_dtype == X_BF16 ? launch_matmul<uint16_t>(a, s) : launch_matmul<float>(a, s);
-  prof_end(pid, s);
-  return e;
+  return a.y_dtype == X_BF16 ? launch_matmul<uint16_t>(a, s) : launch_matmul<float>(a, s);
 }
 
 }  // namespace qmoe
