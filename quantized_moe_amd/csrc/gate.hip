@@ -344,7 +344,7 @@ __global__ __launch_bounds__(256) void gate_kernel(GateLaunch a, int lg_, int gr
           "v_cndmask_b32 %0, %0, %1, %6\n\tv_cndmask_b32 %1, %1, %2, %6\n\t"
           "v_cndmask_b32 %2, %2, %3, %6\n\tv_cndmask_b32 %3, %3, %9, %6\n\t"
           "v_writelane_b32 %4, %7, %8\n\tv_writelane_b32 %5, %10, %8"
-          : "+v"(q[0]), "+v"(q[1]), "+v"(q[2]), "+v"(q[3]), "+v"(my_v), "+v"(my_lane)
+          : "+&v"(q[0]), "+&v"(q[1]), "+&v"(q[2]), "+&v"(q[3]), "+v"(my_v), "+v"(my_lane)
           : "s"(has), "s"(b), "n"(r), "v"(-INFINITY), "s"((int)__builtin_ctzll(has)));
       return true;
     };

@@ -23,3 +23,37 @@ def test_asm_that_writes_m0_says_so():
     assert writers
     for name, s in writers:
         assert '"m0"' in s.split("::")[-1], (name, s)
+
+
+def operands(statement):
+    """(instructions, [(constraint, is an output)]) of an asm statement."""
+    strings = re.compile(r'"((?:[^"\\]|\\.)*)"')
+    template, at = "", 0
+    while True:  # the literals (and macro arguments) before the first colon outside of one
+        m, colon = strings.search(statement, at), statement.find(":", at)
+        if m is None or (0 <= colon < m.start()):
+            break
+        template += m.group(1)
+        at = m.end()
+    rest = statement[at:]
+    found = re.findall(r'"([^"]*)"\s*\(', rest)
+    instructions = [i for i in re.split(r"\\n\\t|\\n|\\t", template) if i.strip()]
+    return instructions, found
+
+
+def test_asm_outputs_written_before_an_input_is_read_have_registers_of_their_own():
+    """Without '&' the compiler may give such an output the register of an input that is still needed."""
+    seen = 0
+    for name, s in asm_statements():
+        instructions, constraints = operands(s)
+        uses = [re.findall(r"%(\d+)", i) for i in instructions]
+        inputs = [i for i, c in enumerate(constraints) if c[:1] not in "=+" and "v" in c]
+        for o, c in enumerate(constraints):
+            if c[:1] not in "=+" or "v" not in c:
+                continue
+            writes = [n for n, u in enumerate(uses) if u and int(u[0]) == o]
+            reads = [n for n, u in enumerate(uses) if any(int(x) in inputs for x in u[1:])]
+            seen += 1
+            if writes and reads and writes[0] < reads[-1]:
+                assert "&" in c, (name, o, instructions)
+    assert seen > 10
