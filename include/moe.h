@@ -597,6 +597,132 @@ int moe_blockscale_down(const uint8_t* hq, const float* hs, int32_t T, int32_t k
                         size_t workspace_bytes, void* stream);
 
 /*
+ * -------------------------------------------------------------------------
+ * int8 operators: a scale per token and per output channel
+ * -------------------------------------------------------------------------
+ * Matrices of signed bytes with one fp32 scale per row:
+ *   activations  q [M][K], s fp32 [M]: value = q * s[m]   (a row is a token)
+ *   weights      q [N][K], s fp32 [N]: value = q * s[n]   (a row is an output channel)
+ * Tensors of several experts are such matrices back to back, [E][N][K] and
+ * [E][N].  These are the layouts in which checkpoints with 8-bit integer weights
+ * and activations come, so nothing is repacked.
+ *
+ * Every product is
+ *   y[m][n] = (fp32(sum_i xq[m][i] wq[n][i]) * xs[m]) * ws[n]
+ * with the sum exact in 32-bit integers (|sum| <= 2^14 K <= 2^28), rounded once
+ * to fp32, and two fp32 products: a row's bits do not depend on the batch that it
+ * comes in, nor on how a call is split.  A scale that is not a number makes the
+ * outputs that it enters NaN.
+ *
+ * Limits: as for the block-scaled operators (K a multiple of 16 in [16, 16384];
+ * N in [1, 65536]; M in [0, 2^20] rows; q pointers 16-byte aligned, their row
+ * strides multiples of 16 bytes; outputs, scales and int32 arrays 16-byte
+ * aligned; M = 0 and T = 0 are valid no-ops).
+ */
+
+/*
+ * Activations to int8: per row
+ *   s = max(max|x|, 2^-100) / 127,  q = x / s rounded to whole numbers
+ * (fp32 divisions, halves to even).  A row that holds a NaN or an infinity gets
+ * s = NaN and codes 0.  x [M] rows of K in x_dtype (MOE_F32 or MOE_BF16), ldx
+ * elements apart (rows 16-byte aligned); q [M] rows ldq bytes apart; s [M].
+ */
+int moe_int8_quantize(const void* x, int32_t x_dtype, int64_t ldx, int32_t M, int32_t K,
+                      int8_t* q, int64_t ldq, float* s, void* stream);
+
+/*
+ * y [M] rows of N in y_dtype (MOE_F32 or MOE_BF16, rounded once more), ldy
+ * elements apart (rows aligned to their element); xq [M] rows ldx bytes apart (at
+ * most 2^22); wq [N][K].  Workspace: moe_int8_matmul_workspace_bytes of the same
+ * M, N, K (null if that is 0): partial sums where few outputs share a long K.
+ */
+int moe_int8_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K, size_t* bytes);
+int moe_int8_matmul(const int8_t* xq, int64_t ldx, const float* xs, int32_t M,
+                    const int8_t* wq, const float* ws, int32_t N, int32_t K, void* y,
+                    int32_t y_dtype, int64_t ldy, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+/*
+ * The routed experts' gate and up products with SwiGLU: for every bucket row r of
+ * expert e (offsets[e] <= r < offsets[e + 1], offsets and perm as moe_bucket
+ * writes them for T tokens of k routes) with token t = perm[r] / k
+ *   h[r] = silu(G_e x_t) * (U_e x_t)    (silu with the hardware's exponential and
+ * reciprocal, a few ulp).  xq [T][d], xs [T]; w_gate, w_up [E][f][d] with scales
+ * [E][f]; h [T*k][f] in h_dtype (MOE_F32 or MOE_BF16, rounded once): rows from
+ * offsets[E] on are not written.  moe_int8_quantize of h gives the down
+ * product's codes, one scale for a whole row.  d and f obey the limits of K.
+ */
+int moe_int8_gateup(const int8_t* xq, const float* xs, int32_t T, int32_t k,
+                    const int32_t* offsets, const int32_t* perm, int32_t E,
+                    const int8_t* w_gate, const float* s_gate, const int8_t* w_up,
+                    const float* s_up, int32_t f, int32_t d, void* h, int32_t h_dtype,
+                    void* stream);
+
+/*
+ * The routed experts' down products and each token's weighted sum:
+ *   y[t] = add[t] + sum_j wt[t][j] * (D_e h)[pos[t*k + j]]
+ * in the order of j, one fp32 multiply-add each, where bucket row r belongs to
+ * expert e as above and routes with pos = T*k (no place) add nothing; add [T][d] is
+ * nullable (no term) and may be y itself.  hq [T*k][f], hs [T*k]; w_down
+ * [E][d][f] with scales [E][d]; y fp32 [T][d].  Workspace:
+ * moe_int8_down_workspace_bytes of the same T, k, d (null if that is 0, as it is
+ * for one and two tokens): the routes' products in fp32.
+ */
+int moe_int8_down_workspace_bytes(int32_t T, int32_t k, int32_t d, size_t* bytes);
+int moe_int8_down(const int8_t* hq, const float* hs, int32_t T, int32_t k, const float* wt,
+                  const int32_t* offsets, const int32_t* pos, int32_t E, const int8_t* w_down,
+                  const float* s_down, int32_t d, int32_t f, const float* add, float* y,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * -------------------------------------------------------------------------
+ * Balance: routes per expert, the balance loss of each sequence, its gradient
+ * -------------------------------------------------------------------------
+ * Tokens lie in S sequences behind one another: sequence s holds the tokens
+ * starts[s] <= t < starts[s + 1] (int32 [S + 1], not decreasing, in [0, T]; null:
+ * S = 1 and every token).  A token takes part if it is in a sequence and has a
+ * route (an idx entry in [0, E); a gate leaves -1 where an expert is missing):
+ * padding behind the last sequence, and tokens without an expert, do not.
+ *
+ *   tokens[s]    = n_s, how many tokens of sequence s take part    int32 [S]
+ *   counts[s][e] = their routes to expert e                        int32 [S][E]
+ *   p[t][e]      = a[t][e] / sum_e' a[t][e']; a = exp(z - max z) for
+ *                  MOE_SCORE_SOFTMAX, sigmoid(z) (z clamped to [-80, 80]) for
+ *                  MOE_SCORE_SIGMOID, and 0 for an expert that is masked (as for
+ *                  moe_gate_topk: z is NaN or <= -2^127; a larger z counts as
+ *                  the largest finite fp32 value at most)
+ *   loss[s]      = alpha E sum_e (counts[s][e] / (k n_s)) (sum_t p[t][e] / n_s)
+ *                  (alpha where tokens and probabilities are spread evenly; 0 for
+ *                  a sequence without tokens)                       fp32 [S]
+ *
+ * The gradient with respect to the logits, the counts taken as constants, with
+ * g[s] the gradient of whatever is minimised with respect to loss[s]:
+ *   w[t][e]  = g[s] alpha E counts[s][e] / (k n_s^2)
+ *   dz[t][e] = p[t][e] (w[t][e] - sum_e' p[t][e'] w[t][e'])
+ *              (MOE_SCORE_SIGMOID: times 1 - sigmoid(z[t][e]))
+ * and 0 for masked experts and for tokens that take no part.
+ *
+ * z [T] rows of E logits in z_dtype (MOE_F32 or MOE_BF16), z_stride elements
+ * apart (any element-aligned address); idx int32 [T][k]; dz as z, in the same
+ * dtype, rounded once; counts and tokens of the forward call go into the backward
+ * one.  Scores and sums are fp32 (exponentials and reciprocals of the hardware, a
+ * few ulp), the sum over tokens fp64; identical inputs give bitwise identical
+ * outputs.  1 <= E <= 1024, 1 <= k <= min(E, 16), 1 <= S <= 65536; T = 0 gives
+ * zeros.  Workspace: moe_balance_loss_workspace_bytes.
+ */
+int moe_balance_loss_workspace_bytes(int32_t T, int32_t S, int32_t E, size_t* bytes);
+int moe_balance_loss(const void* z, int32_t z_dtype, int64_t z_stride, int32_t T, int32_t E,
+                     const int32_t* idx, int32_t k, int32_t score, float alpha,
+                     const int32_t* starts, int32_t S, int32_t* counts, int32_t* tokens,
+                     float* loss, void* workspace, size_t workspace_bytes, void* stream);
+int moe_balance_loss_backward(const void* z, int32_t z_dtype, int64_t z_stride, int32_t T,
+                              int32_t E, const int32_t* idx, int32_t k, int32_t score,
+                              float alpha, const int32_t* starts, int32_t S,
+                              const int32_t* counts, const int32_t* tokens,
+                              const float* grad_loss, void* dz, int64_t dz_stride,
+                              void* stream);
+
+/*
  * Per-kernel timing with HIP events recorded on the stream each kernel is
  * launched on.  Eager use only: do not enable it while a stream is being
  * captured into a graph.  moe_profile_collect synchronises the recorded

@@ -25,7 +25,8 @@ ARCH = "gfx950"
 
 SOURCES = ["api.hip", "route.hip", "bucket.hip", "repack.hip", "decode.hip", "decode_k1.hip", "decode_k2.hip",
            "decode_k3.hip", "decode_unique.hip", "prefill.hip", "dense.hip", "gate.hip", "blockscale_quant.hip",
-           "blockscale_matmul.hip", "blockscale_experts.hip"]
+           "blockscale_matmul.hip", "blockscale_experts.hip", "int8_quant.hip", "int8_matmul.hip", "int8_experts.hip",
+           "balance.hip"]
 PROBE_SOURCES = ["probe.hip"]
 # packed-fp32 VALU forms are disabled: only ordinary fp32 instructions
 COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang",

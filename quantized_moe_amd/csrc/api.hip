@@ -1127,3 +1127,214 @@ extern "C" int moe_blockscale_down(const uint8_t* hq, const float* hs, int32_t T
   if (e != hipSuccess) return hip_fail(e, fn);
   return ok();
 }
+
+// ---------------------------------------------------------------------------
+// int8 operators
+// ---------------------------------------------------------------------------
+extern "C" int moe_int8_quantize(const void* x, int32_t x_dtype, int64_t ldx, int32_t M, int32_t K, int8_t* q, int64_t ldq,
+                                 float* s, void* stream) {
+  const char* fn = "moe_int8_quantize";
+  int rc;
+  if ((rc = check_bs_rows(fn, M)) || (rc = check_bs_k(fn, "K", K)) || (rc = check_dtype(fn, x_dtype))) return rc;
+  if (ldx < K || ldx % (x_dtype == MOE_BF16 ? 8 : 4) != 0)
+    return fail(MOE_ERR_INVALID_ARG, "%s: ldx %lld is below K %d or leaves rows unaligned to 16 bytes", fn, (long long)ldx, K);
+  if (ldq < K || ldq % 16 != 0)
+    return fail(MOE_ERR_INVALID_ARG, "%s: ldq %lld is below K %d or not a multiple of 16", fn, (long long)ldq, K);
+  if (M == 0) return ok();
+  NEED_PTR(x, "x");
+  NEED_PTR(q, "q");
+  NEED_PTR(s, "s");
+  hipStream_t st = (hipStream_t)stream;
+  const int pid = prof_begin("i8_quantize", st);
+  hipError_t e = launch_i8_quantize(x, x_dtype, ldx, M, K, q, ldq, s, st);
+  prof_end(pid, st);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
+static_assert((int64_t)BS_MAX_K << 14 < (int64_t(1) << 31), "the products of a row fit 32 bits");
+
+extern "C" int moe_int8_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K, size_t* bytes) {
+  const char* fn = "moe_int8_matmul_workspace_bytes";
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "%s: bytes is null", fn);
+  int rc;
+  if ((rc = check_bs_rows(fn, M)) || (rc = check_bs_k(fn, "K", K)) || (rc = check_bs_outputs(fn, N))) return rc;
+  *bytes = i8_matmul_ws(M, N, K);
+  return ok();
+}
+
+extern "C" int moe_int8_matmul(const int8_t* xq, int64_t ldx, const float* xs, int32_t M, const int8_t* wq,
+                               const float* ws, int32_t N, int32_t K, void* y, int32_t y_dtype, int64_t ldy,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_int8_matmul";
+  int rc;
+  if ((rc = check_bs_rows(fn, M)) || (rc = check_bs_k(fn, "K", K)) || (rc = check_bs_outputs(fn, N))) return rc;
+  if (y_dtype != MOE_F32 && y_dtype != MOE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: unknown output dtype %d", fn, y_dtype);
+  if (ldx < K || ldx % 16 != 0 || ldx > BS_MAX_LDX)
+    return fail(MOE_ERR_INVALID_ARG, "%s: ldx %lld is below K %d, above %d or not a multiple of 16", fn, (long long)ldx,
+                K, BS_MAX_LDX);
+  if (ldy < N) return fail(MOE_ERR_INVALID_ARG, "%s: ldy %lld below N %d", fn, (long long)ldy, N);
+  if (M == 0) return ok();
+  NEED_PTR(xq, "xq");
+  NEED_PTR(xs, "xs");
+  NEED_PTR(wq, "wq");
+  NEED_PTR(ws, "ws");
+  NEED_PTR(y, "y");
+  const size_t need = i8_matmul_ws(M, N, K);
+  if (need) {
+    if (workspace_bytes < need)
+      return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, workspace_bytes, need);
+    NEED_PTR(workspace, "workspace");
+  }
+  I8Matmul a{xq, ldx, xs, M, wq, ws, N, K, y, y_dtype, ldy, (int*)workspace};
+  hipError_t e = launch_i8_matmul(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
+extern "C" int moe_int8_gateup(const int8_t* xq, const float* xs, int32_t T, int32_t k, const int32_t* offsets,
+                               const int32_t* perm, int32_t E, const int8_t* w_gate, const float* s_gate,
+                               const int8_t* w_up, const float* s_up, int32_t f, int32_t d, void* h, int32_t h_dtype,
+                               void* stream) {
+  const char* fn = "moe_int8_gateup";
+  int rc;
+  if ((rc = check_T(fn, T)) || (rc = check_bs_experts(fn, E, k, d, f))) return rc;
+  if (h_dtype != MOE_F32 && h_dtype != MOE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: unknown output dtype %d", fn, h_dtype);
+  if (T == 0) return ok();
+  NEED_PTR(xq, "xq");
+  NEED_PTR(xs, "xs");
+  NEED_PTR(offsets, "offsets");
+  NEED_PTR(perm, "perm");
+  NEED_PTR(w_gate, "w_gate");
+  NEED_PTR(s_gate, "s_gate");
+  NEED_PTR(w_up, "w_up");
+  NEED_PTR(s_up, "s_up");
+  NEED_PTR(h, "h");
+  I8Gateup a{xq, xs, T, k, offsets, perm, E, w_gate, s_gate, w_up, s_up, f, d, h, h_dtype};
+  hipStream_t s = (hipStream_t)stream;
+  const int pid = prof_begin("i8_gateup", s);
+  hipError_t e = launch_i8_gateup(a, s);
+  prof_end(pid, s);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
+extern "C" int moe_int8_down_workspace_bytes(int32_t T, int32_t k, int32_t d, size_t* bytes) {
+  const char* fn = "moe_int8_down_workspace_bytes";
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "%s: bytes is null", fn);
+  int rc;
+  if ((rc = check_T(fn, T)) || (rc = check_bs_k(fn, "d", d))) return rc;
+  if (k < 1 || k > TOPK_MAX_K) return fail(MOE_ERR_INVALID_ARG, "%s: top_k %d not in [1, %d]", fn, k, TOPK_MAX_K);
+  *bytes = i8_down_ws(T, k, d);
+  return ok();
+}
+
+extern "C" int moe_int8_down(const int8_t* hq, const float* hs, int32_t T, int32_t k, const float* wt,
+                             const int32_t* offsets, const int32_t* pos, int32_t E, const int8_t* w_down,
+                             const float* s_down, int32_t d, int32_t f, const float* add, float* y, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_int8_down";
+  int rc;
+  if ((rc = check_T(fn, T)) || (rc = check_bs_experts(fn, E, k, d, f))) return rc;
+  if (T == 0) return ok();
+  NEED_PTR(hq, "hq");
+  NEED_PTR(hs, "hs");
+  NEED_PTR(wt, "wt");
+  NEED_PTR(offsets, "offsets");
+  NEED_PTR(pos, "pos");
+  NEED_PTR(w_down, "w_down");
+  NEED_PTR(s_down, "s_down");
+  NEED_PTR(y, "y");
+  if (add && !aligned16(add)) return fail(MOE_ERR_INVALID_ARG, "%s: add is not 16-byte aligned", fn);
+  const size_t need = i8_down_ws(T, k, d);
+  if (workspace_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, workspace_bytes, need);
+  if (need) NEED_PTR(workspace, "workspace");
+  I8Down a{hq, hs, T, k, wt, offsets, pos, E, w_down, s_down, d, f, add, y, (float*)workspace};
+  hipError_t e = launch_i8_down(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
+// ---------------------------------------------------------------------------
+// balance loss
+// ---------------------------------------------------------------------------
+static int check_balance(const char* fn, int32_t z_dtype, int64_t z_stride, int32_t T, int32_t E, int32_t k, int32_t score,
+                         float alpha, int32_t S) {
+  int rc;
+  if (E < 1 || E > MAX_EXPERTS) return fail(MOE_ERR_INVALID_ARG, "%s: n_experts %d not in [1, %d]", fn, E, MAX_EXPERTS);
+  if (k < 1 || k > TOPK_MAX_K || k > E)
+    return fail(MOE_ERR_INVALID_ARG, "%s: top_k %d not in [1, min(n_experts, %d)]", fn, k, TOPK_MAX_K);
+  if (S < 1 || S > BALANCE_MAX_S) return fail(MOE_ERR_INVALID_ARG, "%s: %d sequences not in [1, %d]", fn, S, BALANCE_MAX_S);
+  if ((rc = check_T(fn, T)) || (rc = check_dtype(fn, z_dtype))) return rc;
+  if (score != MOE_SCORE_SIGMOID && score != MOE_SCORE_SOFTMAX)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: unknown score %d", fn, score);
+  if (!isfinite(alpha)) return fail(MOE_ERR_INVALID_ARG, "%s: alpha is not finite", fn);
+  if (z_stride < E) return fail(MOE_ERR_INVALID_ARG, "%s: z_stride %lld below n_experts %d", fn, (long long)z_stride, E);
+  return MOE_OK;
+}
+// Logits and their gradients: any address of their elements.
+static bool element_aligned(const void* p, int32_t dtype) { return ((uintptr_t)p & (dtype == MOE_BF16 ? 1u : 3u)) == 0; }
+
+extern "C" int moe_balance_loss_workspace_bytes(int32_t T, int32_t S, int32_t E, size_t* bytes) {
+  const char* fn = "moe_balance_loss_workspace_bytes";
+  if (!bytes) return fail(MOE_ERR_INVALID_ARG, "%s: bytes is null", fn);
+  const int rc = check_balance(fn, MOE_F32, E, T, E, 1, MOE_SCORE_SIGMOID, 1.0f, S);
+  if (rc) return rc;
+  *bytes = balance_ws(T);
+  return ok();
+}
+
+extern "C" int moe_balance_loss(const void* z, int32_t z_dtype, int64_t z_stride, int32_t T, int32_t E, const int32_t* idx,
+                                int32_t k, int32_t score, float alpha, const int32_t* starts, int32_t S, int32_t* counts,
+                                int32_t* tokens, float* loss, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_balance_loss";
+  const int rc = check_balance(fn, z_dtype, z_stride, T, E, k, score, alpha, S);
+  if (rc) return rc;
+  if (!starts && S != 1) return fail(MOE_ERR_INVALID_ARG, "%s: %d sequences without their starts", fn, S);
+  if (T > 0) {
+    if (!z) return fail(MOE_ERR_INVALID_ARG, "%s: z is null", fn);
+    if (!element_aligned(z, z_dtype)) return fail(MOE_ERR_INVALID_ARG, "%s: z is not aligned to its elements", fn);
+    NEED_PTR(idx, "idx");
+  }
+  if (starts) NEED_PTR(starts, "starts");
+  NEED_PTR(counts, "counts");
+  NEED_PTR(tokens, "tokens");
+  NEED_PTR(loss, "loss");
+  const size_t need = balance_ws(T);
+  if (workspace_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, workspace_bytes, need);
+  if (need) NEED_PTR(workspace, "workspace");
+  Balance a{z, z_dtype, z_stride, T, E, idx, k, score == MOE_SCORE_SOFTMAX, alpha, starts, S, counts, tokens, loss,
+            (float*)workspace, nullptr, nullptr, 0};
+  hipError_t e = launch_balance_loss(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}
+
+extern "C" int moe_balance_loss_backward(const void* z, int32_t z_dtype, int64_t z_stride, int32_t T, int32_t E,
+                                         const int32_t* idx, int32_t k, int32_t score, float alpha, const int32_t* starts,
+                                         int32_t S, const int32_t* counts, const int32_t* tokens, const float* grad_loss,
+                                         void* dz, int64_t dz_stride, void* stream) {
+  const char* fn = "moe_balance_loss_backward";
+  const int rc = check_balance(fn, z_dtype, z_stride, T, E, k, score, alpha, S);
+  if (rc) return rc;
+  if (!starts && S != 1) return fail(MOE_ERR_INVALID_ARG, "%s: %d sequences without their starts", fn, S);
+  if (dz_stride < E) return fail(MOE_ERR_INVALID_ARG, "%s: dz_stride %lld below n_experts %d", fn, (long long)dz_stride, E);
+  if (T == 0) return ok();
+  if (!z || !dz) return fail(MOE_ERR_INVALID_ARG, "%s: z or dz is null", fn);
+  if (!element_aligned(z, z_dtype) || !element_aligned(dz, z_dtype))
+    return fail(MOE_ERR_INVALID_ARG, "%s: z or dz is not aligned to its elements", fn);
+  NEED_PTR(idx, "idx");
+  if (starts) NEED_PTR(starts, "starts");
+  NEED_PTR(counts, "counts");
+  NEED_PTR(tokens, "tokens");
+  NEED_PTR(grad_loss, "grad_loss");
+  Balance a{z, z_dtype, z_stride, T, E, idx, k, score == MOE_SCORE_SOFTMAX, alpha, starts, S, const_cast<int32_t*>(counts),
+            const_cast<int32_t*>(tokens), nullptr, nullptr, grad_loss, dz, dz_stride};
+  hipError_t e = launch_balance_backward(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, fn);
+  return ok();
+}

@@ -69,6 +69,22 @@ __device__ __forceinline__ float bs_scale(uint32_t amax) {
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
+// x / s correctly rounded for r = 1 / s correctly rounded: each step adds the
+// residual, exact by the fused multiply-add, times r.  The first leaves a
+// neighbour of the quotient, the second the nearest.  6 instructions for the
+// general division's 10; s >= 2^-80 keeps the residuals of all quotients that
+// E4M3 tells from 0 out of the subnormal range.
+__device__ __forceinline__ float divide_exact(float x, float s, float r) {
+  float q = x * r;
+  q = __builtin_fmaf(__builtin_fmaf(-s, q, x), r, q);
+  return __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-s, q, x), r, q), x);  // (-0 stays -0)
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_umax(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false));
+}
+
 // One output value, fp32 or bf16 (nearest even).
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 
@@ -220,6 +236,56 @@ struct TileScan {
 inline int64_t max_tiles(int64_t n, int E, int bm) {
   const int64_t full = n / bm + (E < n ? E : n);
   return full < n ? full : n;
+}
+
+struct ExpertTile {
+  int e, row0, rows, nt;
+};
+
+// Which M tile and which outputs a block takes.
+//
+// Few tiles: ids run over the M tiles first, and an XCD takes a contiguous
+// eighth of them.  Many tiles: the XCDs take turns at groups of 16 tiles with
+// all their outputs, so that a row's codes are read by one XCD and not by each
+// for its share of the outputs (0.8 GB of 4.1 at 4096 tokens' down), and the
+// tiles of a crowded expert share the weights in its L2.  1024 tokens' gate/up
+// 1229 -> 1118 us; groups of 4 and 8: 1185 and 1143 us.  The groups are as large
+// as gives every XCD the same number of them: 1024 crowded tokens' down products
+// over 64 experts (170 tiles) 300 -> 216 us, gate/up over 128 experts 571 -> 516.
+constexpr int TILE_GROUP = 16;
+struct TilePlan {
+  int by_tile;  // many tiles
+  int tiles;    // M tiles, or (by_tile) M tiles of an XCD: upper bounds
+  int n_tiles;
+  unsigned blocks;
+};
+template <class C>
+static TilePlan tile_plan(int64_t n, int E, int N) {
+  TilePlan p;
+  p.n_tiles = (N + C::BN - 1) / C::BN;
+  p.tiles = (int)max_tiles(n, E, C::BM);
+  p.by_tile = n >= 8 * TILE_GROUP * C::BM;  // a group at least for each XCD
+  if (p.by_tile) p.tiles = (p.tiles + 8 * TILE_GROUP - 1) / (8 * TILE_GROUP) * TILE_GROUP;
+  p.blocks = (unsigned)p.tiles * p.n_tiles * (p.by_tile ? 8 : 1);
+  return p;
+}
+template <int BM>
+__device__ __forceinline__ bool expert_tile(const int32_t* offsets, int E, const TilePlan& p, ExpertTile* t) {
+  const TileScan<BM> scan(offsets, E);
+  int pick;
+  if (p.by_tile) {
+    const int tiles = scan.tiles(), rounds = (tiles + 8 * TILE_GROUP - 1) / (8 * TILE_GROUP);
+    if (tiles == 0) return false;
+    const int group = (tiles + 8 * rounds - 1) / (8 * rounds);  // equal ones, so that every XCD has as many tiles
+    const int i = blockIdx.x >> 3, round = i / (group * p.n_tiles), in = i - round * group * p.n_tiles;
+    t->nt = in / group;
+    pick = (round * 8 + (blockIdx.x & 7)) * group + in % group;
+  } else {
+    const int id = xcd_order(blockIdx.x, gridDim.x);
+    t->nt = id / p.tiles;
+    pick = id - t->nt * p.tiles;
+  }
+  return scan.find(pick, &t->e, &t->row0, &t->rows);
 }
 
 }  // namespace qmoe

@@ -4,56 +4,6 @@
 
 namespace qmoe {
 
-struct ExpertTile {
-  int e, row0, rows, nt;
-};
-
-// Which M tile and which outputs a block takes.
-//
-// Few tiles: ids run over the M tiles first, and an XCD takes a contiguous
-// eighth of them.  Many tiles: the XCDs take turns at groups of 16 tiles with
-// all their outputs, so that a row's codes are read by one XCD and not by each
-// for its share of the outputs (0.8 GB of 4.1 at 4096 tokens' down), and the
-// tiles of a crowded expert share the weights in its L2.  1024 tokens' gate/up
-// 1229 -> 1118 us; groups of 4 and 8: 1185 and 1143 us.  The groups are as large
-// as gives every XCD the same number of them: 1024 crowded tokens' down products
-// over 64 experts (170 tiles) 300 -> 216 us, gate/up over 128 experts 571 -> 516.
-constexpr int TILE_GROUP = 16;
-struct TilePlan {
-  int by_tile;  // many tiles
-  int tiles;    // M tiles, or (by_tile) M tiles of an XCD: upper bounds
-  int n_tiles;
-  unsigned blocks;
-};
-template <class C>
-static TilePlan tile_plan(int64_t n, int E, int N) {
-  TilePlan p;
-  p.n_tiles = (N + C::BN - 1) / C::BN;
-  p.tiles = (int)max_tiles(n, E, C::BM);
-  p.by_tile = n >= 8 * TILE_GROUP * C::BM;  // a group at least for each XCD
-  if (p.by_tile) p.tiles = (p.tiles + 8 * TILE_GROUP - 1) / (8 * TILE_GROUP) * TILE_GROUP;
-  p.blocks = (unsigned)p.tiles * p.n_tiles * (p.by_tile ? 8 : 1);
-  return p;
-}
-template <int BM>
-__device__ __forceinline__ bool expert_tile(const int32_t* offsets, int E, const TilePlan& p, ExpertTile* t) {
-  const TileScan<BM> scan(offsets, E);
-  int pick;
-  if (p.by_tile) {
-    const int tiles = scan.tiles(), rounds = (tiles + 8 * TILE_GROUP - 1) / (8 * TILE_GROUP);
-    if (tiles == 0) return false;
-    const int group = (tiles + 8 * rounds - 1) / (8 * rounds);  // equal ones, so that every XCD has as many tiles
-    const int i = blockIdx.x >> 3, round = i / (group * p.n_tiles), in = i - round * group * p.n_tiles;
-    t->nt = in / group;
-    pick = (round * 8 + (blockIdx.x & 7)) * group + in % group;
-  } else {
-    const int id = xcd_order(blockIdx.x, gridDim.x);
-    t->nt = id / p.tiles;
-    pick = id - t->nt * p.tiles;
-  }
-  return scan.find(pick, &t->e, &t->row0, &t->rows);
-}
-
 // A block owns BM bucket rows of one expert and one group of 128 hidden
 // columns, gate and up, so that the group's maximum stays in it.
 template <class C>
@@ -180,23 +130,33 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void bs_down_kernel(
 }
 
 // y[t] = add[t] + sum_j wt[t][j] ye[pos[t k + j]], 4 outputs per thread.
-__global__ __launch_bounds__(256) void bs_combine_kernel(BsDown a) {
-  const int d4 = a.d / 4;
+__global__ __launch_bounds__(256) void combine_routes_kernel(const float* __restrict__ ye, int T, int k, int d4,
+                                                             const float* __restrict__ wt, const int32_t* __restrict__ pos,
+                                                             const float* add, float* y) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (int64_t)a.T * d4) return;
+  if (i >= (int64_t)T * d4) return;
   const int64_t t = i / d4;
   const int c = (int)(i - t * d4);
-  f32x4_t y = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (a.add) y = reinterpret_cast<const f32x4_t*>(a.add)[i];
-  for (int j = 0; j < a.k; j++) {
-    const int p = a.pos[t * a.k + j];
-    if ((uint32_t)p >= (uint32_t)(a.T * a.k)) continue;  // a route without a place
-    const float w = a.wt[t * a.k + j];
-    const f32x4_t v = reinterpret_cast<const f32x4_t*>(a.ye)[(int64_t)p * d4 + c];
+  f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (add) v = reinterpret_cast<const f32x4_t*>(add)[i];
+  for (int j = 0; j < k; j++) {
+    const int p = pos[t * k + j];
+    if ((uint32_t)p >= (uint32_t)(T * k)) continue;  // a route without a place
+    const float w = wt[t * k + j];
+    const f32x4_t u = reinterpret_cast<const f32x4_t*>(ye)[(int64_t)p * d4 + c];
 #pragma unroll
-    for (int q = 0; q < 4; q++) y[q] = __builtin_fmaf(w, v[q], y[q]);
+    for (int q = 0; q < 4; q++) v[q] = __builtin_fmaf(w, u[q], v[q]);
   }
-  reinterpret_cast<f32x4_t*>(a.y)[i] = y;
+  reinterpret_cast<f32x4_t*>(y)[i] = v;
+}
+
+hipError_t launch_combine(const char* name, const float* ye, int T, int k, int d, const float* wt, const int32_t* pos,
+                          const float* add, float* y, hipStream_t s) {
+  const int pid = prof_begin(name, s);
+  QMOE_LAUNCH(combine_routes_kernel, dim3((unsigned)(((int64_t)T * (d / 4) + 255) / 256)), dim3(256), 0, s, ye, T, k, d / 4,
+              wt, pos, add, y);
+  prof_end(pid, s);
+  return hipGetLastError();
 }
 
 // One or two tokens: one launch and no workspace.  A block owns 16 outputs of
@@ -342,14 +302,11 @@ hipError_t launch_bs_down(const BsDown& a, hipStream_t s) {
     prof_end(pid, s);
     return hipGetLastError();
   }
-  int pid = prof_begin("bs_down", s);
+  const int pid = prof_begin("bs_down", s);
   hipError_t e = launch_down_products(a, s);
   prof_end(pid, s);
   if (e != hipSuccess) return e;
-  pid = prof_begin("bs_combine", s);
-  QMOE_LAUNCH(bs_combine_kernel, dim3((unsigned)(((int64_t)a.T * (a.d / 4) + 255) / 256)), dim3(256), 0, s, a);
-  prof_end(pid, s);
-  return hipGetLastError();
+  return launch_combine("bs_combine", a.ye, a.T, a.k, a.d, a.wt, a.pos, a.add, a.y, s);
 }
 
 }  // namespace qmoe

@@ -10,22 +10,6 @@
 
 namespace qmoe {
 
-// x / s correctly rounded for r = 1 / s correctly rounded: each step adds the
-// residual, exact by the fused multiply-add, times r.  The first leaves a
-// neighbour of the quotient, the second the nearest.  6 instructions for the
-// general division's 10; s >= 2^-80 keeps the residuals of all quotients that
-// E4M3 tells from 0 out of the subnormal range.
-__device__ __forceinline__ float divide_exact(float x, float s, float r) {
-  float q = x * r;
-  q = __builtin_fmaf(__builtin_fmaf(-s, q, x), r, q);
-  return __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-s, q, x), r, q), x);  // (-0 stays -0)
-}
-
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_umax(uint32_t v) {
-  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false));
-}
-
 template <int XDT>
 __global__ __launch_bounds__(256) void bs_quantize_kernel(const void* __restrict__ x, int64_t ldx, int64_t groups,
                                                           int KB, int K, uint8_t* __restrict__ q, int64_t ldq,

@@ -1,4 +1,5 @@
-// The gate and block-scaled operators as Python calls on torch tensors.
+// The gate, the block-scaled and int8 operators and the balance loss as Python calls
+// on torch tensors.
 //
 // A decode step makes these calls for one token, where the kernels take 3 to 5
 // us: checks and marshalling in Python (3 to 5 us a call) would be what such a
@@ -261,9 +262,149 @@ PyObject* down(PyObject* const* a) {
   });
 }
 
+// x, q, s, stream
+PyObject* int8_quantize(PyObject* const* a) {
+  Rows x, q;
+  void *sc, *s;
+  if (!rows_of(a[0], &x) || float_type(x.type) < 0 || !rows_of(a[1], &q) || q.type != at::kChar || q.rows != x.rows ||
+      q.cols != x.cols || !whole(a[2], at::kFloat, {x.rows}, &sc) || !stream_here(a[3]))
+    Py_RETURN_NONE;
+  if (!stream_of(a[3], &s)) return nullptr;
+  return call([&] {
+    return moe_int8_quantize(x.p, float_type(x.type), x.ld, narrow(x.rows), narrow(x.cols), (int8_t*)q.p, q.ld, (float*)sc,
+                             s);
+  });
+}
+
+// xq, xs, wq, ws, y, workspace, stream
+PyObject* int8_matmul(PyObject* const* a) {
+  Rows x, y;
+  at::IntArrayRef w;
+  void *xs, *wq, *ws, *work, *s;
+  size_t work_bytes;
+  if (!rows_of(a[0], &x) || x.type != at::kChar || !rows_of(a[4], &y) || float_type(y.type) < 0 ||
+      !shape_of(a[2], 2, &w) || y.rows != x.rows || y.cols != w[0])
+    Py_RETURN_NONE;
+  const int64_t N = w[0], K = x.cols;
+  if (!whole(a[1], at::kFloat, {x.rows}, &xs) || !whole(a[2], at::kChar, {N, K}, &wq) ||
+      !whole(a[3], at::kFloat, {N}, &ws) || !workspace_of(a[5], &work, &work_bytes) || !stream_here(a[6]))
+    Py_RETURN_NONE;
+  if (!stream_of(a[6], &s)) return nullptr;
+  return call([&] {
+    return moe_int8_matmul((const int8_t*)x.p, x.ld, (const float*)xs, narrow(x.rows), (const int8_t*)wq,
+                           (const float*)ws, narrow(N), narrow(K), y.p, float_type(y.type), y.ld, work, work_bytes, s);
+  });
+}
+
+// xq, xs, k, offsets, perm, w_gate, s_gate, w_up, s_up, h, stream
+PyObject* int8_gateup(PyObject* const* a) {
+  const int64_t k = PyLong_AsLongLong(a[2]);
+  if (k == -1 && PyErr_Occurred()) return nullptr;
+  at::IntArrayRef x, w;
+  Rows hr;
+  if (!shape_of(a[0], 2, &x) || !shape_of(a[5], 3, &w) || !rows_of(a[9], &hr) || float_type(hr.type) < 0 || k < 0 ||
+      k > INT_MAX || x[0] > INT_MAX)
+    Py_RETURN_NONE;
+  const int64_t T = x[0], d = x[1], E = w[0], f = w[1], R = T * k;
+  void *xq, *xs, *offsets, *perm, *wg, *sg, *wu, *su, *h, *s;
+  if (!whole(a[0], at::kChar, {T, d}, &xq) || !whole(a[1], at::kFloat, {T}, &xs) ||
+      !whole(a[3], at::kInt, {E + 1}, &offsets) || !whole(a[4], at::kInt, {R}, &perm) ||
+      !whole(a[5], at::kChar, {E, f, d}, &wg) || !whole(a[6], at::kFloat, {E, f}, &sg) ||
+      !whole(a[7], at::kChar, {E, f, d}, &wu) || !whole(a[8], at::kFloat, {E, f}, &su) ||
+      !whole(a[9], hr.type, {R, f}, &h) || !stream_here(a[10]))
+    Py_RETURN_NONE;
+  if (!stream_of(a[10], &s)) return nullptr;
+  return call([&] {
+    return moe_int8_gateup((const int8_t*)xq, (const float*)xs, narrow(T), narrow(k), (const int32_t*)offsets,
+                           (const int32_t*)perm, narrow(E), (const int8_t*)wg, (const float*)sg, (const int8_t*)wu,
+                           (const float*)su, narrow(f), narrow(d), h, float_type(hr.type), s);
+  });
+}
+
+// hq, hs, wt, offsets, pos, w_down, s_down, y, workspace, add, stream
+PyObject* int8_down(PyObject* const* a) {
+  at::IntArrayRef r, w;
+  if (!shape_of(a[2], 2, &r) || !shape_of(a[5], 3, &w) || r[0] > INT_MAX || r[1] > INT_MAX) Py_RETURN_NONE;
+  const int64_t T = r[0], k = r[1], E = w[0], d = w[1], f = w[2], R = T * k;
+  void *hq, *hs, *wt, *offsets, *pos, *wd, *sd, *y, *work, *add = nullptr, *s;
+  size_t work_bytes;
+  if (!whole(a[0], at::kChar, {R, f}, &hq) || !whole(a[1], at::kFloat, {R}, &hs) ||
+      !whole(a[2], at::kFloat, {T, k}, &wt) || !whole(a[3], at::kInt, {E + 1}, &offsets) ||
+      !whole(a[4], at::kInt, {R}, &pos) || !whole(a[5], at::kChar, {E, d, f}, &wd) ||
+      !whole(a[6], at::kFloat, {E, d}, &sd) || !whole(a[7], at::kFloat, {T, d}, &y) ||
+      !workspace_of(a[8], &work, &work_bytes) || (a[9] != Py_None && !whole(a[9], at::kFloat, {T, d}, &add)) ||
+      !stream_here(a[10]))
+    Py_RETURN_NONE;
+  if (!stream_of(a[10], &s)) return nullptr;
+  return call([&] {
+    return moe_int8_down((const int8_t*)hq, (const float*)hs, narrow(T), narrow(k), (const float*)wt,
+                         (const int32_t*)offsets, (const int32_t*)pos, narrow(E), (const int8_t*)wd, (const float*)sd,
+                         narrow(d), narrow(f), (const float*)add, (float*)y, work, work_bytes, s);
+  });
+}
+
+// What the two balance calls share: z, idx, counts, tokens, starts (or None).
+struct BalanceArgs {
+  Rows z;
+  int64_t k, S, score;
+  double alpha;
+  void *idx, *counts, *tokens, *starts = nullptr, *s;
+};
+bool balance_args(PyObject* z, PyObject* idx, PyObject* counts, PyObject* tokens, PyObject* score, PyObject* alpha,
+                  PyObject* starts, PyObject* stream, BalanceArgs* b) {
+  at::IntArrayRef i, c;
+  if (!rows_of(z, &b->z) || float_type(b->z.type) < 0 || !shape_of(idx, 2, &i) || !shape_of(counts, 2, &c)) return false;
+  b->k = i[1];
+  b->S = c[0];
+  b->score = PyLong_AsLongLong(score);
+  b->alpha = PyFloat_AsDouble(alpha);
+  return whole(idx, at::kInt, {b->z.rows, b->k}, &b->idx) && whole(counts, at::kInt, {b->S, b->z.cols}, &b->counts) &&
+         whole(tokens, at::kInt, {b->S}, &b->tokens) &&
+         (starts == Py_None || whole(starts, at::kInt, {b->S + 1}, &b->starts)) && stream_here(stream);
+}
+
+// z, idx, counts, tokens, loss, workspace, score, alpha, starts, stream
+PyObject* balance_loss(PyObject* const* a) {
+  BalanceArgs b;
+  void *loss, *work;
+  size_t work_bytes;
+  if (!balance_args(a[0], a[1], a[2], a[3], a[6], a[7], a[8], a[9], &b) || !whole(a[4], at::kFloat, {b.S}, &loss) ||
+      !workspace_of(a[5], &work, &work_bytes)) {
+    if (PyErr_Occurred()) return nullptr;
+    Py_RETURN_NONE;
+  }
+  if (PyErr_Occurred() || !stream_of(a[9], &b.s)) return nullptr;
+  return call([&] {
+    return moe_balance_loss(b.z.p, float_type(b.z.type), b.z.ld, narrow(b.z.rows), narrow(b.z.cols), (const int32_t*)b.idx,
+                            narrow(b.k), (int32_t)b.score, (float)b.alpha, (const int32_t*)b.starts, narrow(b.S),
+                            (int32_t*)b.counts, (int32_t*)b.tokens, (float*)loss, work, work_bytes, b.s);
+  });
+}
+
+// z, idx, counts, tokens, grad_loss, dz, score, alpha, starts, stream
+PyObject* balance_loss_backward(PyObject* const* a) {
+  BalanceArgs b;
+  Rows dz;
+  void* grad;
+  if (!balance_args(a[0], a[1], a[2], a[3], a[6], a[7], a[8], a[9], &b) || !whole(a[4], at::kFloat, {b.S}, &grad) ||
+      !rows_of(a[5], &dz) || dz.type != b.z.type || dz.rows != b.z.rows || dz.cols != b.z.cols) {
+    if (PyErr_Occurred()) return nullptr;
+    Py_RETURN_NONE;
+  }
+  if (PyErr_Occurred() || !stream_of(a[9], &b.s)) return nullptr;
+  return call([&] {
+    return moe_balance_loss_backward(b.z.p, float_type(b.z.type), b.z.ld, narrow(b.z.rows), narrow(b.z.cols),
+                                     (const int32_t*)b.idx, narrow(b.k), (int32_t)b.score, (float)b.alpha,
+                                     (const int32_t*)b.starts, narrow(b.S), (const int32_t*)b.counts,
+                                     (const int32_t*)b.tokens, (const float*)grad, dz.p, dz.ld, b.s);
+  });
+}
+
 #define ENTRY(name, n) {#name, (PyCFunction)(void (*)(void))entry<n, name>, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(gate_topk, 5), ENTRY(quantize, 4), ENTRY(matmul, 7), ENTRY(gateup, 12),
-                         ENTRY(down, 11), {nullptr, nullptr, 0, nullptr}};
+                         ENTRY(down, 11), ENTRY(int8_quantize, 4), ENTRY(int8_matmul, 7), ENTRY(int8_gateup, 11),
+                         ENTRY(int8_down, 11), ENTRY(balance_loss, 10), ENTRY(balance_loss_backward, 10),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods};
 
 }  // namespace

@@ -1,0 +1,238 @@
+// The routed experts' products on int8 weights: gate/up with SwiGLU, down with
+// each token's weighted sum.
+#include "int8_tile.hpp"
+
+namespace qmoe {
+
+// A block owns BM bucket rows of one expert and BN hidden columns, gate and up.
+template <class C, typename OUT>
+__global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void i8_gateup_kernel(I8Gateup a, TilePlan plan) {
+  static_assert(C::NMAT == 2 && C::KS == 1, "gate and up");
+  extern __shared__ __align__(1024) uint8_t lds[];
+  ExpertTile t;
+  if (!expert_tile<C::BM>(a.offsets, a.E, plan, &t)) return;
+  const int n0 = t.nt * C::BN, rows_n = min(C::BN, a.f - n0);
+  const int64_t row0 = (int64_t)t.e * a.f + n0, wbytes = (int64_t)rows_n * a.d;
+  const __amdgpu_buffer_rsrc_t wbuf[2] = {buffer_of(a.w_gate + row0 * a.d, wbytes), buffer_of(a.w_up + row0 * a.d, wbytes)};
+  const __amdgpu_buffer_rsrc_t wsbuf[2] = {buffer_of(a.s_gate + row0, rows_n * 4), buffer_of(a.s_up + row0, rows_n * 4)};
+  const __amdgpu_buffer_rsrc_t xbuf = buffer_of(a.xq, (int64_t)a.T * a.d);
+  const __amdgpu_buffer_rsrc_t xsbuf = buffer_of(a.xs, (int64_t)a.T * 4);
+  auto token = [&](int i) { return a.perm[t.row0 + i] / a.k; };
+  typename C::Acc acc[2][C::TN][C::TM];
+  i8_product<C>(
+      lds, wbuf, wsbuf, a.d, xbuf, xsbuf, [&](int i) { return i < t.rows ? (uint32_t)token(i) * a.d : BUFFER_OUT; },
+      [&](int i) { return i < t.rows ? (uint32_t)token(i) * 4 : BUFFER_OUT; }, 0, (a.d + C::BK - 1) / C::BK, acc);
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & (C::MF - 1), half = lane / C::MF;
+  const int wn = wave % C::WN, wm = wave / C::WN;
+#pragma unroll
+  for (int j = 0; j < C::TM; j++) {
+    const int mi = (wm * C::TM + j) * C::MF + r;
+    if (mi >= t.rows) continue;
+    const float xs = i8_xscale<C>(lds, mi);
+    OUT* row = static_cast<OUT*>(a.h) + (int64_t)(t.row0 + mi) * a.f + n0;
+#pragma unroll
+    for (int i = 0; i < C::TN; i++)
+#pragma unroll
+      for (int g = 0; g < C::Step::RUNS; g++) {
+        const int ni = (wn * C::TN + i) * C::MF + 8 * g + 4 * half;
+        const f32x4_t gate = i8_values(i8_run(acc[0][i][j], g), xs, i8_wscale<C>(lds, 0, ni));
+        const f32x4_t up = i8_values(i8_run(acc[1][i][j], g), xs, i8_wscale<C>(lds, 1, ni));
+        f32x4_t h;
+#pragma unroll
+        for (int q = 0; q < 4; q++) h[q] = silu(gate[q]) * up[q];
+        store4(row + ni, h, rows_n - ni, true);  // f is a multiple of 16
+      }
+  }
+}
+
+template <class C, typename OUT>
+static hipError_t launch_gateup(const I8Gateup& a, hipStream_t s) {
+  const TilePlan plan = tile_plan<C>((int64_t)a.T * a.k, a.E, a.f);
+  auto* k = i8_gateup_kernel<C, OUT>;
+  int per_cu, cus;
+  hipError_t e = launch_shape((const void*)k, C::THREADS, C::LDS, C::LDS, &per_cu, &cus);
+  if (e != hipSuccess) return e;
+  QMOE_LAUNCH(k, dim3(plan.blocks), dim3(C::THREADS), C::LDS, s, a, plan);
+  return hipGetLastError();
+}
+
+template <typename OUT>
+static hipError_t pick_gateup(const I8Gateup& a, hipStream_t s) {
+  const int64_t n = (int64_t)a.T * a.k, E = a.E;
+  if (n <= 4 * E) return launch_gateup<I8Tile<16, 8, 1, 1, 1, 128, 2, 1, 2>, OUT>(a, s);
+  if (n <= 32 * E) return launch_gateup<I8Tile<32, 4, 1, 1, 1, 128, 2, 1, 2>, OUT>(a, s);
+  return launch_gateup<I8Tile<32, 4, 1, 1, 2, 128, 2, 1, 2>, OUT>(a, s);
+}
+
+hipError_t launch_i8_gateup(const I8Gateup& a, hipStream_t s) {
+  return a.h_dtype == X_BF16 ? pick_gateup<uint16_t>(a, s) : pick_gateup<float>(a, s);
+}
+
+// ye[r][n] = (D_e h_r)[n] for the bucket rows.
+template <class C>
+__global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void i8_down_kernel(I8Down a, TilePlan plan) {
+  extern __shared__ __align__(1024) uint8_t lds[];
+  ExpertTile t;
+  if (!expert_tile<C::BM>(a.offsets, a.E, plan, &t)) return;
+  const int n0 = t.nt * C::BN, rows_n = min(C::BN, a.d - n0);
+  const int64_t row0 = (int64_t)t.e * a.d + n0;
+  const __amdgpu_buffer_rsrc_t wbuf[1] = {buffer_of(a.w_down + row0 * a.f, (int64_t)rows_n * a.f)};
+  const __amdgpu_buffer_rsrc_t wsbuf[1] = {buffer_of(a.s_down + row0, rows_n * 4)};
+  const __amdgpu_buffer_rsrc_t xbuf = buffer_of(a.hq + (int64_t)t.row0 * a.f, (int64_t)t.rows * a.f);
+  const __amdgpu_buffer_rsrc_t xsbuf = buffer_of(a.hs + t.row0, t.rows * 4);
+  typename C::Acc acc[1][C::TN][C::TM];
+  i8_product<C>(
+      lds, wbuf, wsbuf, a.f, xbuf, xsbuf, [&](int i) { return i < t.rows ? (uint32_t)(i * a.f) : BUFFER_OUT; },
+      [&](int i) { return (uint32_t)(i * 4); }, 0, (a.f + C::BK - 1) / C::BK, acc);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & (C::MF - 1), half = lane / C::MF;
+  const int wn = wave % C::WN, wm = wave / C::WN;
+#pragma unroll
+  for (int j = 0; j < C::TM; j++) {
+    const int mi = (wm * C::TM + j) * C::MF + r;
+    if (mi >= t.rows) continue;
+    const float xs = i8_xscale<C>(lds, mi);
+    float* row = a.ye + (int64_t)(t.row0 + mi) * a.d + n0;
+#pragma unroll
+    for (int i = 0; i < C::TN; i++)
+#pragma unroll
+      for (int g = 0; g < C::Step::RUNS; g++) {
+        const int ni = (wn * C::TN + i) * C::MF + 8 * g + 4 * half;
+        store4(row + ni, i8_values(i8_run(acc[0][i][j], g), xs, i8_wscale<C>(lds, 0, ni)), rows_n - ni, true);
+      }
+  }
+}
+
+// One or two tokens: one launch and no workspace.  A block owns 16 outputs of one
+// token; its 16 waves share the runs of 128 inputs (and, where two groups of waves
+// or more have one for each, the routes), straight from memory with U routes
+// requested at a time.  Column j of the matrix steps' activations is route j's
+// row; the product with route j's weights takes that column and zeros, so one
+// accumulator serves every route.  The waves' sums are added, then the routes
+// weighted in their order.
+template <int U>
+__global__ __launch_bounds__(1024) void i8_down_token_kernel(I8Down a) {
+  constexpr int WAVES = 16;
+  static_assert(TOPK_MAX_K == 16, "a column of the matrix step for each route");
+  __shared__ i32x4_t part[WAVES][16][4];  // [wave][route][output / 4]
+  __shared__ float route_y[16][16];
+  __shared__ int route_row[16], route_e[16];
+  __shared__ float route_wt[16];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, quad = lane >> 4;
+  const int n0 = blockIdx.x * 16, t = blockIdx.y, KB = bs_blocks(a.f);
+  const int64_t out = (int64_t)t * a.d + n0 + r;
+  const float add = a.add && threadIdx.x < 16 ? a.add[out] : 0.0f;  // (requested early, as the weights of the routes)
+  int row = -1, below = 0;
+  float wt = 0.0f;
+  if (wave < a.k) {  // wave j finds route j's row and expert: the last with offsets[e] <= row
+    constexpr int MOST = MAX_EXPERTS / 64;
+    row = a.pos[t * a.k + wave];
+    wt = a.wt[t * a.k + wave];
+    const __amdgpu_buffer_rsrc_t ends = buffer_of(a.offsets + 1, (int64_t)a.E * 4);
+    int end[MOST];
+#pragma unroll
+    for (int i = 0; i < MOST; i++) end[i] = __float_as_int(buffer_load4(ends, (64 * i + lane) * 4));  // all at once
+#pragma unroll
+    for (int i = 0; i < MOST; i++) below += __popcll(__ballot(64 * i + lane < a.E && end[i] <= row));
+  }
+  if (lane == 0) {
+    route_row[wave] = row < a.T * a.k ? row : -1;
+    route_e[wave] = min(below, a.E - 1);
+    route_wt[wave] = wt;
+  }
+  __syncthreads();
+  row = route_row[r];
+  const int e = route_e[r];
+  const uint32_t valid = (uint32_t)__ballot(row >= 0) & 0xffffu;
+  const int64_t x_row = max(row, 0);
+  const int8_t* xp = a.hq + x_row * a.f;
+  // thread (j, n) of the first 256 finishes route j's output n: its scales are requested with the codes
+  const int fj = threadIdx.x >> 4 & 15, fn = threadIdx.x & 15;
+  const bool finish = threadIdx.x < 256 && route_row[fj] >= 0;
+  const float xs = finish ? a.hs[route_row[fj]] : 0.0f;
+  const float ws = finish ? a.s_down[(int64_t)route_e[fj] * a.d + n0 + fn] : 0.0f;
+  const int G = KB >= WAVES ? 1 : WAVES / KB;  // groups of waves that share the routes
+  const int g = KB >= WAVES ? 0 : wave / KB;
+  i32x4_t acc = {0, 0, 0, 0};
+  for (int jb = g; jb < (g < G ? a.k : 0); jb += G * U)
+    for (int kb = KB >= WAVES ? wave : wave - g * KB; kb < KB; kb += WAVES) {
+      const int k0 = kb * BS + 16 * quad;
+      const bool in0 = k0 < a.f, in1 = k0 + 64 < a.f;  // past f: some code of the row, times 0
+      const int c0 = in0 ? k0 : 0, c1 = in1 ? k0 + 64 : 0;
+      i32x4_t w0[U], w1[U];
+#pragma unroll
+      for (int i = 0; i < U; i++) {
+        const int j = jb + G * i;
+        const bool on = j < a.k && (valid >> (j & 15) & 1);  // (else a buffer of no bytes)
+        const int64_t at = ((int64_t)__builtin_amdgcn_readlane(e, j & 15) * a.d + n0) * a.f;
+        const __amdgpu_buffer_rsrc_t wbuf = buffer_of(a.w_down + at, on ? 16 * a.f : 0);
+        w0[i] = buffer_load16(wbuf, r * a.f + c0);
+        w1[i] = buffer_load16(wbuf, r * a.f + c1);
+      }
+      const i32x4_t zero = {0, 0, 0, 0};
+      i32x4_t x0 = *reinterpret_cast<const i32x4_t*>(xp + c0), x1 = *reinterpret_cast<const i32x4_t*>(xp + c1);
+      __builtin_amdgcn_sched_barrier(0);  // (else the loads go between the matrix steps, to save registers)
+      x0 = in0 ? x0 : zero;
+      x1 = in1 ? x1 : zero;
+#pragma unroll
+      for (int i = 0; i < U; i++) {
+        const bool mine = r == jb + G * i;
+        acc = I8Step<16>::mul(w0[i], mine ? x0 : zero, acc);
+        acc = I8Step<16>::mul(w1[i], mine ? x1 : zero, acc);
+      }
+    }
+  part[wave][r][quad] = acc;  // (0 for the routes of other groups)
+  __syncthreads();
+  if (threadIdx.x < 256 && fj < a.k) {
+    int s = part[0][fj][fn >> 2][fn & 3];
+#pragma unroll
+    for (int v = 1; v < WAVES; v++) s += part[v][fj][fn >> 2][fn & 3];
+    route_y[fj][fn] = ((float)s * xs) * ws;
+  }
+  __syncthreads();
+  if (threadIdx.x < 16) {
+    float y = add;
+#pragma unroll
+    for (int i = 0; i < TOPK_MAX_K; i++) y = valid >> i & 1 ? __builtin_fmaf(route_wt[i], route_y[i][fn], y) : y;
+    a.y[out] = y;
+  }
+}
+
+constexpr int TOKEN_MAX_T = 2;
+
+size_t i8_down_ws(int T, int k, int d) { return T <= TOKEN_MAX_T ? 0 : (size_t)T * k * d * 4; }
+
+template <class C>
+static hipError_t launch_down(const I8Down& a, hipStream_t s) {
+  const TilePlan plan = tile_plan<C>((int64_t)a.T * a.k, a.E, a.d);
+  auto* k = i8_down_kernel<C>;
+  int per_cu, cus;
+  hipError_t e = launch_shape((const void*)k, C::THREADS, C::LDS, C::LDS, &per_cu, &cus);
+  if (e != hipSuccess) return e;
+  QMOE_LAUNCH(k, dim3(plan.blocks), dim3(C::THREADS), C::LDS, s, a, plan);
+  return hipGetLastError();
+}
+
+static hipError_t launch_down_products(const I8Down& a, hipStream_t s) {
+  const int64_t n = (int64_t)a.T * a.k, E = a.E;
+  if (n <= 2 * E) return launch_down<I8Tile<16, 8, 1, 1, 1, 128, 2, 1, 1>>(a, s);
+  if (n <= 32 * E) return launch_down<I8Tile<32, 4, 1, 2, 1, 128, 2, 1, 1>>(a, s);
+  return launch_down<I8Tile<32, 4, 1, 2, 2, 128, 2, 1, 1>>(a, s);
+}
+
+hipError_t launch_i8_down(const I8Down& a, hipStream_t s) {
+  if (a.T <= TOKEN_MAX_T) {
+    const int pid = prof_begin("i8_down_token", s);
+    QMOE_LAUNCH(i8_down_token_kernel<6>, dim3(a.d / 16, a.T), dim3(1024), 0, s, a);
+    prof_end(pid, s);
+    return hipGetLastError();
+  }
+  const int pid = prof_begin("i8_down", s);
+  hipError_t e = launch_down_products(a, s);
+  prof_end(pid, s);
+  if (e != hipSuccess) return e;
+  return launch_combine("i8_combine", a.ye, a.T, a.k, a.d, a.wt, a.pos, a.add, a.y, s);
+}
+
+}  // namespace qmoe

@@ -16,7 +16,8 @@ constexpr int TOPK_MAX_K = 16;
 constexpr int TOPK_MAX_PER_LANE = MAX_EXPERTS / 64;
 constexpr int ROUTER_ROWS_MAX_T = 8;  // above this the tiled router runs (router + top-k measured 29 / 32 us at 8 tokens, 51 / 33 us at 16)
 constexpr int GATE_MAX_GROUPS = 64;
-constexpr int BS_MAX_K = 16384, BS_MAX_N = 65536, BS_MAX_ROWS = 1 << 20;  // block-scaled operators
+constexpr int BS_MAX_K = 16384, BS_MAX_N = 65536, BS_MAX_ROWS = 1 << 20;  // block-scaled and int8 operators
+constexpr int BALANCE_MAX_S = 65536;  // sequences
 constexpr int BS_MAX_LDX = 1 << 22;  // (a tile's rows are addressed with 31-bit byte offsets)
 constexpr int DECODE_MAX_T = MOE_DECODE_MAX_T;            // the decode path's limit
 constexpr int AUTO_DECODE_MAX_T = MOE_AUTO_DECODE_MAX_T;  // MOE_PATH_AUTO's switch to prefill
@@ -221,6 +222,83 @@ struct BsDown {
 };
 size_t bs_down_ws(int T, int k, int d);
 hipError_t launch_bs_down(const BsDown& a, hipStream_t s);
+
+// y[t] = add[t] + sum_j wt[t][j] ye[pos[t k + j]], timed under `name`
+hipError_t launch_combine(const char* name, const float* ye, int T, int k, int d, const float* wt, const int32_t* pos,
+                          const float* add, float* y, hipStream_t s);
+
+// int8_quant.hip, int8_matmul.hip, int8_experts.hip: int8 operators with a scale
+// per row and per output channel (arguments as in include/moe.h)
+hipError_t launch_i8_quantize(const void* x, int x_dtype, int64_t ldx, int M, int K, int8_t* q, int64_t ldq, float* s,
+                              hipStream_t st);
+struct I8Matmul {
+  const int8_t* xq;
+  int64_t ldx;
+  const float* xs;
+  int M;
+  const int8_t* wq;
+  const float* ws;
+  int N, K;
+  void* y;
+  int y_dtype;
+  int64_t ldy;
+  int* part;  // i8_matmul_ws() bytes
+};
+size_t i8_matmul_ws(int M, int N, int K);
+hipError_t launch_i8_matmul(const I8Matmul& a, hipStream_t s);
+struct I8Gateup {
+  const int8_t* xq;
+  const float* xs;
+  int T, k;
+  const int32_t *offsets, *perm;
+  int E;
+  const int8_t* w_gate;
+  const float* s_gate;
+  const int8_t* w_up;
+  const float* s_up;
+  int f, d;
+  void* h;
+  int h_dtype;
+};
+hipError_t launch_i8_gateup(const I8Gateup& a, hipStream_t s);
+struct I8Down {
+  const int8_t* hq;
+  const float* hs;
+  int T, k;
+  const float* wt;
+  const int32_t *offsets, *pos;
+  int E;
+  const int8_t* w_down;
+  const float* s_down;
+  int d, f;
+  const float* add;  // nullable
+  float* y;
+  float* ye;  // i8_down_ws() bytes: the bucket rows' products [T k][d]
+};
+size_t i8_down_ws(int T, int k, int d);
+hipError_t launch_i8_down(const I8Down& a, hipStream_t s);
+
+// balance.hip (arguments as in include/moe.h)
+struct Balance {
+  const void* z;
+  int z_dtype;
+  int64_t z_stride;
+  int T, E;
+  const int32_t* idx;
+  int k, softmax;
+  float alpha;
+  const int32_t* starts;  // nullable
+  int S;
+  int32_t *counts, *tokens;
+  float* loss;         // forward
+  float* q;            // forward: balance_ws() bytes, a number for each token
+  const float* grad;   // backward: [S]
+  void* dz;
+  int64_t dz_stride;
+};
+size_t balance_ws(int T);
+hipError_t launch_balance_loss(const Balance& a, hipStream_t s);
+hipError_t launch_balance_backward(const Balance& a, hipStream_t s);
 
 // repack.hip: n_rows rows of K inputs
 hipError_t launch_repack(int fmt, int64_t n_rows, int K, const void* src, void* dst, int to_device, hipStream_t s);

@@ -123,6 +123,19 @@ def lib() -> ctypes.CDLL:
             "moe_blockscale_down_workspace_bytes": ([_I32, _I32, _I32, ctypes.POINTER(_SZ)], ctypes.c_int),
             "moe_blockscale_down": ([_P, _P, _I32, _I32, _P, _P, _P, _I32, _P, _P, _I32, _I32, _P, _P, _P, _SZ, _P],
                                     ctypes.c_int),
+            "moe_int8_quantize": ([_P, _I32, _I64, _I32, _I32, _P, _I64, _P, _P], ctypes.c_int),
+            "moe_int8_matmul_workspace_bytes": ([_I32, _I32, _I32, ctypes.POINTER(_SZ)], ctypes.c_int),
+            "moe_int8_matmul": ([_P, _I64, _P, _I32, _P, _P, _I32, _I32, _P, _I32, _I64, _P, _SZ, _P], ctypes.c_int),
+            "moe_int8_gateup": ([_P, _P, _I32, _I32, _P, _P, _I32, _P, _P, _P, _P, _I32, _I32, _P, _I32, _P],
+                                ctypes.c_int),
+            "moe_int8_down_workspace_bytes": ([_I32, _I32, _I32, ctypes.POINTER(_SZ)], ctypes.c_int),
+            "moe_int8_down": ([_P, _P, _I32, _I32, _P, _P, _P, _I32, _P, _P, _I32, _I32, _P, _P, _P, _SZ, _P],
+                              ctypes.c_int),
+            "moe_balance_loss_workspace_bytes": ([_I32, _I32, _I32, ctypes.POINTER(_SZ)], ctypes.c_int),
+            "moe_balance_loss": ([_P, _I32, _I64, _I32, _I32, _P, _I32, _I32, ctypes.c_float, _P, _I32, _P, _P, _P, _P,
+                                  _SZ, _P], ctypes.c_int),
+            "moe_balance_loss_backward": ([_P, _I32, _I64, _I32, _I32, _P, _I32, _I32, ctypes.c_float, _P, _I32, _P, _P,
+                                           _P, _P, _I64, _P], ctypes.c_int),
             "moe_profile_enable": ([_I32], ctypes.c_int),
             "moe_profile_reset": ([], ctypes.c_int),
             "moe_profile_collect": ([_I32, _P, _P, _P, _P], ctypes.c_int),
@@ -419,6 +432,135 @@ def blockscale_down(hq, hs, wt, offsets, pos, w_down, s_down, y, workspace, add=
         if add is not None:
             _need(fn, add=(add, torch.float32, (T, d)))
         _not_here(fn, hq, hs, wt, offsets, pos, w_down, s_down, y, add, workspace=workspace)
+    if rc:
+        _check(rc)
+
+
+# ---------------------------------------------------------------------------
+# int8 operators
+# ---------------------------------------------------------------------------
+_I8 = (torch.int8,)
+
+
+def int8_quantize(x, q, s, stream=None) -> None:
+    """x [M][K] (float32 or bfloat16) to q int8 [M][K] and s [M]."""
+    rc = (_calls or _load_calls()).int8_quantize(x, q, s, stream)
+    if rc is None:
+        fn = "int8_quantize"
+        _rows_of(fn, "x", x, _XDT), _rows_of(fn, "q", q, _I8)
+        if q.shape != x.shape:
+            raise ValueError(f"{fn}: q has shape {tuple(q.shape)}, needs {tuple(x.shape)}")
+        _need(fn, s=(s, torch.float32, x.shape[:1]))
+        _not_here(fn, x, q, s)
+    if rc:
+        _check(rc)
+
+
+def int8_matmul_workspace_bytes(M: int, N: int, K: int) -> int:
+    out = _SZ()
+    _check(lib().moe_int8_matmul_workspace_bytes(M, N, K, ctypes.byref(out)))
+    return out.value
+
+
+def int8_matmul(xq, xs, wq, ws, y, workspace=None, stream=None) -> None:
+    """y [M][N] (float32 or bfloat16) = xq [M][K] times wq [N][K] transposed, int8,
+    with scales xs [M] and ws [N]."""
+    rc = (_calls or _load_calls()).int8_matmul(xq, xs, wq, ws, y, workspace, stream)
+    if rc is None:
+        fn = "int8_matmul"
+        _rows_of(fn, "xq", xq, _I8), _rows_of(fn, "y", y, _XDT)
+        (M, K), N = xq.shape, wq.shape[0]
+        if y.shape != (M, N):
+            raise ValueError(f"{fn}: y has shape {tuple(y.shape)}, needs {(M, N)}")
+        _need(fn, xs=(xs, torch.float32, (M,)), wq=(wq, torch.int8, (N, K)), ws=(ws, torch.float32, (N,)))
+        _not_here(fn, xq, xs, wq, ws, y, workspace=workspace)
+    if rc:
+        _check(rc)
+
+
+def int8_gateup(xq, xs, k, offsets, perm, w_gate, s_gate, w_up, s_up, h, stream=None) -> None:
+    """h [T*k][f] (float32 or bfloat16): the bucket rows' silu(gate) * up; offsets
+    and perm as bucket() writes them."""
+    rc = (_calls or _load_calls()).int8_gateup(xq, xs, k, offsets, perm, w_gate, s_gate, w_up, s_up, h, stream)
+    if rc is None:
+        fn = "int8_gateup"
+        (T, d), (E, f, _) = xq.shape, w_gate.shape
+        x_dtype_of(h)
+        _need(fn, xq=(xq, torch.int8, (T, d)), xs=(xs, torch.float32, (T,)), offsets=(offsets, torch.int32, (E + 1,)),
+              perm=(perm, torch.int32, (T * k,)), w_gate=(w_gate, torch.int8, (E, f, d)),
+              s_gate=(s_gate, torch.float32, (E, f)), w_up=(w_up, torch.int8, (E, f, d)),
+              s_up=(s_up, torch.float32, (E, f)), h=(h, h.dtype, (T * k, f)))
+        _not_here(fn, xq, xs, offsets, perm, w_gate, s_gate, w_up, s_up, h)
+    if rc:
+        _check(rc)
+
+
+def int8_down_workspace_bytes(T: int, k: int, d: int) -> int:
+    out = _SZ()
+    _check(lib().moe_int8_down_workspace_bytes(T, k, d, ctypes.byref(out)))
+    return out.value
+
+
+def int8_down(hq, hs, wt, offsets, pos, w_down, s_down, y, workspace, add=None, stream=None) -> None:
+    """y [T][d] = add + the weighted sum of each token's experts' down products."""
+    rc = (_calls or _load_calls()).int8_down(hq, hs, wt, offsets, pos, w_down, s_down, y, workspace, add, stream)
+    if rc is None:
+        fn = "int8_down"
+        (T, k), (E, d, f) = wt.shape, w_down.shape
+        _need(fn, hq=(hq, torch.int8, (T * k, f)), hs=(hs, torch.float32, (T * k,)), wt=(wt, torch.float32, (T, k)),
+              offsets=(offsets, torch.int32, (E + 1,)), pos=(pos, torch.int32, (T * k,)),
+              w_down=(w_down, torch.int8, (E, d, f)), s_down=(s_down, torch.float32, (E, d)),
+              y=(y, torch.float32, (T, d)))
+        if add is not None:
+            _need(fn, add=(add, torch.float32, (T, d)))
+        _not_here(fn, hq, hs, wt, offsets, pos, w_down, s_down, y, add, workspace=workspace)
+    if rc:
+        _check(rc)
+
+
+# ---------------------------------------------------------------------------
+# balance loss
+# ---------------------------------------------------------------------------
+def balance_loss_workspace_bytes(T: int, S: int, E: int) -> int:
+    out = _SZ()
+    _check(lib().moe_balance_loss_workspace_bytes(T, S, E, ctypes.byref(out)))
+    return out.value
+
+
+def _balance_need(fn, z, idx, counts, tokens, starts, **more) -> None:
+    _rows_of(fn, "z", z, _XDT)
+    (T, E), S = z.shape, counts.shape[0]
+    _need(fn, idx=(idx, torch.int32, (T, idx.shape[-1])), counts=(counts, torch.int32, (S, E)),
+          tokens=(tokens, torch.int32, (S,)), **{n: (t, torch.float32, (S,)) for n, t in more.items()})
+    if starts is not None:
+        _need(fn, starts=(starts, torch.int32, (S + 1,)))
+
+
+def balance_loss(z, idx, counts, tokens, loss, workspace, score="softmax", alpha=1.0, starts=None, stream=None) -> None:
+    """counts int32 [S][E], tokens int32 [S] and loss [S] of the logits z [T][E]
+    (float32 or bfloat16) and routes idx [T][k]; starts int32 [S + 1] or None (one
+    sequence)."""
+    rc = (_calls or _load_calls()).balance_loss(z, idx, counts, tokens, loss, workspace, _SCORES[score], alpha, starts, stream)
+    if rc is None:
+        fn = "balance_loss"
+        _balance_need(fn, z, idx, counts, tokens, starts, loss=loss)
+        _not_here(fn, z, idx, counts, tokens, loss, starts, workspace=workspace)
+    if rc:
+        _check(rc)
+
+
+def balance_loss_backward(z, idx, counts, tokens, grad_loss, dz, score="softmax", alpha=1.0, starts=None,
+                          stream=None) -> None:
+    """dz [T][E] (z's dtype) of grad_loss [S]; counts and tokens as balance_loss left them."""
+    rc = (_calls or _load_calls()).balance_loss_backward(z, idx, counts, tokens, grad_loss, dz, _SCORES[score], alpha, starts,
+                                                         stream)
+    if rc is None:
+        fn = "balance_loss_backward"
+        _balance_need(fn, z, idx, counts, tokens, starts, grad_loss=grad_loss)
+        _rows_of(fn, "dz", dz, (z.dtype,))
+        if dz.shape != z.shape:
+            raise ValueError(f"{fn}: dz has shape {tuple(dz.shape)}, needs {tuple(z.shape)}")
+        _not_here(fn, z, idx, counts, tokens, grad_loss, dz, starts)
     if rc:
         _check(rc)
 
