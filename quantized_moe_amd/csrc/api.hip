@@ -1283,7 +1283,7 @@ extern "C" int moe_balance_loss_workspace_bytes(int32_t T, int32_t S, int32_t E,
   if (!bytes) return fail(MOE_ERR_INVALID_ARG, "%s: bytes is null", fn);
   const int rc = check_balance(fn, MOE_F32, E, T, E, 1, MOE_SCORE_SIGMOID, 1.0f, S);
   if (rc) return rc;
-  *bytes = balance_ws(T);
+  *bytes = balance_ws(T, S, E);
   return ok();
 }
 
@@ -1303,12 +1303,12 @@ extern "C" int moe_balance_loss(const void* z, int32_t z_dtype, int64_t z_stride
   NEED_PTR(counts, "counts");
   NEED_PTR(tokens, "tokens");
   NEED_PTR(loss, "loss");
-  const size_t need = balance_ws(T);
+  const size_t need = balance_ws(T, S, E);
   if (workspace_bytes < need)
     return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, workspace_bytes, need);
   if (need) NEED_PTR(workspace, "workspace");
   Balance a{z, z_dtype, z_stride, T, E, idx, k, score == MOE_SCORE_SOFTMAX, alpha, starts, S, counts, tokens, loss,
-            (float*)workspace, nullptr, nullptr, 0};
+            (double*)workspace, nullptr, nullptr, 0};
   hipError_t e = launch_balance_loss(a, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, fn);
   return ok();

@@ -291,12 +291,12 @@ struct Balance {
   int S;
   int32_t *counts, *tokens;
   float* loss;         // forward
-  float* q;            // forward: balance_ws() bytes, a number for each token
+  double* q;           // forward: balance_ws() bytes, sums of runs of tokens
   const float* grad;   // backward: [S]
   void* dz;
   int64_t dz_stride;
 };
-size_t balance_ws(int T);
+size_t balance_ws(int T, int S, int E);
 hipError_t launch_balance_loss(const Balance& a, hipStream_t s);
 hipError_t launch_balance_backward(const Balance& a, hipStream_t s);
 

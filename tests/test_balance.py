@@ -98,7 +98,7 @@ def forward(z, idx, starts, score, alpha, S, explicit=True):
     return c, n, loss, st
 
 
-CASES = [(0, 8, 2, 1), (1, 1, 1, 1), (1, 384, 6, 1), (5, 3, 2, 2), (64, 384, 6, 1), (70, 64, 4, 3), (300, 65, 16, 7), (257, 1000, 8, 2),
+CASES = [(0, 8, 2, 1), (0, 16, 2, 2000), (128, 384, 6, 32), (128, 384, 6, 33), (129, 384, 6, 3), (3, 5, 5, 1700), (4097, 9, 3, 1500), (1, 1, 1, 1), (1, 384, 6, 1), (5, 3, 2, 2), (64, 384, 6, 1), (70, 64, 4, 3), (300, 65, 16, 7), (257, 1000, 8, 2),
          (1024, 384, 6, 5), (1500, 130, 3, 200), (2100, 200, 6, 1), (9000, 16, 2, 300), (20000, 40, 2, 1)]
 
 
