@@ -139,13 +139,22 @@ __global__ __launch_bounds__(256) void combine_routes_kernel(const float* __rest
   const int c = (int)(i - t * d4);
   f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
   if (add) v = reinterpret_cast<const f32x4_t*>(add)[i];
-  for (int j = 0; j < k; j++) {
-    const int p = pos[t * k + j];
-    if ((uint32_t)p >= (uint32_t)(T * k)) continue;  // a route without a place
-    const float w = wt[t * k + j];
-    const f32x4_t u = reinterpret_cast<const f32x4_t*>(ye)[(int64_t)p * d4 + c];
+  for (int j0 = 0; j0 < k; j0 += 4) {  // four routes requested at a time, added in their order
+    int p[4];
+    f32x4_t u[4];
 #pragma unroll
-    for (int q = 0; q < 4; q++) v[q] = __builtin_fmaf(w, u[q], v[q]);
+    for (int j = 0; j < 4; j++) p[j] = j0 + j < k ? pos[t * k + j0 + j] : -1;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      if ((uint32_t)p[j] >= (uint32_t)(T * k)) p[j] = -1;  // a route without a place
+      u[j] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(ye) + (int64_t)max(p[j], 0) * d4 + c);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const float w = p[j] >= 0 ? wt[t * k + j0 + j] : 0.0f;
+#pragma unroll
+      for (int q = 0; q < 4; q++) v[q] = p[j] >= 0 ? __builtin_fmaf(w, u[j][q], v[q]) : v[q];
+    }
   }
   reinterpret_cast<f32x4_t*>(y)[i] = v;
 }

@@ -23,27 +23,15 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void i8_gateup_kerne
       lds, wbuf, wsbuf, a.d, xbuf, xsbuf, [&](int i) { return i < t.rows ? (uint32_t)token(i) * a.d : BUFFER_OUT; },
       [&](int i) { return i < t.rows ? (uint32_t)token(i) * 4 : BUFFER_OUT; }, 0, (a.d + C::BK - 1) / C::BK, acc);
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & (C::MF - 1), half = lane / C::MF;
-  const int wn = wave % C::WN, wm = wave / C::WN;
+  i8_store<C>(lds, static_cast<OUT*>(a.h) + (int64_t)t.row0 * a.f + n0, a.f, t.rows, rows_n, true,  // f is a multiple of 16
+              [&](int i, int j, int g, int n, float xs) {
+                const f32x4_t gate = i8_values(i8_run(acc[0][i][j], g), xs, i8_wscale<C>(lds, 0, n));
+                const f32x4_t up = i8_values(i8_run(acc[1][i][j], g), xs, i8_wscale<C>(lds, 1, n));
+                f32x4_t h;
 #pragma unroll
-  for (int j = 0; j < C::TM; j++) {
-    const int mi = (wm * C::TM + j) * C::MF + r;
-    if (mi >= t.rows) continue;
-    const float xs = i8_xscale<C>(lds, mi);
-    OUT* row = static_cast<OUT*>(a.h) + (int64_t)(t.row0 + mi) * a.f + n0;
-#pragma unroll
-    for (int i = 0; i < C::TN; i++)
-#pragma unroll
-      for (int g = 0; g < C::Step::RUNS; g++) {
-        const int ni = (wn * C::TN + i) * C::MF + 8 * g + 4 * half;
-        const f32x4_t gate = i8_values(i8_run(acc[0][i][j], g), xs, i8_wscale<C>(lds, 0, ni));
-        const f32x4_t up = i8_values(i8_run(acc[1][i][j], g), xs, i8_wscale<C>(lds, 1, ni));
-        f32x4_t h;
-#pragma unroll
-        for (int q = 0; q < 4; q++) h[q] = silu(gate[q]) * up[q];
-        store4(row + ni, h, rows_n - ni, true);  // f is a multiple of 16
-      }
-  }
+                for (int q = 0; q < 4; q++) h[q] = silu(gate[q]) * up[q];
+                return h;
+              });
 }
 
 template <class C, typename OUT>
@@ -59,10 +47,8 @@ static hipError_t launch_gateup(const I8Gateup& a, hipStream_t s) {
 
 template <typename OUT>
 static hipError_t pick_gateup(const I8Gateup& a, hipStream_t s) {
-  const int64_t n = (int64_t)a.T * a.k, E = a.E;
-  if (n <= 4 * E) return launch_gateup<I8Tile<16, 8, 1, 1, 1, 128, 2, 1, 2>, OUT>(a, s);
-  if (n <= 32 * E) return launch_gateup<I8Tile<32, 4, 1, 1, 1, 128, 2, 1, 2>, OUT>(a, s);
-  return launch_gateup<I8Tile<32, 4, 1, 1, 2, 128, 2, 1, 2>, OUT>(a, s);
+  if ((int64_t)a.T * a.k <= 48 * (int64_t)a.E) return launch_gateup<I8Tile<32, 2, 1, 1, 2, 128, 3, 1, 2>, OUT>(a, s);
+  return launch_gateup<I8Tile<32, 2, 2, 1, 2, 128, 2, 1, 2>, OUT>(a, s);
 }
 
 hipError_t launch_i8_gateup(const I8Gateup& a, hipStream_t s) {
@@ -85,22 +71,9 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void i8_down_kernel(
   i8_product<C>(
       lds, wbuf, wsbuf, a.f, xbuf, xsbuf, [&](int i) { return i < t.rows ? (uint32_t)(i * a.f) : BUFFER_OUT; },
       [&](int i) { return (uint32_t)(i * 4); }, 0, (a.f + C::BK - 1) / C::BK, acc);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & (C::MF - 1), half = lane / C::MF;
-  const int wn = wave % C::WN, wm = wave / C::WN;
-#pragma unroll
-  for (int j = 0; j < C::TM; j++) {
-    const int mi = (wm * C::TM + j) * C::MF + r;
-    if (mi >= t.rows) continue;
-    const float xs = i8_xscale<C>(lds, mi);
-    float* row = a.ye + (int64_t)(t.row0 + mi) * a.d + n0;
-#pragma unroll
-    for (int i = 0; i < C::TN; i++)
-#pragma unroll
-      for (int g = 0; g < C::Step::RUNS; g++) {
-        const int ni = (wn * C::TN + i) * C::MF + 8 * g + 4 * half;
-        store4(row + ni, i8_values(i8_run(acc[0][i][j], g), xs, i8_wscale<C>(lds, 0, ni)), rows_n - ni, true);
-      }
-  }
+  i8_store<C>(lds, a.ye + (int64_t)t.row0 * a.d + n0, a.d, t.rows, rows_n, true, [&](int i, int j, int g, int n, float xs) {
+    return i8_values(i8_run(acc[0][i][j], g), xs, i8_wscale<C>(lds, 0, n));
+  });
 }
 
 // One or two tokens: one launch and no workspace.  A block owns 16 outputs of one
@@ -216,9 +189,9 @@ static hipError_t launch_down(const I8Down& a, hipStream_t s) {
 
 static hipError_t launch_down_products(const I8Down& a, hipStream_t s) {
   const int64_t n = (int64_t)a.T * a.k, E = a.E;
-  if (n <= 2 * E) return launch_down<I8Tile<16, 8, 1, 1, 1, 128, 2, 1, 1>>(a, s);
-  if (n <= 32 * E) return launch_down<I8Tile<32, 4, 1, 2, 1, 128, 2, 1, 1>>(a, s);
-  return launch_down<I8Tile<32, 4, 1, 2, 2, 128, 2, 1, 1>>(a, s);
+  if (n <= 2 * E) return launch_down<I8Tile<32, 2, 2, 2, 1, 128, 3, 1, 1>>(a, s);
+  if (n <= 128 * E) return launch_down<I8Tile<32, 2, 1, 2, 2, 128, 2, 1, 1>>(a, s);
+  return launch_down<I8Tile<32, 2, 2, 2, 2, 128, 2, 1, 1>>(a, s);
 }
 
 hipError_t launch_i8_down(const I8Down& a, hipStream_t s) {
@@ -229,7 +202,7 @@ hipError_t launch_i8_down(const I8Down& a, hipStream_t s) {
     return hipGetLastError();
   }
   const int pid = prof_begin("i8_down", s);
-  hipError_t e = launch_down_products(a, s);
+  const hipError_t e = launch_down_products(a, s);
   prof_end(pid, s);
   if (e != hipSuccess) return e;
   return launch_combine("i8_combine", a.ye, a.T, a.k, a.d, a.wt, a.pos, a.add, a.y, s);

@@ -3,62 +3,52 @@
 
 namespace qmoe {
 
-// Few rows (M <= 16 TM): bound by the weights' bytes, each read once.  A block
-// owns 16 TN outputs and all rows, its 8 waves share K 128 inputs at a time;
-// operands go straight to registers, U runs of 128 requested at a time, so that a
-// call of a few MB is one round trip to memory.
-template <int TN, int TM, int U, typename OUT>
+// Few rows (M <= 16): bound by the weights' bytes, each read once.  A block owns 16
+// outputs and all rows, its 8 waves share K 128 inputs at a time; operands go straight
+// to registers, U runs of 128 requested at a time, so that a call of a few MB is one
+// round trip to memory.
+template <int U, typename OUT>
 __global__ __launch_bounds__(512) void i8_matmul_rows_kernel(I8Matmul a) {
-  using Step = I8Step<16>;
-  __shared__ i32x4_t part[8][TN * TM][64];
+  __shared__ i32x4_t part[8][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, quad = lane >> 4;
-  const int n0 = blockIdx.x * 16 * TN, KB = bs_blocks(a.K);
-  const __amdgpu_buffer_rsrc_t wbuf = buffer_of(a.wq + (int64_t)n0 * a.K, (int64_t)min(16 * TN, a.N - n0) * a.K);
+  const int n0 = blockIdx.x * 16, KB = bs_blocks(a.K);
+  const __amdgpu_buffer_rsrc_t wbuf = buffer_of(a.wq + (int64_t)n0 * a.K, (int64_t)min(16, a.N - n0) * a.K);
   const __amdgpu_buffer_rsrc_t xbuf = buffer_of(a.xq, (a.M - 1) * a.ldx + a.K);
   const uint32_t woff = r * a.K + 16 * quad;
-  uint32_t xoff[TM];
-#pragma unroll
-  for (int j = 0; j < TM; j++) xoff[j] = 16 * j + r < a.M ? (uint32_t)((16 * j + r) * a.ldx) + 16 * quad : BUFFER_OUT;
-  // wave v stores tile v: its scales are requested with the codes
-  const int m = 16 * (wave % TM) + r, n = n0 + 16 * (wave / TM) + 4 * quad;
+  const uint32_t xoff = r < a.M ? (uint32_t)(r * a.ldx) + 16 * quad : BUFFER_OUT;
+  // wave 0 stores: its scales are requested with the codes
+  const int n = n0 + 4 * quad;
   const __amdgpu_buffer_rsrc_t xsbuf = buffer_of(a.xs, (int64_t)a.M * 4), wsbuf = buffer_of(a.ws, (int64_t)a.N * 4);
-  const float xs = buffer_load4(xsbuf, wave < TN * TM ? m * 4 : BUFFER_OUT);
+  const float xs = buffer_load4(xsbuf, wave == 0 ? r * 4 : BUFFER_OUT);
   f32x4_t ws;
 #pragma unroll
-  for (int q = 0; q < 4; q++) ws[q] = buffer_load4(wsbuf, wave < TN * TM ? (n + q) * 4 : BUFFER_OUT);
-  typename Step::Acc acc[TN][TM] = {};
+  for (int q = 0; q < 4; q++) ws[q] = buffer_load4(wsbuf, wave == 0 ? (n + q) * 4 : BUFFER_OUT);
+  i32x4_t acc = {0, 0, 0, 0};
   for (int k0 = wave; k0 < KB; k0 += 8 * U) {
-    i32x4_t w[U][TN][2], x[U][TM][2];
+    i32x4_t w[U][2], x[U][2];
 #pragma unroll
     for (int u = 0; u < U; u++)
 #pragma unroll
       for (int h = 0; h < 2; h++) {
         const int c = (k0 + 8 * u) * BS + 64 * h;
         const uint32_t o = c + 16 * quad < a.K ? c : BUFFER_OUT;
-#pragma unroll
-        for (int i = 0; i < TN; i++) w[u][i][h] = buffer_load16(wbuf, woff + 16 * i * a.K + o);
-#pragma unroll
-        for (int j = 0; j < TM; j++) x[u][j][h] = buffer_load16(xbuf, out_or_sum(xoff[j], o));
+        w[u][h] = buffer_load16(wbuf, woff + o);
+        x[u][h] = buffer_load16(xbuf, out_or_sum(xoff, o));
       }
 #pragma unroll
     for (int u = 0; u < U; u++)
 #pragma unroll
-      for (int h = 0; h < 2; h++)
-#pragma unroll
-        for (int i = 0; i < TN; i++)
-#pragma unroll
-          for (int j = 0; j < TM; j++) acc[i][j] = Step::mul(w[u][i][h], x[u][j][h], acc[i][j]);
+      for (int h = 0; h < 2; h++) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u][h], x[u][h], acc, 0, 0, 0);
   }
-#pragma unroll
-  for (int i = 0; i < TN * TM; i++) part[wave][i][lane] = acc[i / TM][i % TM];
+  part[wave][lane] = acc;
   __syncthreads();
-  if (wave >= TN * TM) return;
-  i32x4_t y = part[0][wave][lane];
+  if (wave > 0) return;
+  i32x4_t y = part[0][lane];
 #pragma unroll
-  for (int u = 1; u < 8; u++) y += part[u][wave][lane];
+  for (int u = 1; u < 8; u++) y += part[u][lane];
   const bool vec = a.ldy % 4 == 0 && ((uintptr_t)a.y & (4 * sizeof(OUT) - 1)) == 0;
-  if (m < a.M) store4(static_cast<OUT*>(a.y) + m * a.ldy + n, i8_values(y, xs, ws), a.N - n, vec);
+  if (r < a.M) store4(static_cast<OUT*>(a.y) + r * a.ldy + n, i8_values(y, xs, ws), a.N - n, vec);
 }
 
 // grid.y > 1: K is shared by that many blocks of a tile; each leaves its sums in
@@ -105,22 +95,28 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void i8_matmul_tile_
     }
     return;
   }
-  OUT* y = static_cast<OUT*>(a.y);
-  // four outputs leave as one store where every row allows it
-  const bool vec = a.ldy % 4 == 0 && ((uintptr_t)a.y & (4 * sizeof(OUT) - 1)) == 0;
+  OUT* y = static_cast<OUT*>(a.y) + m0 * a.ldy + n0;
+  if constexpr (C::KS == 1) {
+    const bool vec = a.ldy * sizeof(OUT) % 16 == 0 && ((uintptr_t)a.y & 15) == 0;
+    i8_store<C>(lds, y, a.ldy, rows_m, rows_n, vec, [&](int i, int j, int g, int n, float xs) {
+      return i8_values(i8_run(acc[0][i][j], g), xs, i8_wscale<C>(lds, 0, n));
+    });
+  } else {
+    // four outputs leave as one store where every row allows it
+    const bool vec = a.ldy % 4 == 0 && ((uintptr_t)a.y & (4 * sizeof(OUT) - 1)) == 0;
 #pragma unroll
-  for (int j = 0; j < C::TM; j++) {
-    const int mi = (wm * C::TM + j) * C::MF + r, m = m0 + mi;
-    if (m >= a.M) continue;
-    const float xs = i8_xscale<C>(lds, mi);
-    OUT* row = y + m * a.ldy;
+    for (int j = 0; j < C::TM; j++) {
+      const int mi = (wm * C::TM + j) * C::MF + r;
+      if (mi >= rows_m) continue;
+      const float xs = i8_xscale<C>(lds, mi);
 #pragma unroll
-    for (int i = 0; i < C::TN; i++)
+      for (int i = 0; i < C::TN; i++)
 #pragma unroll
-      for (int g = 0; g < C::Step::RUNS; g++) {
-        const int ni = (wn * C::TN + i) * C::MF + 8 * g + 4 * half;
-        store4(row + n0 + ni, i8_values(i8_run(acc[0][i][j], g), xs, i8_wscale<C>(lds, 0, ni)), a.N - n0 - ni, vec);
-      }
+        for (int g = 0; g < C::Step::RUNS; g++) {
+          const int ni = (wn * C::TN + i) * C::MF + 8 * g + 4 * half;
+          store4(y + mi * a.ldy + ni, i8_values(i8_run(acc[0][i][j], g), xs, i8_wscale<C>(lds, 0, ni)), rows_n - ni, vec);
+        }
+    }
   }
 }
 
@@ -143,13 +139,10 @@ static int64_t tile_count(int M, int N, int bm, int bn) {
   return (int64_t)((M + bm - 1) / bm) * ((N + bn - 1) / bn);
 }
 
-static int split_k(int M, int N, int K) {
-  const int64_t tiles = tile_count(M, N, 64, 64);
-  const int KB = bs_blocks(K);
-  if (M <= 32 || tiles > 128 || KB < 32) return 1;
-  const int64_t s = 256 / tiles < KB / 8 ? 256 / tiles : KB / 8;
-  return (int)s;
-}
+// Blocks that share a tile's K: four, with a launch more to add their sums, where the
+// 32 x 32 tiles leave three quarters of the CUs idle and K is past 8192.  us for one
+// and four: 33 x 256 x 16384 12.0 and 8.8, x 8192 8.1 and 7.9 (24 x 256: 8.1 and 7.7).
+static int split_k(int M, int N, int K) { return K > 8192 && tile_count(M, N, 32, 32) <= 64 ? 4 : 1; }
 
 size_t i8_matmul_ws(int M, int N, int K) {
   const int s = split_k(M, N, K);
@@ -175,23 +168,63 @@ static hipError_t launch_tile(const I8Matmul& a, hipStream_t s, int parts = 1) {
   return hipGetLastError();
 }
 
-template <int TN, int TM, int U, typename OUT>
+template <typename OUT>
 static hipError_t launch_rows(const I8Matmul& a, hipStream_t s) {
-  auto* k = i8_matmul_rows_kernel<TN, TM, U, OUT>;
+  auto* k = i8_matmul_rows_kernel<4, OUT>;
   const int pid = prof_begin("i8_matmul", s);
-  QMOE_LAUNCH(k, dim3((a.N + 16 * TN - 1) / (16 * TN)), dim3(512), 0, s, a);
+  QMOE_LAUNCH(k, dim3((a.N + 15) / 16), dim3(512), 0, s, a);
   prof_end(pid, s);
   return hipGetLastError();
 }
 
+// The variant: up to 16 rows straight from memory; else the tile (rows x outputs)
+// that costs least, as a part for each begun round of tiles over the CUs and a part
+// for the tiles themselves (more of them at work lower the clock).  Fitted to N = K =
+// 4096, bf16 outputs, us at M rows (in brackets what the model says):
+//    32 x 32, 8 wave groups share K   64 7.2 (6.5)    128 12.5 (13)
+//    64 x 32, 4                       64 8.4 (8.1)    128 8.7 (8.6)    256 15.8 (17.2)
+//    64 x 64, 2                       128 10.3 (9.8)  256 10.7 (10.7)  512 19.8 (21.4)   704 30.1 (31.6)
+//    64 x 96, 2                       512 24.8 (24.9) 700 26.6 (27.6)  1000 x 2500 26.7 (26.7)
+//    64 x 128                         384 13.8 (13.9) 512 14.8 (14.8)  640 28.2 (26.9)
+//   128 x 128, four stages            640 19.8 (19.7) 768 20.3 (20.7)  1024 22.2 (22.8)  2048 45.1 (45.6)
+//   128 x 128, two, two blocks a CU   1024 26.6 (26.5) 1500 32.8 (32.8) 2048 39.0 (39.0) 2800 59 (62)  5000 93 (104)
+//   256 x 256                         2048 45.7 (45.5) 2800 48.4 (51.3) 4096 61.3 (61.0)  5000 110 (99)
+// 8192 x 8192 x 8192 on 256 x 256: 444 to 458 (2.4 POP/s; the library's int8 product
+// without scales 526).  There the card's power is the bound: tiles that need fewer
+// cycles ran at a lower clock (798 thousand at 1.68 GHz, 922 at 1.97), and the same
+// loop without its copies into LDS took 367.
+// Rows against 32 x 32 tiles at M = 1, 8 and 16: 4096 x 4096 5.3, 6.0 and 6.6 for 6.6;
+// 8192 x 8192 14.1, 15.3 and 17.8 for 13; 700 x 1040 3.8 for 4.9.
 template <typename OUT>
 static hipError_t launch_matmul(const I8Matmul& a, hipStream_t s) {
-  if (a.M <= 16) return launch_rows<1, 1, 4, OUT>(a, s);
-  if (a.M <= 32) return launch_rows<1, 2, 2, OUT>(a, s);
-  auto tiles = [&](int bn, int bm) { return tile_count(a.M, a.N, bm, bn); };
-  if (tiles(256, 256) >= 192) return launch_tile<I8Tile<32, 2, 2, 4, 4, 64, 4, 1, 1>, OUT>(a, s);
-  if (tiles(128, 128) >= 128) return launch_tile<I8Tile<32, 2, 2, 2, 2, 128, 2, 2, 1>, OUT>(a, s);
-  return launch_tile<I8Tile<32, 2, 2, 1, 1, 128, 2, 3, 1>, OUT>(a, s, split_k(a.M, a.N, a.K));
+  const int parts = split_k(a.M, a.N, a.K);
+  if (a.M <= 16 && a.N <= 4096 && parts == 1) return launch_rows<OUT>(a, s);
+  static constexpr struct {
+    int bm, bn, round;
+    float begun, full;
+  } TILES[8] = {{32, 32, 256, 5.8f, 0.7f},    {64, 32, 256, 7.6f, 1.0f},    {64, 64, 256, 8.8f, 1.9f},   {64, 96, 256, 8.8f, 5.4f},
+                {64, 128, 256, 11.2f, 3.6f},  {128, 128, 256, 14.5f, 8.3f}, {128, 128, 512, 14.0f, 25.0f}, {256, 256, 256, 30.0f, 31.0f}};
+  int best = 0;
+  float least = INFINITY;
+  for (int i = 0; i < (parts == 1 ? 8 : 1); i++) {
+    const auto& x = TILES[i];
+    const int64_t n = tile_count(a.M, a.N, x.bm, x.bn);
+    const float cost = x.begun * (float)((n + x.round - 1) / x.round) + x.full * (float)n / (float)x.round;
+    if (cost < least) {
+      least = cost;
+      best = i;
+    }
+  }
+  switch (best) {
+    case 0: return launch_tile<I8Tile<32, 1, 1, 1, 1, 64, 3, 8, 1>, OUT>(a, s, parts);
+    case 1: return launch_tile<I8Tile<32, 1, 2, 1, 1, 128, 3, 4, 1>, OUT>(a, s);
+    case 2: return launch_tile<I8Tile<32, 2, 2, 1, 1, 128, 4, 2, 1>, OUT>(a, s);
+    case 3: return launch_tile<I8Tile<32, 3, 2, 1, 1, 128, 3, 2, 1>, OUT>(a, s);
+    case 4: return launch_tile<I8Tile<32, 4, 2, 1, 1, 128, 4, 1, 1>, OUT>(a, s);
+    case 5: return launch_tile<I8Tile<32, 4, 2, 1, 2, 64, 4, 1, 1>, OUT>(a, s);
+    case 6: return launch_tile<I8Tile<32, 4, 2, 1, 2, 128, 2, 1, 1>, OUT>(a, s);
+    default: return launch_tile<I8Tile<32, 4, 2, 2, 4, 128, 2, 1, 1>, OUT>(a, s);
+  }
 }
 
 hipError_t launch_i8_matmul(const I8Matmul& a, hipStream_t s) {

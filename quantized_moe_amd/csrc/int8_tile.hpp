@@ -59,8 +59,9 @@ struct I8Tile {
   static constexpr int SCALES = KS * ST * STAGE;  // [NMAT][BN] of the outputs, [BM] of the rows, behind the stages
   static constexpr int S_ROWS = (BM + 63) / 64 * 64;
   static constexpr int LDS = SCALES + (NMAT * ((BN + 63) / 64 * 64) + S_ROWS) * 4;
-  static constexpr int W_COPIES = BN / COPY_ROWS / WAVES, X_UNITS = BM / COPY_ROWS;
-  static constexpr int X_COPIES = (X_UNITS + WAVES - 1) / WAVES;  // (waves past the units bring some again)
+  static constexpr int W_UNITS = BN / COPY_ROWS, X_UNITS = BM / COPY_ROWS;
+  static constexpr int W_COPIES = (W_UNITS + WAVES - 1) / WAVES;  // (waves past the units bring some again)
+  static constexpr int X_COPIES = (X_UNITS + WAVES - 1) / WAVES;
   static constexpr int COPIES = NMAT * W_COPIES + X_COPIES;
   static constexpr int ROWS = NMAT * TN, FRAGS = ROWS + TM, MULS = ROWS * TM;
   static constexpr int REGS = ACC * MULS;  // accumulators of a lane
@@ -70,16 +71,18 @@ struct I8Tile {
   static constexpr int WAVES_PER_SIMD_REG = REGS > 128 ? 1 : REGS > 64 ? 2 : 4;
   static constexpr int WAVES_PER_SIMD = WAVES_PER_SIMD_LDS < WAVES_PER_SIMD_REG ? WAVES_PER_SIMD_LDS : WAVES_PER_SIMD_REG;
   static_assert(SUBS % 2 == 0, "operands alternate between two sets of registers");
-  static_assert(W_COPIES * COPY_ROWS * WAVES == BN && X_UNITS * COPY_ROWS == BM, "whole copies");
+  static_assert(W_UNITS * COPY_ROWS == BN && X_UNITS * COPY_ROWS == BM, "whole copies");
   static_assert((KS - 1) * WAVES * 64 * REGS * 4 <= SCALES, "the groups' sums fit the stages");
   static_assert(ST >= 2 && (ST - 1) * COPIES <= 63, "copies in flight are counted in 6 bits");
   static_assert(LDS <= 160 * 1024, "LDS of a CU");
 };
 
-// Where 16-byte piece p of row r lies in a stage's row.
+// Where 16-byte piece p of row r lies in a stage's row: so that the same piece of
+// 16 consecutive rows, which one cycle of a read takes, is in 16 different places
+// of LDS's 64 banks.
 template <int BK>
 __device__ __forceinline__ int i8_place(int r, int p) {
-  return BK == 128 ? p ^ (r & 7) : p ^ ((r >> 1) & 3);
+  return BK == 128 ? p ^ ((r >> 1) & 7) : p ^ ((r >> 2) & 3);
 }
 
 // acc[mat][i][j] = the wave's tiles of exact sums.  wbuf: the tile's rows of each
@@ -99,10 +102,10 @@ __device__ __forceinline__ bool i8_product(uint8_t* lds, const __amdgpu_buffer_r
   // l % PIECES (an involution: the piece that lies there).
   const int crow = lane / C::PIECES;
   uint32_t woff[C::W_COPIES], xoff[C::X_COPIES];
-  static_assert(C::COPY_ROWS % 8 == 0, "a copy's rows swizzle alike");
-  const int col = i8_place<BK>(crow, lane % C::PIECES) * 16;
+  static_assert(C::COPY_ROWS * WAVES % 16 == 0, "every copy of a wave is swizzled alike");  // (as BN and BM % 16 == 0)
+  const int col = i8_place<BK>(C::COPY_ROWS * wave + crow, lane % C::PIECES) * 16;
 #pragma unroll
-  for (int i = 0; i < C::W_COPIES; i++) woff[i] = (uint32_t)(C::COPY_ROWS * (wave + i * WAVES) + crow) * K + col;
+  for (int i = 0; i < C::W_COPIES; i++) woff[i] = (uint32_t)(C::COPY_ROWS * ((wave + i * WAVES) % C::W_UNITS) + crow) * K + col;
 #pragma unroll
   for (int i = 0; i < C::X_COPIES; i++) {
     const uint32_t o = xrow(C::COPY_ROWS * ((wave + i * WAVES) % C::X_UNITS) + crow);
@@ -114,7 +117,7 @@ __device__ __forceinline__ bool i8_product(uint8_t* lds, const __amdgpu_buffer_r
     const uint32_t at = base + stage * C::STAGE;
     if (i < C::NMAT * C::W_COPIES) {
       const int mat = i / C::W_COPIES, c = i % C::W_COPIES;
-      lds_copy16(wbuf[mat], at + mat * C::BN * BK + (wave + c * WAVES) * 1024, woff[c], kb * BK);
+      lds_copy16(wbuf[mat], at + mat * C::BN * BK + (wave + c * WAVES) % C::W_UNITS * 1024, woff[c], kb * BK);
     } else {
       const int c = i - C::NMAT * C::W_COPIES;
       lds_copy16(xbuf, at + C::W_BYTES + (wave + c * WAVES) % C::X_UNITS * 1024, xoff[c], kb * BK);
@@ -133,17 +136,17 @@ __device__ __forceinline__ bool i8_product(uint8_t* lds, const __amdgpu_buffer_r
   // the scales, 64 a copy, ahead of the codes
   {
     const uint32_t at = lds_address(lds + C::SCALES);
-    constexpr int W_UNITS = (C::BN + 63) / 64;
-    for (int u = block_wave; u < C::NMAT * W_UNITS + C::S_ROWS / 64; u += WAVES * KS) {
-      if (u < C::NMAT * W_UNITS) {
-        const int in = u % W_UNITS * 64 + lane;
+    constexpr int WS_UNITS = (C::BN + 63) / 64;
+    for (int u = block_wave; u < C::NMAT * WS_UNITS + C::S_ROWS / 64; u += WAVES * KS) {
+      if (u < C::NMAT * WS_UNITS) {
+        const int in = u % WS_UNITS * 64 + lane;
         const uint32_t off = in < C::BN ? in * 4 : BUFFER_OUT;
-        if (C::NMAT == 1 || u < W_UNITS)
+        if (C::NMAT == 1 || u < WS_UNITS)
           lds_copy4(wsbuf[0], at + u * 256, off, 0);
         else
           lds_copy4(wsbuf[C::NMAT - 1], at + u * 256, off, 0);
       } else {
-        const int i = (u - C::NMAT * W_UNITS) * 64 + lane;
+        const int i = (u - C::NMAT * WS_UNITS) * 64 + lane;
         lds_copy4(xsbuf, at + u * 256, i < C::BM ? srow(i) : BUFFER_OUT, 0);
       }
     }
@@ -248,6 +251,64 @@ __device__ __forceinline__ f32x4_t i8_values(i32x4_t sum, float xs, f32x4_t ws) 
 template <class Acc>
 __device__ __forceinline__ i32x4_t i8_run(const Acc& a, int g) {
   return i32x4_t{a[4 * g], a[4 * g + 1], a[4 * g + 2], a[4 * g + 3]};
+}
+
+// Stores the wave's tiles: value(i, j, g, n, xs) gives run g of tile (i, j), four
+// outputs from column n of the block's tile on, for a row of scale xs.  The lanes hold 4 outputs of
+// 32 rows each, 16 or 32 bytes a row of one store; through the stages (free by then,
+// each wave in a part of its own) they leave as whole lines.  vec: rows of 16-byte
+// pieces; rows, cols: how many the block's tile has.
+template <class C, typename OUT, class Value>
+__device__ __forceinline__ void i8_store(uint8_t* lds, OUT* out, int64_t ld, int rows, int cols, bool vec, Value&& value) {
+  static_assert(C::MF == 32 && C::KS == 1, "every wave stores");
+  constexpr int W = C::TN * 32, PIECE = 16 / sizeof(OUT), STRIDE = W * sizeof(OUT) + 16;
+  constexpr int LANES = W / PIECE, AT_ONCE = 64 / LANES;  // lanes of a row, rows of a store
+  static_assert(C::WAVES * 32 * STRIDE <= C::SCALES, "a part for every wave");
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 31, half = lane >> 5;
+  const int wn = wave % C::WN, wm = wave / C::WN;
+  uint8_t* mine = lds + wave * 32 * STRIDE;
+  const bool whole = vec && rows >= C::BM && cols >= C::BN;
+#pragma unroll
+  for (int j = 0; j < C::TM; j++) {
+    const int m0 = (wm * C::TM + j) * 32;
+    const float xs = i8_xscale<C>(lds, m0 + r);
+#pragma unroll
+    for (int i = 0; i < C::TN; i++)
+#pragma unroll
+      for (int g = 0; g < 4; g++) {
+        const int n = i * 32 + 8 * g + 4 * half;
+        store4(reinterpret_cast<OUT*>(mine + r * STRIDE) + n, value(i, j, g, wn * W + n, xs), 4, true);
+      }
+    auto piece = [&](int q) {
+      return *reinterpret_cast<const u32x4_t*>(mine + (q * AT_ONCE + lane / LANES) * STRIDE + lane % LANES * 16);
+    };
+    const int m = m0 + lane / LANES, n = wn * W + lane % LANES * PIECE;
+    OUT* to = out + m * ld + n;
+    if (whole) {
+#pragma unroll
+      for (int q = 0; q < 32 / AT_ONCE; q++) __builtin_nontemporal_store(piece(q), reinterpret_cast<u32x4_t*>(to + q * AT_ONCE * ld));
+    } else {
+#pragma unroll 1
+      for (int q = 0; q < 32 / AT_ONCE; q++) {
+        const u32x4_t v = piece(q);
+        if (m + q * AT_ONCE >= rows) break;
+        OUT* p = to + q * AT_ONCE * ld;
+        if (vec && n + PIECE <= cols) {
+          __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(p));
+        } else {
+#pragma unroll
+          for (int e = 0; e < PIECE; e++) {
+            OUT o;
+            if constexpr (sizeof(OUT) == 4)
+              o = __uint_as_float(v[e]);
+            else
+              o = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+            if (n + e < cols) p[e] = o;
+          }
+        }
+      }
+    }
+  }
 }
 
 }  // namespace qmoe

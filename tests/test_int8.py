@@ -131,7 +131,9 @@ def run_matmul(xq, xs, wq, ws, dtype, ldx=None, ldy=None, offset=0):
 
 SHAPES = [(1, 1, 16), (1, 17, 144), (3, 70, 272), (16, 64, 1040), (17, 33, 528), (32, 100, 4112), (33, 65, 48), (64, 64, 128),
           (65, 130, 400), (100, 300, 8192), (250, 1000, 4112), (257, 259, 144), (300, 640, 1040), (1000, 1100, 2064),
-          (700, 2500, 656), (1025, 1030, 80), (2048, 2050, 272), (4100, 3100, 208), (1, 4096, 4096), (24, 6200, 1040)]
+          (700, 2500, 656), (1025, 1030, 80), (2048, 2050, 272), (4100, 3100, 208), (1, 4096, 4096), (24, 6200, 1040),
+          (33, 250, 16384), (5, 70, 8208), (128, 4100, 272), (130, 2050, 144), (256, 4000, 144), (250, 5000, 80), (512, 3900, 208),
+          (450, 6100, 144), (1000, 3900, 144), (1024, 4096, 4096), (1500, 4090, 272), (2500, 4100, 144), (4090, 4090, 144)]
 
 
 @gpu
