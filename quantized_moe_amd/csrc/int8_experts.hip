@@ -23,7 +23,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void i8_gateup_kerne
       lds, wbuf, wsbuf, a.d, xbuf, xsbuf, [&](int i) { return i < t.rows ? (uint32_t)token(i) * a.d : BUFFER_OUT; },
       [&](int i) { return i < t.rows ? (uint32_t)token(i) * 4 : BUFFER_OUT; }, 0, (a.d + C::BK - 1) / C::BK, acc);
 
-  i8_store<C>(lds, static_cast<OUT*>(a.h) + (int64_t)t.row0 * a.f + n0, a.f, t.rows, rows_n, true,  // f is a multiple of 16
+  i8_store<C>(lds, static_cast<OUT*>(a.h) + (int64_t)t.row0 * a.f + n0, a.f, t.rows, rows_n, 16,  // f is a multiple of 16
               [&](int i, int j, int g, int n, float xs) {
                 const f32x4_t gate = i8_values(i8_run(acc[0][i][j], g), xs, i8_wscale<C>(lds, 0, n));
                 const f32x4_t up = i8_values(i8_run(acc[1][i][j], g), xs, i8_wscale<C>(lds, 1, n));
@@ -45,10 +45,14 @@ static hipError_t launch_gateup(const I8Gateup& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// The tile, by the rows that an expert has on average.  Measured, 384 experts x 4096 x
+// 2048 unless given, us for 64 rows x 64 outputs (three stages) / 128 x 64:
+//   0.02 rows (1 token) 18.9 / 24.8, 0.1 (8 tokens) 130 / 138, 4 (256) 1071 / 1184, 16 (1024) 1124 / 1277,
+//   48 (1024, 128 experts) 451 / 505, 96 (64 experts) 267 / 237, 256 (16 experts, crowded) 134 / 118
 template <typename OUT>
 static hipError_t pick_gateup(const I8Gateup& a, hipStream_t s) {
-  if ((int64_t)a.T * a.k <= 48 * (int64_t)a.E) return launch_gateup<I8Tile<32, 2, 1, 1, 2, 128, 3, 1, 2>, OUT>(a, s);
-  return launch_gateup<I8Tile<32, 2, 2, 1, 2, 128, 2, 1, 2>, OUT>(a, s);
+  if ((int64_t)a.T * a.k <= 64 * (int64_t)a.E) return launch_gateup<I8Tile<32, 2, 2, 1, 1, 128, 3, 1, 2>, OUT>(a, s);
+  return launch_gateup<I8Tile<32, 2, 4, 1, 1, 128, 2, 1, 2>, OUT>(a, s);
 }
 
 hipError_t launch_i8_gateup(const I8Gateup& a, hipStream_t s) {
@@ -71,7 +75,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void i8_down_kernel(
   i8_product<C>(
       lds, wbuf, wsbuf, a.f, xbuf, xsbuf, [&](int i) { return i < t.rows ? (uint32_t)(i * a.f) : BUFFER_OUT; },
       [&](int i) { return (uint32_t)(i * 4); }, 0, (a.f + C::BK - 1) / C::BK, acc);
-  i8_store<C>(lds, a.ye + (int64_t)t.row0 * a.d + n0, a.d, t.rows, rows_n, true, [&](int i, int j, int g, int n, float xs) {
+  i8_store<C>(lds, a.ye + (int64_t)t.row0 * a.d + n0, a.d, t.rows, rows_n, 16, [&](int i, int j, int g, int n, float xs) {
     return i8_values(i8_run(acc[0][i][j], g), xs, i8_wscale<C>(lds, 0, n));
   });
 }
@@ -187,9 +191,16 @@ static hipError_t launch_down(const I8Down& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// The tile, as for gate/up: 64 rows x 128 outputs on eight waves (to keep loads in
+// flight), on two (fewer reads of LDS), and 128 x 128.  The products without the sum:
+//   0.06 rows (4 tokens) 35.0 / 38.6 / 49.0, 0.1 (8 tokens) 72.9 / 76.4 / 78.3, 1 (64) 346 / 352 / 388,
+//   16 (1024) 606 / 606 / 637, 48 (512 over 64 experts) 122 / 123 / 129, 64 crowded 797 / 786 / 832,
+//   64 uniform 786 / 769 / 745, 384 (64 experts x 2000 x 1408) 169 / 165 / 147, 1024 (16 experts, crowded) 258 / 253 / 215
+// Bound by memory: without its matrix steps the 64-row product takes as long (819 us
+// then), without its stores 680.
 static hipError_t launch_down_products(const I8Down& a, hipStream_t s) {
   const int64_t n = (int64_t)a.T * a.k, E = a.E;
-  if (n <= 2 * E) return launch_down<I8Tile<32, 2, 2, 2, 1, 128, 3, 1, 1>>(a, s);
+  if (n <= 16 * E) return launch_down<I8Tile<32, 4, 2, 1, 1, 128, 2, 1, 1>>(a, s);
   if (n <= 128 * E) return launch_down<I8Tile<32, 2, 1, 2, 2, 128, 2, 1, 1>>(a, s);
   return launch_down<I8Tile<32, 2, 2, 2, 2, 128, 2, 1, 1>>(a, s);
 }

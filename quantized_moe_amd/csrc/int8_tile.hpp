@@ -256,10 +256,11 @@ __device__ __forceinline__ i32x4_t i8_run(const Acc& a, int g) {
 // Stores the wave's tiles: value(i, j, g, n, xs) gives run g of tile (i, j), four
 // outputs from column n of the block's tile on, for a row of scale xs.  The lanes hold 4 outputs of
 // 32 rows each, 16 or 32 bytes a row of one store; through the stages (free by then,
-// each wave in a part of its own) they leave as whole lines.  vec: rows of 16-byte
-// pieces; rows, cols: how many the block's tile has.
+// each wave in a part of its own) they leave as whole lines, past the caches.  align:
+// bytes that every row of the result is aligned to; rows, cols: how many the block's
+// tile has.
 template <class C, typename OUT, class Value>
-__device__ __forceinline__ void i8_store(uint8_t* lds, OUT* out, int64_t ld, int rows, int cols, bool vec, Value&& value) {
+__device__ __forceinline__ void i8_store(uint8_t* lds, OUT* out, int64_t ld, int rows, int cols, int align, Value&& value) {
   static_assert(C::MF == 32 && C::KS == 1, "every wave stores");
   constexpr int W = C::TN * 32, PIECE = 16 / sizeof(OUT), STRIDE = W * sizeof(OUT) + 16;
   constexpr int LANES = W / PIECE, AT_ONCE = 64 / LANES;  // lanes of a row, rows of a store
@@ -267,7 +268,7 @@ __device__ __forceinline__ void i8_store(uint8_t* lds, OUT* out, int64_t ld, int
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 31, half = lane >> 5;
   const int wn = wave % C::WN, wm = wave / C::WN;
   uint8_t* mine = lds + wave * 32 * STRIDE;
-  const bool whole = vec && rows >= C::BM && cols >= C::BN;
+  const bool whole = align >= 16 && rows >= C::BM && cols >= C::BN;
 #pragma unroll
   for (int j = 0; j < C::TM; j++) {
     const int m0 = (wm * C::TM + j) * 32;
@@ -293,8 +294,14 @@ __device__ __forceinline__ void i8_store(uint8_t* lds, OUT* out, int64_t ld, int
         const u32x4_t v = piece(q);
         if (m + q * AT_ONCE >= rows) break;
         OUT* p = to + q * AT_ONCE * ld;
-        if (vec && n + PIECE <= cols) {
+        if (align >= 16 && n + PIECE <= cols) {
           __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(p));
+        } else if (align >= 8 && n + PIECE <= cols) {
+          __builtin_nontemporal_store(u32x2_t{v[0], v[1]}, reinterpret_cast<u32x2_t*>(p));
+          __builtin_nontemporal_store(u32x2_t{v[2], v[3]}, reinterpret_cast<u32x2_t*>(p) + 1);
+        } else if (align >= 4 && n + PIECE <= cols) {
+#pragma unroll
+          for (int e = 0; e < 4; e++) __builtin_nontemporal_store(v[e], reinterpret_cast<uint32_t*>(p) + e);
         } else {
 #pragma unroll
           for (int e = 0; e < PIECE; e++) {

@@ -150,13 +150,13 @@ def test_matmul_is_exact(M, N, K):
 
 @gpu
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("M,N,K", [(2, 30, 272), (20, 66, 144), (70, 129, 400), (300, 640, 1040), (2050, 2050, 144)])
+@pytest.mark.parametrize("M,N,K", [(2, 30, 272), (20, 66, 144), (70, 129, 400), (300, 640, 1040), (450, 6100, 144), (1000, 3900, 144), (2050, 2050, 144), (4090, 4090, 144)])
 def test_matmul_strides_and_what_lies_beside(M, N, K, dtype):
     """Rows of x and y further apart, y at an address of its element only: nothing beside the outputs is written."""
     rng = np.random.default_rng(M)
     xq, xs, wq, ws = make_codes(rng, M, K), make_scales(rng, 1.0, M), make_codes(rng, N, K), make_scales(rng, 0.05, N)
     want = torch.from_numpy(product(xq, xs, wq, ws)).to(dtype)
-    for ldy in (N + 4, N + 3):
+    for ldy in (N + 4, N + 3, -(-N // 8) * 8 + 8, -(-N // 8) * 8 + 4, -(-N // 8) * 8 + 2):  # every alignment of a row
         y, ybuf = run_matmul(xq, xs, wq, ws, dtype, ldx=K + 48, ldy=ldy)
         assert torch.equal(y.cpu(), want)
         y.fill_(3.0)
