@@ -703,7 +703,7 @@ int moe_int8_down(const int8_t* hq, const float* hs, int32_t T, int32_t k, const
  * and 0 for masked experts and for tokens that take no part.
  *
  * z [T] rows of E logits in z_dtype (MOE_F32 or MOE_BF16), z_stride elements
- * apart (any element-aligned address); idx int32 [T][k]; dz as z, in the same
+ * apart; idx int32 [T][k]; all arrays but the workspace at any element-aligned address; dz as z, in the same
  * dtype, rounded once; counts and tokens of the forward call go into the backward
  * one.  Scores and sums are fp32 (exponentials and reciprocals of the hardware, a
  * few ulp), the sum over tokens fp64; identical inputs give bitwise identical

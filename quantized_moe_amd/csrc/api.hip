@@ -1275,8 +1275,13 @@ static int check_balance(const char* fn, int32_t z_dtype, int64_t z_stride, int3
   if (z_stride < E) return fail(MOE_ERR_INVALID_ARG, "%s: z_stride %lld below n_experts %d", fn, (long long)z_stride, E);
   return MOE_OK;
 }
-// Logits and their gradients: any address of their elements.
+// These operators read and write single elements: any address of one.
 static bool element_aligned(const void* p, int32_t dtype) { return ((uintptr_t)p & (dtype == MOE_BF16 ? 1u : 3u)) == 0; }
+#define NEED_WORDS(p, what)                                                                        \
+  do {                                                                                             \
+    if (!(p)) return fail(MOE_ERR_INVALID_ARG, "%s: %s is null", fn, what);                        \
+    if (!element_aligned(p, MOE_F32)) return fail(MOE_ERR_INVALID_ARG, "%s: %s is not 4-byte aligned", fn, what); \
+  } while (0)
 
 extern "C" int moe_balance_loss_workspace_bytes(int32_t T, int32_t S, int32_t E, size_t* bytes) {
   const char* fn = "moe_balance_loss_workspace_bytes";
@@ -1297,12 +1302,12 @@ extern "C" int moe_balance_loss(const void* z, int32_t z_dtype, int64_t z_stride
   if (T > 0) {
     if (!z) return fail(MOE_ERR_INVALID_ARG, "%s: z is null", fn);
     if (!element_aligned(z, z_dtype)) return fail(MOE_ERR_INVALID_ARG, "%s: z is not aligned to its elements", fn);
-    NEED_PTR(idx, "idx");
+    NEED_WORDS(idx, "idx");
   }
-  if (starts) NEED_PTR(starts, "starts");
-  NEED_PTR(counts, "counts");
-  NEED_PTR(tokens, "tokens");
-  NEED_PTR(loss, "loss");
+  if (starts) NEED_WORDS(starts, "starts");
+  NEED_WORDS(counts, "counts");
+  NEED_WORDS(tokens, "tokens");
+  NEED_WORDS(loss, "loss");
   const size_t need = balance_ws(T, S, E);
   if (workspace_bytes < need)
     return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, workspace_bytes, need);
@@ -1327,11 +1332,11 @@ extern "C" int moe_balance_loss_backward(const void* z, int32_t z_dtype, int64_t
   if (!z || !dz) return fail(MOE_ERR_INVALID_ARG, "%s: z or dz is null", fn);
   if (!element_aligned(z, z_dtype) || !element_aligned(dz, z_dtype))
     return fail(MOE_ERR_INVALID_ARG, "%s: z or dz is not aligned to its elements", fn);
-  NEED_PTR(idx, "idx");
-  if (starts) NEED_PTR(starts, "starts");
-  NEED_PTR(counts, "counts");
-  NEED_PTR(tokens, "tokens");
-  NEED_PTR(grad_loss, "grad_loss");
+  NEED_WORDS(idx, "idx");
+  if (starts) NEED_WORDS(starts, "starts");
+  NEED_WORDS(counts, "counts");
+  NEED_WORDS(tokens, "tokens");
+  NEED_WORDS(grad_loss, "grad_loss");
   Balance a{z, z_dtype, z_stride, T, E, idx, k, score == MOE_SCORE_SOFTMAX, alpha, starts, S, const_cast<int32_t*>(counts),
             const_cast<int32_t*>(tokens), nullptr, nullptr, grad_loss, dz, dz_stride};
   hipError_t e = launch_balance_backward(a, (hipStream_t)stream);

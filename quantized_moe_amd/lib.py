@@ -485,7 +485,7 @@ def int8_gateup(xq, xs, k, offsets, perm, w_gate, s_gate, w_up, s_up, h, stream=
     if rc is None:
         fn = "int8_gateup"
         (T, d), (E, f, _) = xq.shape, w_gate.shape
-        x_dtype_of(h)
+        _rows_of(fn, "h", h, _XDT)
         _need(fn, xq=(xq, torch.int8, (T, d)), xs=(xs, torch.float32, (T,)), offsets=(offsets, torch.int32, (E + 1,)),
               perm=(perm, torch.int32, (T * k,)), w_gate=(w_gate, torch.int8, (E, f, d)),
               s_gate=(s_gate, torch.float32, (E, f)), w_up=(w_up, torch.int8, (E, f, d)),

@@ -177,3 +177,100 @@ def test_even_load_gives_alpha():
         dz = torch.empty_like(z)
         lib.balance_loss_backward(z, torch.from_numpy(idx).to(DEV), c, n, torch.ones(1, device=DEV), dz, score=score, alpha=0.25)
         assert (dz == 0).all()
+
+
+# ------------------------------------------------------- the torch function ----
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,S", [(40, 3), (700, 4)])
+def test_autograd(T, S, score, dtype):
+    """balance.balance_loss as a training step uses it: with other terms of z, weights per sequence, logits that are not contiguous."""
+    from quantized_moe_amd import balance
+
+    rng = np.random.default_rng(T)
+    E, k = 24, 3
+    z, idx, starts = make(rng, T, E, k, S, dtype=dtype)
+    weights = rng.standard_normal(S).astype(np.float32)
+    leaf = z.t().contiguous().to(DEV).requires_grad_()          # z itself is its transpose
+    st, wt = torch.from_numpy(starts).to(DEV), torch.from_numpy(weights).to(DEV)
+    loss, counts, tokens = balance.balance_loss(leaf.t(), torch.from_numpy(idx).to(DEV), score=score, alpha=0.3, starts=st)
+    assert loss.requires_grad and not counts.requires_grad and not tokens.requires_grad
+    (loss * wt).sum().backward()
+    c, n, want, dz, unit = plain(z.double().numpy(), idx, starts, score, 0.3, weights)
+    assert np.array_equal(counts.cpu().numpy(), c) and np.array_equal(tokens.cpu().numpy(), n)
+    assert (np.abs(loss.detach().cpu().numpy() - want) <= want * (Q(E, 6.0) + STEP)).all()
+    tol = unit * (2 * Q(E, 6.0) + 8 * STEP) + (np.abs(dz) * 2.0 ** -8 * 1.01 if dtype == torch.bfloat16 else 0)
+    assert (np.abs(leaf.grad.t().double().cpu().numpy() - dz) <= tol + 2.0 ** -126).all()
+    # the mean over sequences: a broadcast gradient
+    leaf.grad = None
+    balance.balance_loss(leaf.t(), torch.from_numpy(idx).to(DEV), score=score, alpha=0.3, starts=st)[0].mean().backward()
+    dz, unit = plain(z.double().numpy(), idx, starts, score, 0.3, np.full(S, 1 / S, np.float32))[3:]
+    tol = unit * (2 * Q(E, 6.0) + 8 * STEP) + (np.abs(dz) * 2.0 ** -8 * 1.01 if dtype == torch.bfloat16 else 0)
+    assert (np.abs(leaf.grad.t().double().cpu().numpy() - dz) <= tol + 2.0 ** -126).all()
+
+
+@gpu
+def test_gradient_against_differences_on_the_gpu():
+    """Central differences of the kernel's own loss, over a step of 1/16: they are off by h^2 / 6 of the third derivative, which
+    is at most 6 of the loss's share of a token, and by the loss's rounding over 2 h."""
+    rng = np.random.default_rng(4)
+    T, E, k, h = 6, 8, 2, 2.0 ** -4
+    for score in ("softmax", "sigmoid"):
+        z, idx, starts = make(rng, T, E, k, 1, mask=0)
+        c, n, loss, _ = forward(z.to(DEV), idx, starts, score, 1.0, 1)
+        dz = torch.empty(T, E, device=DEV)
+        lib.balance_loss_backward(z.to(DEV), torch.from_numpy(idx).to(DEV), c, n, torch.ones(1, device=DEV), dz, score=score)
+        share = E * float(c.max()) / (k * float(n) ** 2)
+        for t in range(T):
+            for e in range(E):
+                ends = []
+                for d in (h, -h):
+                    v = z.clone()
+                    v[t, e] += d
+                    ends.append(float(forward(v.to(DEV), idx, starts, score, 1.0, 1)[2]))
+                assert abs((ends[0] - ends[1]) / (2 * h) - float(dz[t, e])) <= h * h * share + float(loss) * (Q(E, 6.0) + STEP) / h
+
+
+@gpu
+def test_step_in_a_graph():
+    """Forward and backward captured, replayed on new logits with eager calls between."""
+    rng = np.random.default_rng(9)
+    T, E, k = 900, 72, 4
+    z, idx, starts = make(rng, T, E, k, 5)
+    zg, ig, st = z.to(DEV), torch.from_numpy(idx).to(DEV), torch.from_numpy(starts).to(DEV)
+    c, n, loss = torch.empty(5, E, dtype=torch.int32, device=DEV), torch.empty(5, dtype=torch.int32, device=DEV), torch.empty(5, device=DEV)
+    work = torch.empty(lib.balance_loss_workspace_bytes(T, 5, E), dtype=torch.uint8, device=DEV)
+    dz, g = torch.empty_like(zg), torch.ones(5, device=DEV)
+
+    def step():
+        lib.balance_loss(zg, ig, c, n, loss, work, starts=st)
+        lib.balance_loss_backward(zg, ig, c, n, g, dz, starts=st)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(4):
+        zg.copy_(z.roll(i, 0))
+        ig.copy_(torch.from_numpy(np.roll(idx, 7 * i, 0)))
+        step()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (c, n, loss, dz)]
+        for t in (c, n, loss, dz):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((c, n, loss, dz), want))
+
+
+@gpu
+def test_identical_calls_give_identical_bits():
+    rng = np.random.default_rng(10)
+    for T, S in ((100, 3), (5000, 1), (5000, 70)):
+        z, idx, starts = make(rng, T, 96, 4, S)
+        first = forward(z.to(DEV), idx, starts, "softmax", 1.0, S)
+        for _ in range(5):
+            again = forward(z.to(DEV), idx, starts, "softmax", 1.0, S)
+            assert all(torch.equal(a, b) for a, b in zip(first[:3], again[:3]))
