@@ -18,7 +18,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void i8_gateup_kerne
   const __amdgpu_buffer_rsrc_t xbuf = buffer_of(a.xq, (int64_t)a.T * a.d);
   const __amdgpu_buffer_rsrc_t xsbuf = buffer_of(a.xs, (int64_t)a.T * 4);
   auto token = [&](int i) { return a.perm[t.row0 + i] / a.k; };
-  typename C::Acc acc[2][C::TN][C::TM];
+  i32x16_t acc[2][C::TN][C::TM];
   i8_product<C>(
       lds, wbuf, wsbuf, a.d, xbuf, xsbuf, [&](int i) { return i < t.rows ? (uint32_t)token(i) * a.d : BUFFER_OUT; },
       [&](int i) { return i < t.rows ? (uint32_t)token(i) * 4 : BUFFER_OUT; }, 0, (a.d + C::BK - 1) / C::BK, acc);
@@ -51,8 +51,8 @@ static hipError_t launch_gateup(const I8Gateup& a, hipStream_t s) {
 //   48 (1024, 128 experts) 451 / 505, 96 (64 experts) 267 / 237, 256 (16 experts, crowded) 134 / 118
 template <typename OUT>
 static hipError_t pick_gateup(const I8Gateup& a, hipStream_t s) {
-  if ((int64_t)a.T * a.k <= 64 * (int64_t)a.E) return launch_gateup<I8Tile<32, 2, 2, 1, 1, 128, 3, 1, 2>, OUT>(a, s);
-  return launch_gateup<I8Tile<32, 2, 4, 1, 1, 128, 2, 1, 2>, OUT>(a, s);
+  if ((int64_t)a.T * a.k <= 64 * (int64_t)a.E) return launch_gateup<I8Tile<2, 2, 1, 1, 128, 3, 1, 2>, OUT>(a, s);
+  return launch_gateup<I8Tile<2, 4, 1, 1, 128, 2, 1, 2>, OUT>(a, s);
 }
 
 hipError_t launch_i8_gateup(const I8Gateup& a, hipStream_t s) {
@@ -71,7 +71,7 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void i8_down_kernel(
   const __amdgpu_buffer_rsrc_t wsbuf[1] = {buffer_of(a.s_down + row0, rows_n * 4)};
   const __amdgpu_buffer_rsrc_t xbuf = buffer_of(a.hq + (int64_t)t.row0 * a.f, (int64_t)t.rows * a.f);
   const __amdgpu_buffer_rsrc_t xsbuf = buffer_of(a.hs + t.row0, t.rows * 4);
-  typename C::Acc acc[1][C::TN][C::TM];
+  i32x16_t acc[1][C::TN][C::TM];
   i8_product<C>(
       lds, wbuf, wsbuf, a.f, xbuf, xsbuf, [&](int i) { return i < t.rows ? (uint32_t)(i * a.f) : BUFFER_OUT; },
       [&](int i) { return (uint32_t)(i * 4); }, 0, (a.f + C::BK - 1) / C::BK, acc);
@@ -155,8 +155,8 @@ __global__ __launch_bounds__(1024) void i8_down_token_kernel(I8Down a) {
 #pragma unroll
       for (int i = 0; i < U; i++) {
         const bool mine = r == jb + G * i;
-        acc = I8Step<16>::mul(w0[i], mine ? x0 : zero, acc);
-        acc = I8Step<16>::mul(w1[i], mine ? x1 : zero, acc);
+        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w0[i], mine ? x0 : zero, acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w1[i], mine ? x1 : zero, acc, 0, 0, 0);
       }
     }
   part[wave][r][quad] = acc;  // (0 for the routes of other groups)
@@ -200,9 +200,9 @@ static hipError_t launch_down(const I8Down& a, hipStream_t s) {
 // then), without its stores 680.
 static hipError_t launch_down_products(const I8Down& a, hipStream_t s) {
   const int64_t n = (int64_t)a.T * a.k, E = a.E;
-  if (n <= 16 * E) return launch_down<I8Tile<32, 4, 2, 1, 1, 128, 2, 1, 1>>(a, s);
-  if (n <= 128 * E) return launch_down<I8Tile<32, 2, 1, 2, 2, 128, 2, 1, 1>>(a, s);
-  return launch_down<I8Tile<32, 2, 2, 2, 2, 128, 2, 1, 1>>(a, s);
+  if (n <= 16 * E) return launch_down<I8Tile<4, 2, 1, 1, 128, 2, 1, 1>>(a, s);
+  if (n <= 128 * E) return launch_down<I8Tile<2, 1, 2, 2, 128, 2, 1, 1>>(a, s);
+  return launch_down<I8Tile<2, 2, 2, 2, 128, 2, 1, 1>>(a, s);
 }
 
 hipError_t launch_i8_down(const I8Down& a, hipStream_t s) {

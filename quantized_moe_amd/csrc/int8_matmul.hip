@@ -69,26 +69,26 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void i8_matmul_tile_
   const __amdgpu_buffer_rsrc_t wsbuf[1] = {buffer_of(a.ws + n0, (int64_t)rows_n * 4)};
   const __amdgpu_buffer_rsrc_t xbuf = buffer_of(a.xq + m0 * a.ldx, (rows_m - 1) * a.ldx + a.K);
   const __amdgpu_buffer_rsrc_t xsbuf = buffer_of(a.xs + m0, (int64_t)rows_m * 4);
-  typename C::Acc acc[1][C::TN][C::TM];
+  i32x16_t acc[1][C::TN][C::TM];
   if (!i8_product<C>(
           lds, wbuf, wsbuf, a.K, xbuf, xsbuf, [&](int i) { return i < rows_m ? (uint32_t)(i * a.ldx) : BUFFER_OUT; },
           [&](int i) { return (uint32_t)(i * 4); }, (int)(blockIdx.y * KB / gridDim.y),
           (int)((blockIdx.y + 1) * KB / gridDim.y), acc))
     return;
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & (C::MF - 1), half = lane / C::MF;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 31, half = lane >> 5;
   const int wn = wave % C::WN, wm = wave / C::WN;
   if (gridDim.y > 1) {
     int* part = a.part + (int64_t)blockIdx.y * a.M * a.N;
 #pragma unroll
     for (int j = 0; j < C::TM; j++) {
-      const int m = m0 + (wm * C::TM + j) * C::MF + r;
+      const int m = m0 + (wm * C::TM + j) * 32 + r;
       if (m >= a.M) continue;
 #pragma unroll
       for (int i = 0; i < C::TN; i++)
 #pragma unroll
-        for (int g = 0; g < C::Step::RUNS; g++) {
-          const int n = n0 + (wn * C::TN + i) * C::MF + 8 * g + 4 * half;
+        for (int g = 0; g < 4; g++) {
+          const int n = n0 + (wn * C::TN + i) * 32 + 8 * g + 4 * half;
           store4(reinterpret_cast<float*>(part) + (int64_t)m * a.N + n, __builtin_bit_cast(f32x4_t, i8_run(acc[0][i][j], g)),
                  a.N - n, a.N % 4 == 0);
         }
@@ -106,14 +106,14 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void i8_matmul_tile_
     const bool vec = a.ldy % 4 == 0 && ((uintptr_t)a.y & (4 * sizeof(OUT) - 1)) == 0;
 #pragma unroll
     for (int j = 0; j < C::TM; j++) {
-      const int mi = (wm * C::TM + j) * C::MF + r;
+      const int mi = (wm * C::TM + j) * 32 + r;
       if (mi >= rows_m) continue;
       const float xs = i8_xscale<C>(lds, mi);
 #pragma unroll
       for (int i = 0; i < C::TN; i++)
 #pragma unroll
-        for (int g = 0; g < C::Step::RUNS; g++) {
-          const int ni = (wn * C::TN + i) * C::MF + 8 * g + 4 * half;
+        for (int g = 0; g < 4; g++) {
+          const int ni = (wn * C::TN + i) * 32 + 8 * g + 4 * half;
           store4(y + mi * a.ldy + ni, i8_values(i8_run(acc[0][i][j], g), xs, i8_wscale<C>(lds, 0, ni)), rows_n - ni, vec);
         }
     }
@@ -184,7 +184,6 @@ static hipError_t launch_rows(const I8Matmul& a, hipStream_t s) {
 //    32 x 32, 8 wave groups share K   64 7.2 (6.5)    128 12.5 (13)
 //    64 x 32, 4                       64 8.4 (8.1)    128 8.7 (8.6)    256 15.8 (17.2)
 //    64 x 64, 2                       128 10.3 (9.8)  256 10.7 (10.7)  512 19.8 (21.4)   704 30.1 (31.6)
-//    64 x 96, 2                       512 24.8 (24.9) 700 26.6 (27.6)  1000 x 2500 26.7 (26.7)
 //    64 x 128                         384 13.8 (13.9) 512 14.8 (14.8)  640 28.2 (26.9)
 //   128 x 128, four stages            640 19.8 (19.7) 768 20.3 (20.7)  1024 22.2 (22.8)  2048 45.1 (45.6)
 //   128 x 128, two, two blocks a CU   1024 26.6 (26.5) 1500 32.8 (32.8) 2048 39.0 (39.0) 2800 59 (62)  5000 93 (104)
@@ -202,11 +201,11 @@ static hipError_t launch_matmul(const I8Matmul& a, hipStream_t s) {
   static constexpr struct {
     int bm, bn, round;
     float begun, full;
-  } TILES[8] = {{32, 32, 256, 5.8f, 0.7f},    {64, 32, 256, 7.6f, 1.0f},    {64, 64, 256, 8.8f, 1.9f},   {64, 96, 256, 8.8f, 5.4f},
-                {64, 128, 256, 11.2f, 3.6f},  {128, 128, 256, 14.5f, 8.3f}, {128, 128, 512, 14.0f, 25.0f}, {256, 256, 256, 30.0f, 31.0f}};
+  } TILES[7] = {{32, 32, 256, 5.8f, 0.7f},    {64, 32, 256, 7.6f, 1.0f},     {64, 64, 256, 8.8f, 1.9f},  {64, 128, 256, 11.2f, 3.6f},
+                {128, 128, 256, 14.5f, 8.3f}, {128, 128, 512, 14.0f, 25.0f}, {256, 256, 256, 30.0f, 31.0f}};
   int best = 0;
   float least = INFINITY;
-  for (int i = 0; i < (parts == 1 ? 8 : 1); i++) {
+  for (int i = 0; i < (parts == 1 ? 7 : 1); i++) {
     const auto& x = TILES[i];
     const int64_t n = tile_count(a.M, a.N, x.bm, x.bn);
     const float cost = x.begun * (float)((n + x.round - 1) / x.round) + x.full * (float)n / (float)x.round;
@@ -216,14 +215,13 @@ static hipError_t launch_matmul(const I8Matmul& a, hipStream_t s) {
     }
   }
   switch (best) {
-    case 0: return launch_tile<I8Tile<32, 1, 1, 1, 1, 64, 3, 8, 1>, OUT>(a, s, parts);
-    case 1: return launch_tile<I8Tile<32, 1, 2, 1, 1, 128, 3, 4, 1>, OUT>(a, s);
-    case 2: return launch_tile<I8Tile<32, 2, 2, 1, 1, 128, 4, 2, 1>, OUT>(a, s);
-    case 3: return launch_tile<I8Tile<32, 3, 2, 1, 1, 128, 3, 2, 1>, OUT>(a, s);
-    case 4: return launch_tile<I8Tile<32, 4, 2, 1, 1, 128, 4, 1, 1>, OUT>(a, s);
-    case 5: return launch_tile<I8Tile<32, 4, 2, 1, 2, 64, 4, 1, 1>, OUT>(a, s);
-    case 6: return launch_tile<I8Tile<32, 4, 2, 1, 2, 128, 2, 1, 1>, OUT>(a, s);
-    default: return launch_tile<I8Tile<32, 4, 2, 2, 4, 128, 2, 1, 1>, OUT>(a, s);
+    case 0: return launch_tile<I8Tile<1, 1, 1, 1, 64, 3, 8, 1>, OUT>(a, s, parts);
+    case 1: return launch_tile<I8Tile<1, 2, 1, 1, 128, 3, 4, 1>, OUT>(a, s);
+    case 2: return launch_tile<I8Tile<2, 2, 1, 1, 128, 4, 2, 1>, OUT>(a, s);
+    case 3: return launch_tile<I8Tile<4, 2, 1, 1, 128, 4, 1, 1>, OUT>(a, s);
+    case 4: return launch_tile<I8Tile<4, 2, 1, 2, 64, 4, 1, 1>, OUT>(a, s);
+    case 5: return launch_tile<I8Tile<4, 2, 1, 2, 128, 2, 1, 1>, OUT>(a, s);
+    default: return launch_tile<I8Tile<4, 2, 2, 4, 128, 2, 1, 1>, OUT>(a, s);
   }
 }
 

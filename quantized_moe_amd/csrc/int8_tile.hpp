@@ -6,11 +6,12 @@
 // integers (|sum| <= 2^14 K <= 2^28), so it is exact whatever the order in which
 // steps, waves and blocks add it, and the scales are met once at the end.
 //
-// Matrix-unit steps: 32x32x32 runs at 4.3 to 4.7 POP/s, 16x16x64 at 2.4 to 2.6 (independent
-// accumulators, no operands read), so the 16-wide one is for tiles of at most 16
-// rows, which are bound by the weights' bytes.  The operands are taken as
-// (weights, activations): the result's columns (lane % MF) are activation rows,
-// and a lane's values are runs of 4 consecutive outputs of one row.
+// Matrix-unit steps: 32x32x32 runs at 4.3 to 4.7 POP/s, 16x16x64 at 2.4 to 2.6
+// (independent accumulators, no operands read), so the 16-wide one is for calls of at
+// most 16 rows, which are bound by the weights' bytes.  The operands are taken as
+// (weights, activations): the result's columns (lane % 32) are activation rows, and a
+// lane's 16 values are 4 runs of 4 consecutive outputs of one row, run g at 8 g + 4
+// (lane / 32).
 #pragma once
 
 #include "blockscale.hpp"
@@ -19,41 +20,19 @@ namespace qmoe {
 
 typedef int i32x16_t __attribute__((ext_vector_type(16)));
 
-template <int MF>
-struct I8Step;  // rows and outputs of a matrix step: MF x MF, K = 16 * 64 / MF
-template <>
-struct I8Step<32> {
-  using Acc = i32x16_t;
-  static constexpr int RUNS = 4;  // runs of 4 outputs in a lane, 8 apart
-  static __device__ __forceinline__ Acc mul(i32x4_t w, i32x4_t x, Acc c) {
-    return __builtin_amdgcn_mfma_i32_32x32x32_i8(w, x, c, 0, 0, 0);
-  }
-};
-template <>
-struct I8Step<16> {
-  using Acc = i32x4_t;
-  static constexpr int RUNS = 1;
-  static __device__ __forceinline__ Acc mul(i32x4_t w, i32x4_t x, Acc c) {
-    return __builtin_amdgcn_mfma_i32_16x16x64_i8(w, x, c, 0, 0, 0);
-  }
-};
-
-// A block's tile: NMAT weight matrices x WN x TN tiles of MF outputs by WM x TM
-// tiles of MF rows, WN x WM waves.  BK inputs at a time go to LDS by
+// A block's tile: NMAT weight matrices x WN x TN tiles of 32 outputs by WM x TM
+// tiles of 32 rows, WN x WM waves.  BK inputs at a time go to LDS by
 // asynchronous copies, ST stages deep; the 16-byte pieces of a row are swizzled
 // so that the 8 rows a read touches at once are in different banks.  KS groups of
 // such waves share the K blocks (group g takes blocks g, g + KS, ...), each with
 // stages of its own, and their sums are added at the end: where tiles are few, a
 // CU has more waves and a shorter chain of steps.
-template <int MF_, int WN_, int WM_, int TN_, int TM_, int BK_, int ST_, int KS_, int NMAT_>
+template <int WN_, int WM_, int TN_, int TM_, int BK_, int ST_, int KS_, int NMAT_>
 struct I8Tile {
-  static constexpr int MF = MF_, WN = WN_, WM = WM_, TN = TN_, TM = TM_, BK = BK_, ST = ST_, KS = KS_, NMAT = NMAT_;
-  using Step = I8Step<MF>;
-  using Acc = typename Step::Acc;
-  static constexpr int ACC = 4 * Step::RUNS;  // values of a tile in a lane
+  static constexpr int WN = WN_, WM = WM_, TN = TN_, TM = TM_, BK = BK_, ST = ST_, KS = KS_, NMAT = NMAT_;
   static constexpr int WAVES = WN * WM, THREADS = 64 * WAVES * KS;
-  static constexpr int BN = WN * TN * MF, BM = WM * TM * MF;
-  static constexpr int KSTEP = 16 * 64 / MF, SUBS = BK / KSTEP;  // matrix steps of a K block
+  static constexpr int BN = WN * TN * 32, BM = WM * TM * 32;
+  static constexpr int SUBS = BK / 32;  // matrix steps of a K block
   static constexpr int PIECES = BK / 16, COPY_ROWS = 64 / PIECES;
   static constexpr int W_BYTES = NMAT * BN * BK, STAGE = W_BYTES + BM * BK;
   static constexpr int SCALES = KS * ST * STAGE;  // [NMAT][BN] of the outputs, [BM] of the rows, behind the stages
@@ -64,7 +43,7 @@ struct I8Tile {
   static constexpr int X_COPIES = (X_UNITS + WAVES - 1) / WAVES;
   static constexpr int COPIES = NMAT * W_COPIES + X_COPIES;
   static constexpr int ROWS = NMAT * TN, FRAGS = ROWS + TM, MULS = ROWS * TM;
-  static constexpr int REGS = ACC * MULS;  // accumulators of a lane
+  static constexpr int REGS = 16 * MULS;  // accumulators of a lane
   // blocks that fit a CU's LDS, and the registers to match
   static constexpr int BLOCKS = 160 * 1024 / LDS;
   static constexpr int WAVES_PER_SIMD_LDS = BLOCKS * WAVES * KS / 4 > 0 ? BLOCKS * WAVES * KS / 4 : 1;
@@ -94,7 +73,7 @@ template <class C, class XRow, class SRow>
 __device__ __forceinline__ bool i8_product(uint8_t* lds, const __amdgpu_buffer_rsrc_t (&wbuf)[C::NMAT],
                                            const __amdgpu_buffer_rsrc_t (&wsbuf)[C::NMAT], int K,
                                            __amdgpu_buffer_rsrc_t xbuf, __amdgpu_buffer_rsrc_t xsbuf, XRow xrow, SRow srow,
-                                           int kb0, int kb1, typename C::Acc (&acc)[C::NMAT][C::TN][C::TM]) {
+                                           int kb0, int kb1, i32x16_t (&acc)[C::NMAT][C::TN][C::TM]) {
   constexpr int WAVES = C::WAVES, TN = C::TN, TM = C::TM, KS = C::KS, ROWS = C::ROWS, BK = C::BK;
   const int lane = threadIdx.x & 63, block_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = block_wave / WAVES, wave = block_wave % WAVES;
@@ -153,12 +132,12 @@ __device__ __forceinline__ bool i8_product(uint8_t* lds, const __amdgpu_buffer_r
   }
 
   const int wn = wave % C::WN, wm = wave / C::WN;
-  const int r = lane & (C::MF - 1), half = lane / C::MF;
-  typename C::Acc* flat = &acc[0][0][0];
+  const int r = lane & 31, half = lane >> 5;
+  i32x16_t* flat = &acc[0][0][0];
 #pragma unroll
   for (int i = 0; i < C::MULS; i++)
 #pragma unroll
-    for (int q = 0; q < C::ACC; q++) flat[i][q] = 0;
+    for (int q = 0; q < 16; q++) flat[i][q] = 0;
 #pragma unroll
   for (int b = 0; b < C::ST; b++) {
     const int kb = kb0 + group + b * KS;
@@ -169,11 +148,11 @@ __device__ __forceinline__ bool i8_product(uint8_t* lds, const __amdgpu_buffer_r
   // Operands of step `sub` of a stage: ROWS of weights, then TM of activations.
   int place[C::SUBS];
 #pragma unroll
-  for (int s = 0; s < C::SUBS; s++) place[s] = i8_place<BK>(r, s * (C::KSTEP / 16) + half) * 16;
-  const int wrow = (wn * TN * C::MF + r) * BK, xrow0 = C::W_BYTES + (wm * TM * C::MF + r) * BK;
+  for (int s = 0; s < C::SUBS; s++) place[s] = i8_place<BK>(r, 2 * s + half) * 16;
+  const int wrow = (wn * TN * 32 + r) * BK, xrow0 = C::W_BYTES + (wm * TM * 32 + r) * BK;
   i32x4_t f[2][C::FRAGS];
   auto read = [&](const uint8_t* st, int sub, int i, int to) {
-    const int at = i < ROWS ? wrow + (i / TN * C::BN + i % TN * C::MF) * BK : xrow0 + (i - ROWS) * C::MF * BK;
+    const int at = i < ROWS ? wrow + (i / TN * C::BN + i % TN * 32) * BK : xrow0 + (i - ROWS) * 32 * BK;
     f[to][i] = *reinterpret_cast<const i32x4_t*>(st + at + place[sub]);
   };
   lds_landed<(C::ST - 1) * C::COPIES>();
@@ -199,7 +178,7 @@ __device__ __forceinline__ bool i8_product(uint8_t* lds, const __amdgpu_buffer_r
 #pragma unroll
       for (int m = 0; m < C::MULS; m++) {
         const int i = m / TM, j = m % TM;
-        flat[m] = C::Step::mul(f[sub & 1][i], f[sub & 1][ROWS + j], flat[m]);
+        flat[m] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f[sub & 1][i], f[sub & 1][ROWS + j], flat[m], 0, 0, 0);
 #pragma unroll
         for (int q = m * READS; q < (m + 1) * READS && q < C::FRAGS; q++)
           read(from, last ? 0 : sub + 1, q, (sub + 1) & 1);
@@ -218,7 +197,7 @@ __device__ __forceinline__ bool i8_product(uint8_t* lds, const __amdgpu_buffer_r
     if (group > 0) {
 #pragma unroll
       for (int i = 0; i < C::REGS; i++)
-        sums[((group - 1) * C::REGS + i) * WAVES * 64 + gt] = flat[i / C::ACC][i % C::ACC];
+        sums[((group - 1) * C::REGS + i) * WAVES * 64 + gt] = flat[i / 16][i % 16];
     }
     __syncthreads();
     if (group > 0) return false;
@@ -226,12 +205,12 @@ __device__ __forceinline__ bool i8_product(uint8_t* lds, const __amdgpu_buffer_r
     for (int g = 1; g < KS; g++)
 #pragma unroll
       for (int i = 0; i < C::REGS; i++)
-        flat[i / C::ACC][i % C::ACC] += sums[((g - 1) * C::REGS + i) * WAVES * 64 + gt];
+        flat[i / 16][i % 16] += sums[((g - 1) * C::REGS + i) * WAVES * 64 + gt];
   }
   return true;
 }
 
-// The staged scales: of the wave's output 4 (lane / MF) + 8 g + q of tile i, and of its row of tile j.
+// The staged scales: of 4 of the tile's outputs from n_in_tile on, and of its row m_in_tile.
 template <class C>
 __device__ __forceinline__ f32x4_t i8_wscale(const uint8_t* lds, int mat, int n_in_tile) {
   return *reinterpret_cast<const f32x4_t*>(lds + C::SCALES + (mat * ((C::BN + 63) / 64 * 64) + n_in_tile) * 4);
@@ -248,8 +227,7 @@ __device__ __forceinline__ f32x4_t i8_values(i32x4_t sum, float xs, f32x4_t ws) 
   for (int q = 0; q < 4; q++) y[q] = ((float)sum[q] * xs) * ws[q];
   return y;
 }
-template <class Acc>
-__device__ __forceinline__ i32x4_t i8_run(const Acc& a, int g) {
+__device__ __forceinline__ i32x4_t i8_run(const i32x16_t& a, int g) {
   return i32x4_t{a[4 * g], a[4 * g + 1], a[4 * g + 2], a[4 * g + 3]};
 }
 
@@ -261,7 +239,7 @@ __device__ __forceinline__ i32x4_t i8_run(const Acc& a, int g) {
 // tile has.
 template <class C, typename OUT, class Value>
 __device__ __forceinline__ void i8_store(uint8_t* lds, OUT* out, int64_t ld, int rows, int cols, int align, Value&& value) {
-  static_assert(C::MF == 32 && C::KS == 1, "every wave stores");
+  static_assert(C::KS == 1, "every wave stores");
   constexpr int W = C::TN * 32, PIECE = 16 / sizeof(OUT), STRIDE = W * sizeof(OUT) + 16;
   constexpr int LANES = W / PIECE, AT_ONCE = 64 / LANES;  // lanes of a row, rows of a store
   static_assert(C::WAVES * 32 * STRIDE <= C::SCALES, "a part for every wave");
