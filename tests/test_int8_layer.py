@@ -145,3 +145,16 @@ def test_layer_refusals():
         layer.balance(4, starts=torch.zeros(3, dtype=torch.int32))
     with pytest.raises(ValueError, match="the router 8"):
         int8.Int8Layer(torch.zeros(8, 256), lib.gate(4, 2), (torch.zeros(8, 128, 256), None), None, None)
+
+
+@gpu
+def test_example_runs_and_gives_the_routers_gradient():
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "int8_layer.py")
+    spec = importlib.util.spec_from_file_location("int8_layer_example", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    grad = example.main(["--experts", "16", "--width", "256", "--hidden", "128", "--tokens", "1,40"])
+    assert grad.shape == (16, 256) and torch.isfinite(grad).all() and float(grad.norm()) > 0
