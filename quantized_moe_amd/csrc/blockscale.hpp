@@ -118,6 +118,12 @@ __device__ __forceinline__ void lds_copy16(__amdgpu_buffer_rsrc_t r, uint32_t ld
                ::"s"(lds), "v"(off), "s"(r), "s"(soff)
                : "memory", "m0");
 }
+// The same past the caches: for bytes that no other block reads.
+__device__ __forceinline__ void lds_copy16_once(__amdgpu_buffer_rsrc_t r, uint32_t lds, uint32_t off, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
+               ::"s"(lds), "v"(off), "s"(r), "s"(soff)
+               : "memory", "m0");
+}
 __device__ __forceinline__ void lds_copy4(__amdgpu_buffer_rsrc_t r, uint32_t lds, uint32_t off, uint32_t soff) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
                ::"s"(lds), "v"(off), "s"(r), "s"(soff)
@@ -208,11 +214,12 @@ struct TileScan {
     before = upto - n;
   }
   __device__ __forceinline__ int tiles() const { return __builtin_amdgcn_readlane(upto, 63); }
-  // Tile `tile`'s expert, first row and row count.  false: there are fewer.
-  __device__ __forceinline__ bool find(int tile, int* e_out, int* row0, int* rows) const {
+  // Tile `tile`'s expert, first row and row count, and whether it is that expert's
+  // only one.  false: there are fewer.
+  __device__ __forceinline__ bool find(int tile, int* e_out, int* row0, int* rows, bool* alone) const {
     const uint64_t has = __ballot(tile < upto);
     if (has == 0) return false;
-    int left = tile - before, e = e0, first = 0, count = 0;
+    int left = tile - before, e = e0, first = 0, count = 0, of = 0;
 #pragma unroll
     for (int i = 0; i < MOST; i++)
       if (i < C) {
@@ -221,6 +228,7 @@ struct TileScan {
           e = e0 + i;
           first = off[i] + left * BM;
           count = min(BM, off[i + 1] - first);
+          of = t;
         }
         left -= t;
       }
@@ -228,6 +236,7 @@ struct TileScan {
     *e_out = __builtin_amdgcn_readlane(e, src);
     *row0 = __builtin_amdgcn_readlane(first, src);
     *rows = __builtin_amdgcn_readlane(count, src);
+    *alone = __builtin_amdgcn_readlane(of, src) == 1;
     return true;
   }
 };
@@ -240,6 +249,7 @@ inline int64_t max_tiles(int64_t n, int E, int bm) {
 
 struct ExpertTile {
   int e, row0, rows, nt;
+  bool alone;  // the only M tile of its expert
 };
 
 // Which M tile and which outputs a block takes.
@@ -285,7 +295,7 @@ __device__ __forceinline__ bool expert_tile(const int32_t* offsets, int E, const
     t->nt = id / p.tiles;
     pick = id - t->nt * p.tiles;
   }
-  return scan.find(pick, &t->e, &t->row0, &t->rows);
+  return scan.find(pick, &t->e, &t->row0, &t->rows, &t->alone);
 }
 
 }  // namespace qmoe

@@ -4,9 +4,19 @@
 
 namespace qmoe {
 
+// Weights that no other block reads (those of an expert with one M tile) go past the
+// caches where a call's weights are more than these hold until the next call: us with
+// and without, 1024 tokens' gate/up 966 and 1090 (6.7 TB/s), 8 tokens' 118 and 132,
+// their down products 566 and 606, 65 and 73; but 1 token's gate/up (101 MB) 21.1 and
+// 18.9, 4 tokens' over 64 experts x 2048 x 1408 (138 MB) 30.0 and 25.4, their down
+// products 18.1 and 18.5, and with few M tiles of many rows each there is no such expert.
+static bool read_once(int64_t n, int E, int64_t expert_bytes) {
+  return (n < E ? n : E) * expert_bytes > (int64_t(160) << 20);
+}
+
 // A block owns BM bucket rows of one expert and BN hidden columns, gate and up.
 template <class C, typename OUT>
-__global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void i8_gateup_kernel(I8Gateup a, TilePlan plan) {
+__global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void i8_gateup_kernel(I8Gateup a, TilePlan plan, bool once) {
   static_assert(C::NMAT == 2 && C::KS == 1, "gate and up");
   extern __shared__ __align__(1024) uint8_t lds[];
   ExpertTile t;
@@ -19,10 +29,13 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void i8_gateup_kerne
   const __amdgpu_buffer_rsrc_t xsbuf = buffer_of(a.xs, (int64_t)a.T * 4);
   auto token = [&](int i) { return a.perm[t.row0 + i] / a.k; };
   i32x16_t acc[2][C::TN][C::TM];
-  i8_product<C>(
-      lds, wbuf, wsbuf, a.d, xbuf, xsbuf, [&](int i) { return i < t.rows ? (uint32_t)token(i) * a.d : BUFFER_OUT; },
-      [&](int i) { return i < t.rows ? (uint32_t)token(i) * 4 : BUFFER_OUT; }, 0, (a.d + C::BK - 1) / C::BK, acc);
-
+  auto xrow = [&](int i) { return i < t.rows ? (uint32_t)token(i) * a.d : BUFFER_OUT; };
+  auto srow = [&](int i) { return i < t.rows ? (uint32_t)token(i) * 4 : BUFFER_OUT; };
+  const int KB = (a.d + C::BK - 1) / C::BK;
+  if (once && t.alone)
+    i8_product<C, true>(lds, wbuf, wsbuf, a.d, xbuf, xsbuf, xrow, srow, 0, KB, acc);
+  else
+    i8_product<C>(lds, wbuf, wsbuf, a.d, xbuf, xsbuf, xrow, srow, 0, KB, acc);
   i8_store<C>(lds, static_cast<OUT*>(a.h) + (int64_t)t.row0 * a.f + n0, a.f, t.rows, rows_n, 16,  // f is a multiple of 16
               [&](int i, int j, int g, int n, float xs) {
                 const f32x4_t gate = i8_values(i8_run(acc[0][i][j], g), xs, i8_wscale<C>(lds, 0, n));
@@ -36,12 +49,13 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void i8_gateup_kerne
 
 template <class C, typename OUT>
 static hipError_t launch_gateup(const I8Gateup& a, hipStream_t s) {
-  const TilePlan plan = tile_plan<C>((int64_t)a.T * a.k, a.E, a.f);
+  const int64_t n = (int64_t)a.T * a.k;
+  const TilePlan plan = tile_plan<C>(n, a.E, a.f);
   auto* k = i8_gateup_kernel<C, OUT>;
   int per_cu, cus;
   hipError_t e = launch_shape((const void*)k, C::THREADS, C::LDS, C::LDS, &per_cu, &cus);
   if (e != hipSuccess) return e;
-  QMOE_LAUNCH(k, dim3(plan.blocks), dim3(C::THREADS), C::LDS, s, a, plan);
+  QMOE_LAUNCH(k, dim3(plan.blocks), dim3(C::THREADS), C::LDS, s, a, plan, read_once(n, a.E, 2 * (int64_t)a.f * a.d));
   return hipGetLastError();
 }
 
@@ -61,7 +75,7 @@ hipError_t launch_i8_gateup(const I8Gateup& a, hipStream_t s) {
 
 // ye[r][n] = (D_e h_r)[n] for the bucket rows.
 template <class C>
-__global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void i8_down_kernel(I8Down a, TilePlan plan) {
+__global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void i8_down_kernel(I8Down a, TilePlan plan, bool once) {
   extern __shared__ __align__(1024) uint8_t lds[];
   ExpertTile t;
   if (!expert_tile<C::BM>(a.offsets, a.E, plan, &t)) return;
@@ -72,9 +86,13 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void i8_down_kernel(
   const __amdgpu_buffer_rsrc_t xbuf = buffer_of(a.hq + (int64_t)t.row0 * a.f, (int64_t)t.rows * a.f);
   const __amdgpu_buffer_rsrc_t xsbuf = buffer_of(a.hs + t.row0, t.rows * 4);
   i32x16_t acc[1][C::TN][C::TM];
-  i8_product<C>(
-      lds, wbuf, wsbuf, a.f, xbuf, xsbuf, [&](int i) { return i < t.rows ? (uint32_t)(i * a.f) : BUFFER_OUT; },
-      [&](int i) { return (uint32_t)(i * 4); }, 0, (a.f + C::BK - 1) / C::BK, acc);
+  auto xrow = [&](int i) { return i < t.rows ? (uint32_t)(i * a.f) : BUFFER_OUT; };
+  auto srow = [&](int i) { return (uint32_t)(i * 4); };
+  const int KB = (a.f + C::BK - 1) / C::BK;
+  if (once && t.alone)
+    i8_product<C, true>(lds, wbuf, wsbuf, a.f, xbuf, xsbuf, xrow, srow, 0, KB, acc);
+  else
+    i8_product<C>(lds, wbuf, wsbuf, a.f, xbuf, xsbuf, xrow, srow, 0, KB, acc);
   i8_store<C>(lds, a.ye + (int64_t)t.row0 * a.d + n0, a.d, t.rows, rows_n, 16, [&](int i, int j, int g, int n, float xs) {
     return i8_values(i8_run(acc[0][i][j], g), xs, i8_wscale<C>(lds, 0, n));
   });
@@ -182,12 +200,13 @@ size_t i8_down_ws(int T, int k, int d) { return T <= TOKEN_MAX_T ? 0 : (size_t)T
 
 template <class C>
 static hipError_t launch_down(const I8Down& a, hipStream_t s) {
-  const TilePlan plan = tile_plan<C>((int64_t)a.T * a.k, a.E, a.d);
+  const int64_t n = (int64_t)a.T * a.k;
+  const TilePlan plan = tile_plan<C>(n, a.E, a.d);
   auto* k = i8_down_kernel<C>;
   int per_cu, cus;
   hipError_t e = launch_shape((const void*)k, C::THREADS, C::LDS, C::LDS, &per_cu, &cus);
   if (e != hipSuccess) return e;
-  QMOE_LAUNCH(k, dim3(plan.blocks), dim3(C::THREADS), C::LDS, s, a, plan);
+  QMOE_LAUNCH(k, dim3(plan.blocks), dim3(C::THREADS), C::LDS, s, a, plan, read_once(n, a.E, (int64_t)a.f * a.d));
   return hipGetLastError();
 }
 

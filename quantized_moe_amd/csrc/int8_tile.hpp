@@ -67,9 +67,10 @@ __device__ __forceinline__ int i8_place(int r, int p) {
 // acc[mat][i][j] = the wave's tiles of exact sums.  wbuf: the tile's rows of each
 // matrix, K bytes apart; xbuf with xrow(i): the byte offset of row i's codes
 // (BUFFER_OUT: no such row); K blocks (of BK) kb0 <= kb < kb1.  wsbuf, xsbuf with
-// srow(i) (row i's): the scales, left in LDS behind the stages.  With KS > 1 the
+// srow(i) (row i's): the scales, left in LDS behind the stages.  ONCE: no other block
+// reads these weights, which then go past the caches.  With KS > 1 the
 // sums are group 0's; false for the other groups' threads.
-template <class C, class XRow, class SRow>
+template <class C, bool ONCE = false, class XRow, class SRow>
 __device__ __forceinline__ bool i8_product(uint8_t* lds, const __amdgpu_buffer_rsrc_t (&wbuf)[C::NMAT],
                                            const __amdgpu_buffer_rsrc_t (&wsbuf)[C::NMAT], int K,
                                            __amdgpu_buffer_rsrc_t xbuf, __amdgpu_buffer_rsrc_t xsbuf, XRow xrow, SRow srow,
@@ -96,7 +97,11 @@ __device__ __forceinline__ bool i8_product(uint8_t* lds, const __amdgpu_buffer_r
     const uint32_t at = base + stage * C::STAGE;
     if (i < C::NMAT * C::W_COPIES) {
       const int mat = i / C::W_COPIES, c = i % C::W_COPIES;
-      lds_copy16(wbuf[mat], at + mat * C::BN * BK + (wave + c * WAVES) % C::W_UNITS * 1024, woff[c], kb * BK);
+      const uint32_t to = at + mat * C::BN * BK + (wave + c * WAVES) % C::W_UNITS * 1024;
+      if (ONCE)
+        lds_copy16_once(wbuf[mat], to, woff[c], kb * BK);
+      else
+        lds_copy16(wbuf[mat], to, woff[c], kb * BK);
     } else {
       const int c = i - C::NMAT * C::W_COPIES;
       lds_copy16(xbuf, at + C::W_BYTES + (wave + c * WAVES) % C::X_UNITS * 1024, xoff[c], kb * BK);
