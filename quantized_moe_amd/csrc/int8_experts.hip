@@ -104,7 +104,9 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void i8_down_kernel(
 // requested at a time.  Column j of the matrix steps' activations is route j's
 // row; the product with route j's weights takes that column and zeros, so one
 // accumulator serves every route.  The waves' sums are added, then the routes
-// weighted in their order.
+// weighted in their order.  Bound by the weights, after two loads in a row (positions
+// and offsets, then weights): 6 of 384 experts x 2048 x 4096, 1 token 11.2 us (4.5 TB/s
+// over the whole call; weights past the caches 12.4), 2 tokens 20.9.
 template <int U>
 __global__ __launch_bounds__(1024) void i8_down_token_kernel(I8Down a) {
   constexpr int WAVES = 16;

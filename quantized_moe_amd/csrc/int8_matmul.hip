@@ -98,7 +98,8 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void i8_matmul_tile_
   OUT* y = static_cast<OUT*>(a.y) + m0 * a.ldy + n0;
   if constexpr (C::KS == 1) {
     const uint32_t bits = (uint32_t)(a.ldy * sizeof(OUT)) | (uint32_t)(uintptr_t)a.y;
-    i8_store<C>(lds, y, a.ldy, rows_m, rows_n, bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 2, [&](int i, int j, int g, int n, float xs) {
+    const int align = bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 2;
+    i8_store<C>(lds, y, a.ldy, rows_m, rows_n, align, [&](int i, int j, int g, int n, float xs) {
       return i8_values(i8_run(acc[0][i][j], g), xs, i8_wscale<C>(lds, 0, n));
     });
   } else {

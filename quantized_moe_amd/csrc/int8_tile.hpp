@@ -23,7 +23,7 @@ typedef int i32x16_t __attribute__((ext_vector_type(16)));
 // A block's tile: NMAT weight matrices x WN x TN tiles of 32 outputs by WM x TM
 // tiles of 32 rows, WN x WM waves.  BK inputs at a time go to LDS by
 // asynchronous copies, ST stages deep; the 16-byte pieces of a row are swizzled
-// so that the 8 rows a read touches at once are in different banks.  KS groups of
+// so that what a read touches at once is in different banks.  KS groups of
 // such waves share the K blocks (group g takes blocks g, g + KS, ...), each with
 // stages of its own, and their sums are added at the end: where tiles are few, a
 // CU has more waves and a shorter chain of steps.
@@ -68,8 +68,8 @@ __device__ __forceinline__ int i8_place(int r, int p) {
 // matrix, K bytes apart; xbuf with xrow(i): the byte offset of row i's codes
 // (BUFFER_OUT: no such row); K blocks (of BK) kb0 <= kb < kb1.  wsbuf, xsbuf with
 // srow(i) (row i's): the scales, left in LDS behind the stages.  ONCE: no other block
-// reads these weights, which then go past the caches.  With KS > 1 the
-// sums are group 0's; false for the other groups' threads.
+// reads these weights, which then go past the caches.  With KS > 1 the sums are group
+// 0's; false for the other groups' threads.
 template <class C, bool ONCE = false, class XRow, class SRow>
 __device__ __forceinline__ bool i8_product(uint8_t* lds, const __amdgpu_buffer_rsrc_t (&wbuf)[C::NMAT],
                                            const __amdgpu_buffer_rsrc_t (&wsbuf)[C::NMAT], int K,
