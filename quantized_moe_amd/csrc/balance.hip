@@ -410,10 +410,10 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(Balance a, int ru
       },
       [&](int t, TokenRow<PER>& row, bool routed) {
         const bool live = seq.s >= 0 && routed;
-        const float q = row.share(), scale = row.sum > 0.0f ? coef / row.sum : 0.0f;
+        const float q = row.share(), inv = row.sum > 0.0f ? 1.0f / row.sum : 0.0f;  // (sums are at least e^-80)
 #pragma unroll
         for (int i = 0; i < PER; i++) {
-          float g = row.a[i] * scale * (seq.c[i] - q);
+          float g = row.a[i] * inv * (coef * (seq.c[i] - q));
           if (!SOFTMAX) g *= row.u[i];
           g = live && row.a[i] > 0.0f ? g : 0.0f;
           if constexpr (ZDT == X_BF16) {

@@ -166,6 +166,20 @@ def test_extreme_logits(score):
 
 
 @gpu
+def test_large_gradients_of_far_logits():
+    """Every sigmoid at its smallest, e^-80: the probabilities are those of equal logits, whatever the sequence's gradient."""
+    z = torch.full((1, 3), -90.0, device=DEV)
+    idx = np.array([[0, 1]], np.int32)
+    c, n, _, _ = forward(z, idx, np.array([0, 1], np.int32), "sigmoid", 1.0, 1)
+    for g in (1e-20, 1.0, 1e30):
+        got = torch.empty(1, 3, device=DEV)
+        lib.balance_loss_backward(z, torch.from_numpy(idx).to(DEV), c, n, torch.full((1,), g, device=DEV), got, score="sigmoid")
+        _, _, _, dz, unit = plain(z.cpu().double().numpy(), idx, [0, 1], "sigmoid", 1.0, np.array([g]))
+        assert np.abs(dz).max() > 0.1 * g
+        assert (np.abs(got.double().cpu().numpy() - dz) <= unit * 2 * Q(3, 80.0)).all()
+
+
+@gpu
 def test_even_load_gives_alpha():
     """Every expert asked for alike: the loss is alpha and no logit is pushed."""
     T, E = 512, 64
