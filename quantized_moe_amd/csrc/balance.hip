@@ -201,20 +201,15 @@ constexpr int COUNT_HELD = 12288;                // counts that a block holds in
 constexpr int COUNT_HELD_S = COUNT_HELD / 8;     // ... of so many sequences at most (with fewer than 8 experts too)
 __device__ __host__ __forceinline__ int held_sequences(int E) { return COUNT_HELD / (E < 8 ? 8 : E); }
 
-// n routes of a token, counted for sequence s: in LDS for the `held` sequences from
-// s0 on, in memory for later ones.  Whole numbers: the order of the atomics changes
-// nothing.  true: one of them is a route.
-template <bool ALL_HELD>
-__device__ __forceinline__ bool count_routes(const int (&e)[8], int n, int E, int s, int s0, int held, int* hist, int32_t* counts) {
+// n routes of a token added to its sequence's counts in LDS.  Whole numbers: the order
+// of the atomics changes nothing.  true: one of them is a route.
+__device__ __forceinline__ bool count_routes(const int (&e)[8], int n, int E, int* hist) {
   bool any = false;
 #pragma unroll
   for (int j = 0; j < 8; j++) {
     if (j >= n || (uint32_t)e[j] >= (uint32_t)E) continue;
     any = true;
-    if (ALL_HELD || s - s0 < held)
-      atomicAdd(&hist[(s - s0) * E + e[j]], 1);
-    else
-      atomicAdd(&counts[(int64_t)s * E + e[j]], 1);
+    atomicAdd(&hist[e[j]], 1);
   }
   return any;
 }
@@ -224,39 +219,68 @@ __device__ __forceinline__ void load_routes(const Balance& a, int t, int j, int 
   for (int i = 0; i < 8; i++) e[i] = a.idx[(int64_t)t * a.k + min(j + i, a.k - 1)];
 }
 
-// 1024 tokens a block, a thread each; the counts are added to cleared memory.
-__global__ __launch_bounds__(1024) void balance_count_kernel(Balance a) {
+// Four threads a token (routes r, r + 4, ..: a thread's LDS atomics follow each other),
+// 256 tokens at a time, all routes requested first.  WHOLE: one block takes all tokens
+// and sequences and writes the counts; else they are added to cleared memory, from so
+// many tokens a block that 64 blocks at most add to the same counts.
+constexpr int COUNT_TOKENS = 1024;  // of a block at most
+template <bool WHOLE>
+__global__ __launch_bounds__(1024) void balance_count_kernel(Balance a, int per) {
+  constexpr int N = COUNT_TOKENS / 256;
   __shared__ int hist[COUNT_HELD], live[COUNT_HELD_S];
-  const int t0 = blockIdx.x * 1024, t = min(t0 + (int)threadIdx.x, a.T - 1);
-  int e[8], end;
-  load_routes(a, t, 0, e);
+  const int r = threadIdx.x & 3, t0 = blockIdx.x * per, t1 = min(t0 + per, a.T), first = t0 + (threadIdx.x >> 2);
+  int e[N][4], end;
+#pragma unroll
+  for (int i = 0; i < N; i++)
+    if (t0 + i * 256 < t1)
+#pragma unroll
+      for (int j = 0; j < 4; j++)
+        e[i][j] = r + 4 * j < a.k ? a.idx[(int64_t)min(first + i * 256, a.T - 1) * a.k + r + 4 * j] : -1;
   const Starts starts(a.starts, a.S, a.T);
-  int s0 = max(starts.find(t0, &end), 0), s1 = a.S - 1;
-  if (a.S >= 64) {  // (fewer are taken whole)
+  int s0 = WHOLE ? 0 : max(starts.find(t0, &end), 0), s1 = a.S - 1;
+  if (!WHOLE && a.S >= 64) {  // (fewer are taken whole)
     s0 = max(sequence_of(a.starts, a.S, t0), 0);
-    s1 = min(sequence_of(a.starts, a.S, min(t0 + 1023, a.T - 1)), a.S - 1);
+    s1 = min(sequence_of(a.starts, a.S, t1 - 1), a.S - 1);
   }
-  const int held = min(held_sequences(a.E), s1 - s0 + 1), n = held * a.E;  // (<= 0: no token of any sequence)
+  const int held = WHOLE ? a.S : min(held_sequences(a.E), s1 - s0 + 1), n = held * a.E;  // (<= 0: no token of any sequence)
   for (int i = threadIdx.x; i < n; i += 1024) hist[i] = 0;
   for (int i = threadIdx.x; i < held; i += 1024) live[i] = 0;
-  const int s = starts.find_lane(t);
   __syncthreads();
-  if (t0 + (int)threadIdx.x < a.T && s >= s0 && s <= s1) {
-    bool any = count_routes<false>(e, a.k, a.E, s, s0, held, hist, a.counts);
-    if (a.k > 8) {
-      load_routes(a, t, 8, e);
-      any |= count_routes<false>(e, a.k - 8, a.E, s, s0, held, hist, a.counts);
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    if (t0 + i * 256 >= t1) break;
+    const int t = first + i * 256, s = starts.find_lane(t);
+    const bool in = t < t1 && s >= s0 && s <= s1, here = WHOLE || s - s0 < held;
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      if (!in || (uint32_t)e[i][j] >= (uint32_t)a.E) continue;
+      any = true;
+      if (here)
+        atomicAdd(&hist[(s - s0) * a.E + e[i][j]], 1);
+      else
+        atomicAdd(&a.counts[(int64_t)s * a.E + e[i][j]], 1);
     }
-    if (any && s - s0 < held)
+    const bool routed = __ballot(any) >> (threadIdx.x & 60) & 15;  // one of the token's four threads
+    if (r != 0 || !routed) continue;
+    if (here)
       atomicAdd(&live[s - s0], 1);
-    else if (any)
+    else
       atomicAdd(&a.tokens[s], 1);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += 1024)
-    if (hist[i]) atomicAdd(&a.counts[(int64_t)s0 * a.E + i], hist[i]);
-  for (int i = threadIdx.x; i < held; i += 1024)
-    if (live[i]) atomicAdd(&a.tokens[s0 + i], live[i]);
+  for (int i = threadIdx.x; i < n; i += 1024) {
+    if (WHOLE)
+      a.counts[i] = hist[i];
+    else if (hist[i])
+      atomicAdd(&a.counts[(int64_t)s0 * a.E + i], hist[i]);
+  }
+  for (int i = threadIdx.x; i < held; i += 1024) {
+    if (WHOLE)
+      a.tokens[i] = live[i];
+    else if (live[i])
+      atomicAdd(&a.tokens[s0 + i], live[i]);
+  }
 }
 
 __device__ __forceinline__ float loss_of(const Balance& a, double sum, int tokens) {
@@ -449,10 +473,10 @@ __global__ __launch_bounds__(1024) void balance_small_kernel(Balance a) {
   if (my < a.T) {
     bool any = my_s >= 0 && my_s < a.S;
     if (any) {
-      any = count_routes<true>(e, a.k, a.E, my_s, 0, a.S, hist, nullptr);
+      any = count_routes(e, a.k, a.E, hist + my_s * a.E);
       if (a.k > 8) {
         load_routes(a, my, 8, e);
-        any |= count_routes<true>(e, a.k - 8, a.E, my_s, 0, a.S, hist, nullptr);
+        any |= count_routes(e, a.k - 8, a.E, hist + my_s * a.E);
       }
       if (any) atomicAdd(&live[my_s], 1);
     }
@@ -548,19 +572,27 @@ static hipError_t launch(const char* name, const Balance& a, hipStream_t s) {
 
 hipError_t launch_balance_loss(const Balance& a, hipStream_t s) {
   if (is_small(a.T, a.S, a.E)) return launch<SMALL>("balance_small", a, s);
-  const int64_t n = (int64_t)a.S * a.E;
-  int pid = prof_begin("balance_clear", s);
-  QMOE_LAUNCH(balance_clear_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a.counts, n, a.tokens, a.S);
-  prof_end(pid, s);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if (a.T > 0) {
+  hipError_t e;
+  int pid;
+  if (a.T > 0 && a.T <= COUNT_TOKENS && a.S <= held_sequences(a.E)) {
     pid = prof_begin("balance_count", s);
-    QMOE_LAUNCH(balance_count_kernel, dim3((unsigned)((a.T + 1023) / 1024)), dim3(1024), 0, s, a);
+    QMOE_LAUNCH(balance_count_kernel<true>, dim3(1), dim3(1024), 0, s, a, COUNT_TOKENS);
     prof_end(pid, s);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    if ((e = launch<FORWARD>("balance_forward", a, s)) != hipSuccess) return e;
+  } else {
+    const int64_t n = (int64_t)a.S * a.E;
+    pid = prof_begin("balance_clear", s);
+    QMOE_LAUNCH(balance_clear_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a.counts, n, a.tokens, a.S);
+    prof_end(pid, s);
+    if (a.T > 0) {
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      const int per = min(COUNT_TOKENS, (a.T + 64 * 256 - 1) / (64 * 256) * 256);
+      pid = prof_begin("balance_count", s);
+      QMOE_LAUNCH(balance_count_kernel<false>, dim3((unsigned)((a.T + per - 1) / per)), dim3(1024), 0, s, a, per);
+      prof_end(pid, s);
+    }
   }
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (a.T > 0 && (e = launch<FORWARD>("balance_forward", a, s)) != hipSuccess) return e;
   pid = prof_begin("balance_sum", s);
   QMOE_LAUNCH(balance_sum_kernel, dim3((unsigned)((a.S + 3) / 4)), dim3(256), 0, s, a, run_of(a.T));
   prof_end(pid, s);
