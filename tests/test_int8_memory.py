@@ -265,9 +265,10 @@ def test_every_launch_is_timed_under_its_name():
             "balance_loss": ["balance_small"], "balance_loss_backward": ["balance_backward"]}
     for n, (call, args) in calls.items():
         assert names(call, **args) == want[n]
-    z, idx = torch.zeros(500, 8, device=DEV), torch.zeros(500, 2, dtype=torch.int32, device=DEV)
-    big = dict(calls["balance_loss"][1], z=z, idx=idx, workspace=torch.empty(4000, dtype=torch.uint8, device=DEV))
-    assert names(lib.balance_loss, **big) == ["balance_clear", "balance_count", "balance_forward", "balance_sum"]
+    for T, more in ((500, []), (1500, ["balance_clear"])):
+        big = dict(calls["balance_loss"][1], z=torch.zeros(T, 8, device=DEV), idx=torch.zeros(T, 2, dtype=torch.int32, device=DEV),
+                   workspace=torch.empty(8 * T, dtype=torch.uint8, device=DEV))
+        assert names(lib.balance_loss, **big) == more + ["balance_count", "balance_forward", "balance_sum"]
     x, w = torch.zeros(33, 16384, dtype=torch.int8, device=DEV), torch.zeros(64, 16384, dtype=torch.int8, device=DEV)
     work = torch.empty(lib.int8_matmul_workspace_bytes(33, 64, 16384), dtype=torch.uint8, device=DEV)
     assert names(lib.int8_matmul, xq=x, xs=torch.zeros(33, device=DEV), wq=w, ws=torch.zeros(64, device=DEV),
