@@ -59,14 +59,23 @@ static hipError_t launch_gateup(const I8Gateup& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The tile, by the rows that an expert has on average.  Measured, 384 experts x 4096 x
-// 2048 unless given, us for 64 rows x 64 outputs (three stages) / 128 x 64:
-//   0.02 rows (1 token) 18.9 / 24.8, 0.1 (8 tokens) 130 / 138, 4 (256) 1071 / 1184, 16 (1024) 1124 / 1277,
-//   48 (1024, 128 experts) 451 / 505, 96 (64 experts) 267 / 237, 256 (16 experts, crowded) 134 / 118
+// Whether n rows of N outputs fill the CUs with tiles of bm x bn.
+static bool fills(int64_t n, int N, int bm, int bn) { return n / bm * ((N + bn - 1) / bn) >= 256; }
+
+// The tile, by the rows that an expert has on average, the large ones only where they
+// fill the CUs.  Measured, 384 experts x 4096 x 2048 unless given, us for 64 rows x 64
+// outputs (three stages) / 128 x 64 / 256 x 128:
+//   0.02 rows (1 token) 18.9 / 24.8, 0.1 (8 tokens) 130 / 138, 4 (256) 1071 / 1184, 16 (1024) 1124 / 1277
+//   (these four before weights went past the caches), 48 (1024, 128 experts) 364 / 373,
+//   64 (4096) uniform 1417 / 1237, crowded 1403 / 1463, 96 (1024, 64 experts) 297 / 253 / 426,
+//   256 (1024, 16 experts, crowded) 141 / 122 / 143, 384 (1024, 16 experts) 189 / 152 / 128,
+//   384 (4096, 64 experts) 730 / 611 / 529, 4096 (one expert) 109 / 78 / 67, 1000 (one) 28 / 29 / 46
 template <typename OUT>
 static hipError_t pick_gateup(const I8Gateup& a, hipStream_t s) {
-  if ((int64_t)a.T * a.k <= 64 * (int64_t)a.E) return launch_gateup<I8Tile<2, 2, 1, 1, 128, 3, 1, 2>, OUT>(a, s);
-  return launch_gateup<I8Tile<2, 4, 1, 1, 128, 2, 1, 2>, OUT>(a, s);
+  const int64_t n = (int64_t)a.T * a.k, E = a.E;
+  if (n > 320 * E && fills(n, a.f, 256, 128)) return launch_gateup<I8Tile<2, 4, 2, 2, 64, 3, 1, 2>, OUT>(a, s);
+  if (n > 64 * E && fills(n, a.f, 128, 64)) return launch_gateup<I8Tile<2, 2, 1, 2, 128, 2, 1, 2>, OUT>(a, s);
+  return launch_gateup<I8Tile<2, 2, 1, 1, 128, 3, 1, 2>, OUT>(a, s);
 }
 
 hipError_t launch_i8_gateup(const I8Gateup& a, hipStream_t s) {
@@ -213,17 +222,20 @@ static hipError_t launch_down(const I8Down& a, hipStream_t s) {
 }
 
 // The tile, as for gate/up: 64 rows x 128 outputs on eight waves (to keep loads in
-// flight), on two (fewer reads of LDS), and 128 x 128.  The products without the sum:
-//   0.06 rows (4 tokens) 35.0 / 38.6 / 49.0, 0.1 (8 tokens) 72.9 / 76.4 / 78.3, 1 (64) 346 / 352 / 388,
-//   16 (1024) 606 / 606 / 637, 48 (512 over 64 experts) 122 / 123 / 129, 64 crowded 797 / 786 / 832,
-//   64 uniform 786 / 769 / 745, 384 (64 experts x 2000 x 1408) 169 / 165 / 147, 1024 (16 experts, crowded) 258 / 253 / 215
-// Bound by memory: without its matrix steps the 64-row product takes as long (819 us
-// then), without its stores 680.
+// flight), on two (fewer reads of LDS), 128 x 128 and 256 x 256.  The products without
+// the sum, us:
+//   0.06 rows (4 tokens) 33.6 / 37.5 / 48.6, 0.1 (8 tokens) 64.5 / 68.8 / 73.4, 1 (64) 314 / 318 / 362,
+//   16 (1024) 566 / 567 / 609, 48 (512 over 64 experts) 114 / 116 / 124, 64 crowded 784 / 767 / 819 / 895,
+//   64 uniform 783 / 760 / 705 / 839, 256 (1024, 16 experts, crowded) 86 / 87 / 77 / 74,
+//   384 (64 experts) 430 / 414 / 359 / 308, 1024 (16 experts, crowded) 267 / 255 / 218 / 189
+// Up to some hundred rows bound by memory: without its matrix steps the 64-row product
+// took as long (819 us then), without its stores 680.
 static hipError_t launch_down_products(const I8Down& a, hipStream_t s) {
   const int64_t n = (int64_t)a.T * a.k, E = a.E;
-  if (n <= 16 * E) return launch_down<I8Tile<4, 2, 1, 1, 128, 2, 1, 1>>(a, s);
-  if (n <= 128 * E) return launch_down<I8Tile<2, 1, 2, 2, 128, 2, 1, 1>>(a, s);
-  return launch_down<I8Tile<2, 2, 2, 2, 128, 2, 1, 1>>(a, s);
+  if (n >= 256 * E && fills(n, a.d, 256, 256)) return launch_down<I8Tile<4, 2, 2, 4, 128, 2, 1, 1>>(a, s);
+  if (n > 128 * E && fills(n, a.d, 128, 128)) return launch_down<I8Tile<2, 2, 2, 2, 128, 2, 1, 1>>(a, s);
+  if (n > 16 * E) return launch_down<I8Tile<2, 1, 2, 2, 128, 2, 1, 1>>(a, s);
+  return launch_down<I8Tile<4, 2, 1, 1, 128, 2, 1, 1>>(a, s);
 }
 
 hipError_t launch_i8_down(const I8Down& a, hipStream_t s) {

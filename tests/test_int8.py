@@ -209,7 +209,8 @@ def silu64(g):
 
 
 EXPERTS = [(1, 8, 2, 64, 48), (1, 16, 6, 256, 272), (2, 4, 4, 144, 128), (3, 40, 5, 272, 144), (8, 64, 6, 512, 400), (60, 4, 2, 144, 272),
-           (200, 8, 3, 256, 128), (130, 2, 2, 400, 528), (300, 3, 1, 128, 256), (700, 24, 4, 64, 80)]
+           (200, 8, 3, 256, 128), (130, 2, 2, 400, 528), (300, 3, 1, 128, 256), (700, 24, 4, 64, 80),
+           (1030, 4, 4, 64, 2064), (1000, 3, 2, 2064, 64), (4200, 2, 2, 4112, 16), (2100, 8, 4, 80, 4000), (1200, 30, 4, 1040, 1040)]
 
 
 @gpu
