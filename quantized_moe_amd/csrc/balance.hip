@@ -299,7 +299,7 @@ __device__ __forceinline__ double sequence_sum(const Balance& a, int s, int run)
   const int first = bound_of(a.starts, s, a.T), end = bound_of(a.starts, s + 1, a.T);
   double v = 0.0;
   int block = (first + per - 1) / per;
-  if (first < block * per && lane < ROW_WAVES) {
+  if (first < min(end, block * per) && lane < ROW_WAVES) {  // (an empty sequence at T has no place in a.q)
     const int w = (block - 1) * per + lane * run;
     if (w + run > first && w < end) v = a.q[max(w, first)];
   }

@@ -180,6 +180,24 @@ def test_large_gradients_of_far_logits():
 
 
 @gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,empty", [(8195, 3), (16449, 100), (65529, 1)])
+def test_empty_sequences_at_the_end(T, empty, score):
+    """Sequences that begin where the last token ends, with several tokens a wave and a last
+    wave that has fewer: they have no partial sum (and no place in the workspace) of their own."""
+    rng = np.random.default_rng(T)
+    z, idx, _ = make(rng, T, 24, 3, 1)
+    starts = np.array([0, 0, T // 3, T // 3, T - 1] + [T] * (empty + 1), np.int32)
+    S = len(starts) - 1
+    c, n, loss, _ = forward(z.to(DEV), idx, starts, score, 0.5, S)
+    rc, rn, rl, _, _ = plain(z.double().numpy(), idx, starts, score, 0.5)
+    assert (c.cpu().numpy() == rc).all() and (n.cpu().numpy() == rn).all()
+    got = loss.double().cpu().numpy()
+    assert (got[rn == 0] == 0).all()
+    assert (np.abs(got - rl) <= rl * (Q(24, 6.0) + STEP)).all()
+
+
+@gpu
 def test_even_load_gives_alpha():
     """Every expert asked for alike: the loss is alpha and no logit is pushed."""
     T, E = 512, 64
