@@ -649,7 +649,9 @@ int moe_int8_matmul(const int8_t* xq, int64_t ldx, const float* xs, int32_t M,
  *   h[r] = silu(G_e x_t) * (U_e x_t)    (silu with the hardware's exponential and
  * reciprocal, a few ulp).  xq [T][d], xs [T]; w_gate, w_up [E][f][d] with scales
  * [E][f]; h [T*k][f] in h_dtype (MOE_F32 or MOE_BF16, rounded once): rows from
- * offsets[E] on are not written.  moe_int8_quantize of h gives the down
+ * offsets[E] on are not written.  (moe_bucket sets offsets[E] to T*k: the rows of
+ * routes without a place lie behind the last expert's and are written with it, from
+ * any token or from zeros; no pos names them.)  moe_int8_quantize of h gives the down
  * product's codes, one scale for a whole row.  d and f obey the limits of K.
  */
 int moe_int8_gateup(const int8_t* xq, const float* xs, int32_t T, int32_t k,
