@@ -705,11 +705,12 @@ int moe_int8_down(const int8_t* hq, const float* hs, int32_t T, int32_t k, const
  * and 0 for masked experts and for tokens that take no part.
  *
  * z [T] rows of E logits in z_dtype (MOE_F32 or MOE_BF16), z_stride elements
- * apart; idx int32 [T][k]; all arrays but the workspace at any element-aligned address; dz as z, in the same
- * dtype, rounded once, not overlapping it; counts and tokens of the forward call go into the backward
- * one.  Scores and sums are fp32 (exponentials and reciprocals of the hardware, a
- * few ulp), the sum over tokens fp64; identical inputs give bitwise identical
- * outputs.  1 <= E <= 1024, 1 <= k <= min(E, 16), 1 <= S <= 65536; T = 0 gives
+ * apart; idx int32 [T][k]; all arrays but the workspace at any element-aligned
+ * address; dz as z, in the same dtype, rounded once, not overlapping it.  z, idx,
+ * starts, counts and tokens of the backward call are those of the forward one, with
+ * what they held then.  Scores and sums are fp32 (exponentials and reciprocals of the
+ * hardware, a few ulp), the sum over tokens fp64; identical inputs give bitwise
+ * identical outputs.  1 <= E <= 1024, 1 <= k <= min(E, 16), 1 <= S <= 65536; T = 0 gives
  * zeros.  Workspace: moe_balance_loss_workspace_bytes.
  */
 int moe_balance_loss_workspace_bytes(int32_t T, int32_t S, int32_t E, size_t* bytes);

@@ -17,7 +17,10 @@ class _BalanceLoss(torch.autograd.Function):
         loss = torch.empty(S, dtype=torch.float32, device=z.device)
         work = torch.empty(lib.balance_loss_workspace_bytes(T, S, E), dtype=torch.uint8, device=z.device)
         lib.balance_loss(z, idx, counts, tokens, loss, work, score=score, alpha=alpha, starts=starts)
-        ctx.save_for_backward(z, idx, counts, tokens, starts)
+        # A copy of the routes: a gate writes the next batch's over them, and torch, which
+        # cannot see that, would take those for this batch's.
+        routes = idx.clone() if ctx.needs_input_grad[0] else idx
+        ctx.save_for_backward(z, routes, counts, tokens, starts)
         ctx.score, ctx.alpha = score, alpha
         ctx.mark_non_differentiable(counts, tokens)
         return loss, counts, tokens
@@ -36,5 +39,6 @@ def balance_loss(z: torch.Tensor, idx: torch.Tensor, score: str = "softmax", alp
     """(loss fp32 [S], counts int32 [S][E], tokens int32 [S]) of router logits z [T][E]
     (float32 or bfloat16) and the routes idx int32 [T][k] that a gate chose from them, for
     the S sequences that starts (int32 [S + 1], or None: one) cuts the tokens into.  The
-    loss is differentiable with respect to z, once; the counts are constants of it."""
+    loss is differentiable with respect to z, once; the counts are constants of it.  idx may
+    be a buffer that later calls write over: the backward pass has a copy of it."""
     return _BalanceLoss.apply(z, idx, starts, score, alpha)

@@ -1,0 +1,71 @@
+"""The differentiable balance loss in a program's hands: buffers that later calls write over.
+Tolerances as in test_balance.py.
+"""
+import numpy as np
+import pytest
+import torch
+
+from quantized_moe_amd import balance, lib
+from test_balance import Q, STEP, make, plain
+
+gpu = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture
+def calls_on_the_cpu(monkeypatch):
+    """The library's two balance calls replaced: the routes that each of them was given."""
+    got = {"forward": [], "backward": []}
+
+    def forward(z, idx, counts, tokens, loss, work, score, alpha, starts):
+        got["forward"].append(idx.clone())
+        counts.zero_(), tokens.zero_(), loss.zero_()
+
+    def backward(z, idx, counts, tokens, grad_loss, dz, score, alpha, starts):
+        got["backward"].append(idx.clone())
+        dz.zero_()
+
+    monkeypatch.setattr(lib, "balance_loss", forward)
+    monkeypatch.setattr(lib, "balance_loss_backward", backward)
+    monkeypatch.setattr(lib, "balance_loss_workspace_bytes", lambda *a: 0)
+    return got
+
+
+def test_gradient_of_overwritten_routes_on_the_cpu(calls_on_the_cpu):
+    """Routes that a kernel wrote over, which torch cannot know of: the backward call gets those of its forward call."""
+    idx = torch.tensor([[0, 1], [-1, -1]], dtype=torch.int32)
+    z = torch.zeros(2, 4, requires_grad=True)
+    loss, _, _ = balance.balance_loss(z, idx)
+    idx.numpy()[:] = [[-1, -1], [2, 3]]
+    loss.sum().backward()
+    assert calls_on_the_cpu["backward"][0].tolist() == [[0, 1], [-1, -1]]
+
+
+def gradient(z, idx, starts, score, alpha, weights):
+    """The definition's gradient and what a value of it may be off by."""
+    dz, unit = plain(z.double().numpy(), idx, starts, score, alpha, weights)[3:]
+    return dz, unit * (2 * Q(z.shape[1], 6.0) + 8 * STEP) + 2.0 ** -126
+
+
+@gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T", [60, 700])
+def test_two_micro_batches_over_one_buffer_of_routes(T, score):
+    """Two batches through one gate's buffers, then one backward pass: padding lies elsewhere in each."""
+    rng = np.random.default_rng(T)
+    E, k = 24, 3
+    gate = lib.gate(E, k, score=score)
+    idx, wt = torch.empty(T, k, dtype=torch.int32, device=DEV), torch.empty(T, k, device=DEV)
+    total, batches = 0.0, []
+    for first in (0, T // 2):
+        z = make(rng, T, E, k, 1, mask=0)[0]
+        z[first: first + T // 4] = -float("inf")      # no route
+        leaf = z.to(DEV).requires_grad_()
+        lib.gate_topk(gate, leaf.detach(), idx, wt)
+        total = total + balance.balance_loss(leaf, idx, score=score, alpha=0.3)[0].sum()
+        batches.append((z, leaf, idx.cpu().numpy()))
+    total.backward()
+    for z, leaf, routes in batches:
+        assert ((routes < 0).all(1)).sum() == T // 4
+        want, tol = gradient(z, routes, [0, T], score, 0.3, np.ones(1))
+        assert (np.abs(leaf.grad.double().cpu().numpy() - want) <= tol).all()
