@@ -40,5 +40,8 @@ def balance_loss(z: torch.Tensor, idx: torch.Tensor, score: str = "softmax", alp
     (float32 or bfloat16) and the routes idx int32 [T][k] that a gate chose from them, for
     the S sequences that starts (int32 [S + 1], or None: one) cuts the tokens into.  The
     loss is differentiable with respect to z, once; the counts are constants of it.  idx may
-    be a buffer that later calls write over: the backward pass has a copy of it."""
+    be a buffer that later calls write over: the backward pass has a copy of it.  z, starts
+    and the counts are kept as they are: as with any torch function, the backward pass
+    refuses them once they have been written over (by lib.router_logits, a product or
+    lib.balance_loss too)."""
     return _BalanceLoss.apply(z, idx, starts, score, alpha)

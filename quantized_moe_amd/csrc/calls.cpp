@@ -134,12 +134,20 @@ bool stream_of(PyObject* o, void** s) {
   return !PyErr_Occurred();
 }
 
+// `written`: outputs that a differentiable function may have kept (logits, counts).  They
+// count as written in place, so that its backward pass refuses them instead of taking
+// the new values for the old.
 template <class F>
-PyObject* call(F&& f) {
+PyObject* call(F&& f, std::initializer_list<PyObject*> written = {}) {
   int rc;
   Py_BEGIN_ALLOW_THREADS;
   rc = f();
   Py_END_ALLOW_THREADS;
+  if (rc == MOE_OK || rc == MOE_ERR_HIP)
+    for (PyObject* o : written) {
+      const at::Tensor& t = THPVariable_Unpack(o);
+      if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+    }
   return PyLong_FromLong(rc);
 }
 
@@ -212,7 +220,7 @@ PyObject* matmul(PyObject* const* a) {
     return moe_blockscale_matmul((const uint8_t*)x.p, x.ld, (const float*)xs, narrow(x.rows), (const uint8_t*)wq,
                                  (const float*)ws, narrow(N), narrow(K), y.p, float_type(y.type), y.ld, work,
                                  work_bytes, s);
-  });
+  }, {a[4]});
 }
 
 // xq, xs, k, offsets, perm, w_gate, s_gate, w_up, s_up, hq, hs, stream
@@ -293,7 +301,7 @@ PyObject* int8_matmul(PyObject* const* a) {
   return call([&] {
     return moe_int8_matmul((const int8_t*)x.p, x.ld, (const float*)xs, narrow(x.rows), (const int8_t*)wq,
                            (const float*)ws, narrow(N), narrow(K), y.p, float_type(y.type), y.ld, work, work_bytes, s);
-  });
+  }, {a[4]});
 }
 
 // xq, xs, k, offsets, perm, w_gate, s_gate, w_up, s_up, h, stream
@@ -378,7 +386,7 @@ PyObject* balance_loss(PyObject* const* a) {
     return moe_balance_loss(b.z.p, float_type(b.z.type), b.z.ld, narrow(b.z.rows), narrow(b.z.cols), (const int32_t*)b.idx,
                             narrow(b.k), (int32_t)b.score, (float)b.alpha, (const int32_t*)b.starts, narrow(b.S),
                             (int32_t*)b.counts, (int32_t*)b.tokens, (float*)loss, work, work_bytes, b.s);
-  });
+  }, {a[2], a[3], a[4]});
 }
 
 // z, idx, counts, tokens, grad_loss, dz, score, alpha, starts, stream

@@ -341,6 +341,8 @@ def router_logits(w_router, x, z, stream=None) -> None:
           z=(z, torch.float32, (T, E)))
     _check_here("router_logits", stream, w_router, x, z)
     _check(lib().moe_router_logits(_ptr(w_router), E, d, _ptr(x), x_dtype_of(x), T, _ptr(z), _stream(stream)))
+    if not z.is_inference():
+        torch.autograd.graph.increment_version(z)  # (written in place, where a differentiable function kept it)
 
 
 def gate_topk(gate: MoeGate, z, idx, wt, stream=None) -> None:

@@ -69,3 +69,50 @@ def test_two_micro_batches_over_one_buffer_of_routes(T, score):
         assert ((routes < 0).all(1)).sum() == T // 4
         want, tol = gradient(z, routes, [0, T], score, 0.3, np.ones(1))
         assert (np.abs(leaf.grad.double().cpu().numpy() - want) <= tol).all()
+
+
+@gpu
+@pytest.mark.parametrize("how", ["router_logits", "int8_matmul", "blockscale_matmul", "balance_loss"])
+def test_values_that_were_written_over_are_refused(how):
+    """Logits in a buffer of the library's calls, and the counts that were returned: another call's outputs in
+    their place stop the backward pass."""
+    T, E, d, k = 40, 16, 256, 3
+    i8 = lambda *n: torch.ones(*n, dtype=torch.int8, device=DEV)  # noqa: E731
+    f = lambda *n: torch.ones(*n, device=DEV)  # noqa: E731
+    z, idx = torch.randn(T, E, device=DEV), torch.zeros(T, k, dtype=torch.int32, device=DEV)
+    leaf = z.detach().requires_grad_()                 # (its gradient is the router's to use)
+    loss, counts, tokens = balance.balance_loss(leaf, idx)
+    if how == "router_logits":
+        lib.router_logits(f(E, d), f(T, d), z)
+    elif how == "int8_matmul":
+        lib.int8_matmul(i8(T, d), f(T), i8(E, d), f(E), z)
+    elif how == "blockscale_matmul":
+        lib.blockscale_matmul(i8(T, d).view(torch.uint8), f(T, 2), i8(E, d).view(torch.uint8), f(1, 2), z)
+    else:
+        lib.balance_loss(torch.randn(T, E, device=DEV), idx, counts, tokens, torch.empty(1, device=DEV), None)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.sum().backward()
+
+
+@gpu
+def test_inputs_and_refused_calls_do_not_count_as_written():
+    T, E = 5, 8
+    z, idx = torch.randn(T, E, device=DEV), torch.zeros(T, 2, dtype=torch.int32, device=DEV)
+    starts = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    out = [torch.empty(1, E, dtype=torch.int32, device=DEV), torch.empty(1, dtype=torch.int32, device=DEV), torch.empty(1, device=DEV)]
+    versions = lambda: [t._version for t in (z, idx, starts, *out)]  # noqa: E731
+    old = versions()
+    with pytest.raises(lib.MoeError, match="alpha"):
+        lib.balance_loss(z, idx, *out, None, alpha=float("inf"), starts=starts)
+    assert versions() == old
+    lib.balance_loss(z, idx, *out, None, starts=starts)
+    assert versions() == [v + (i > 2) for i, v in enumerate(old)]
+    with torch.inference_mode():
+        more = [torch.empty_like(t) for t in out]
+        lib.balance_loss(z, idx, *more, None, starts=starts)
+        assert all(torch.equal(a, b) for a, b in zip(out, more))
+        logits = torch.empty(T, E, device=DEV)
+        lib.router_logits(torch.ones(E, 256, device=DEV), torch.ones(T, 256, device=DEV), logits)
+    lib.balance_loss(z, idx, *more, None, starts=starts)   # tensors without a version, outside of that mode
+    lib.router_logits(torch.ones(E, 256, device=DEV), torch.ones(T, 256, device=DEV), logits)
+    assert (logits == 256).all()
