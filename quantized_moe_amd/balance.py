@@ -10,8 +10,9 @@ class _BalanceLoss(torch.autograd.Function):
     @staticmethod
     def forward(ctx, z, idx, starts, score, alpha):
         (T, E), S = z.shape, 1 if starts is None else starts.shape[0] - 1
-        if z.stride(1) != 1 and E > 1:
+        if (E > 1 and z.stride(1) != 1) or (T > 1 and z.stride(0) < E):  # (expanded rows, too)
             z = z.contiguous()
+        idx, starts = idx.contiguous(), starts if starts is None else starts.contiguous()
         counts = torch.empty(S, E, dtype=torch.int32, device=z.device)
         tokens = torch.empty(S, dtype=torch.int32, device=z.device)
         loss = torch.empty(S, dtype=torch.float32, device=z.device)
@@ -38,7 +39,8 @@ class _BalanceLoss(torch.autograd.Function):
 def balance_loss(z: torch.Tensor, idx: torch.Tensor, score: str = "softmax", alpha: float = 1.0, starts=None):
     """(loss fp32 [S], counts int32 [S][E], tokens int32 [S]) of router logits z [T][E]
     (float32 or bfloat16) and the routes idx int32 [T][k] that a gate chose from them, for
-    the S sequences that starts (int32 [S + 1], or None: one) cuts the tokens into.  The
+    the S sequences that starts (int32 [S + 1], or None: one) cuts the tokens into, with
+    any strides.  The
     loss is differentiable with respect to z, once; the counts are constants of it.  idx may
     be a buffer that later calls write over: the backward pass has a copy of it.  z, starts
     and the counts are kept as they are: as with any torch function, the backward pass

@@ -116,3 +116,41 @@ def test_inputs_and_refused_calls_do_not_count_as_written():
     lib.balance_loss(z, idx, *more, None, starts=starts)   # tensors without a version, outside of that mode
     lib.router_logits(torch.ones(E, 256, device=DEV), torch.ones(T, 256, device=DEV), logits)
     assert (logits == 256).all()
+
+
+def test_strides_on_the_cpu(calls_on_the_cpu, monkeypatch):
+    """Rows that overlap, columns with gaps, routes and starts that are columns of something: the calls get rows one after another."""
+    inner, seen = lib.balance_loss, []
+    monkeypatch.setattr(lib, "balance_loss", lambda z, idx, *a, **kw: (seen.append((z, idx, kw["starts"])), inner(z, idx, *a, **kw)))
+    starts = torch.tensor([[0, 2], [2, 3], [5, 5]], dtype=torch.int32)[:, 0]
+    for z in (torch.zeros(1, 6).expand(5, 6), torch.zeros(1, 1).expand(5, 1), torch.zeros(30).as_strided((5, 6), (3, 1)),
+              torch.zeros(6, 5).t(), torch.zeros(5, 12)[:, ::2], torch.zeros(5, 9)[:, :6]):
+        balance.balance_loss(z.requires_grad_(), torch.zeros(5, 2, dtype=torch.int32)[:, ::2], starts=starts)
+    assert len(seen) == 6
+    for z, idx, st in seen:
+        assert (z.stride(1) == 1 or z.shape[1] == 1) and z.stride(0) >= z.shape[1] and idx.is_contiguous() and st.tolist() == [0, 2, 5]
+        assert st.is_contiguous()
+    assert seen[-1][0].stride(0) == 9  # (rows further apart are taken as they are)
+
+
+@gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T", [50, 600])
+def test_expanded_logits(T, score):
+    """One row of logits for every token, as a bias of the router gives them: its gradient is the sum over the tokens."""
+    rng = np.random.default_rng(T)
+    E, k = 12, 2
+    idx = make(rng, T, E, k, 1)[1]
+    row = torch.from_numpy(rng.standard_normal((1, E)).astype(np.float32))
+    leaf = row.to(DEV).requires_grad_()
+    routes = torch.from_numpy(np.repeat(idx, 2, 1)).to(DEV)[:, ::2]
+    starts = torch.tensor([0, 9, T // 3, 9, T, 9], dtype=torch.int32, device=DEV)[::2]
+    loss, counts, tokens = balance.balance_loss(leaf.expand(T, E), routes, score=score, starts=starts)
+    z = row.expand(T, E).contiguous()
+    c, n, want, dz, unit = plain(z.double().numpy(), idx, [0, T // 3, T], score, 1.0, np.ones(2))
+    assert np.array_equal(counts.cpu().numpy(), c) and np.array_equal(tokens.cpu().numpy(), n)
+    assert (np.abs(loss.detach().cpu().numpy() - want) <= want * (Q(E, 6.0) + STEP)).all()
+    loss.sum().backward()
+    tol = unit * (2 * Q(E, 6.0) + 8 * STEP) + 2.0 ** -126
+    # torch's sum over the rows: at most T fp32 additions of the terms' magnitudes
+    assert (np.abs(leaf.grad.double().cpu().numpy() - dz.sum(0)) <= tol.sum(0) + T * STEP * np.abs(dz).sum(0)).all()
