@@ -358,14 +358,19 @@ struct BalanceArgs {
   double alpha;
   void *idx, *counts, *tokens, *starts = nullptr, *s;
 };
-bool balance_args(PyObject* z, PyObject* idx, PyObject* counts, PyObject* tokens, PyObject* score, PyObject* alpha,
-                  PyObject* starts, PyObject* stream, BalanceArgs* b) {
+// The numbers come first: nothing else is asked of Python while their error is set.
+bool balance_numbers(PyObject* score, PyObject* alpha, BalanceArgs* b) {
+  b->score = PyLong_AsLongLong(score);
+  if (b->score == -1 && PyErr_Occurred()) return false;
+  b->alpha = PyFloat_AsDouble(alpha);
+  return b->alpha != -1.0 || !PyErr_Occurred();
+}
+bool balance_args(PyObject* z, PyObject* idx, PyObject* counts, PyObject* tokens, PyObject* starts, PyObject* stream,
+                  BalanceArgs* b) {
   at::IntArrayRef i, c;
   if (!rows_of(z, &b->z) || float_type(b->z.type) < 0 || !shape_of(idx, 2, &i) || !shape_of(counts, 2, &c)) return false;
   b->k = i[1];
   b->S = c[0];
-  b->score = PyLong_AsLongLong(score);
-  b->alpha = PyFloat_AsDouble(alpha);
   return whole(idx, at::kInt, {b->z.rows, b->k}, &b->idx) && whole(counts, at::kInt, {b->S, b->z.cols}, &b->counts) &&
          whole(tokens, at::kInt, {b->S}, &b->tokens) &&
          (starts == Py_None || whole(starts, at::kInt, {b->S + 1}, &b->starts)) && stream_here(stream);
@@ -376,12 +381,11 @@ PyObject* balance_loss(PyObject* const* a) {
   BalanceArgs b;
   void *loss, *work;
   size_t work_bytes;
-  if (!balance_args(a[0], a[1], a[2], a[3], a[6], a[7], a[8], a[9], &b) || !whole(a[4], at::kFloat, {b.S}, &loss) ||
-      !workspace_of(a[5], &work, &work_bytes)) {
-    if (PyErr_Occurred()) return nullptr;
+  if (!balance_numbers(a[6], a[7], &b)) return nullptr;
+  if (!balance_args(a[0], a[1], a[2], a[3], a[8], a[9], &b) || !whole(a[4], at::kFloat, {b.S}, &loss) ||
+      !workspace_of(a[5], &work, &work_bytes))
     Py_RETURN_NONE;
-  }
-  if (PyErr_Occurred() || !stream_of(a[9], &b.s)) return nullptr;
+  if (!stream_of(a[9], &b.s)) return nullptr;
   return call([&] {
     return moe_balance_loss(b.z.p, float_type(b.z.type), b.z.ld, narrow(b.z.rows), narrow(b.z.cols), (const int32_t*)b.idx,
                             narrow(b.k), (int32_t)b.score, (float)b.alpha, (const int32_t*)b.starts, narrow(b.S),
@@ -394,12 +398,11 @@ PyObject* balance_loss_backward(PyObject* const* a) {
   BalanceArgs b;
   Rows dz;
   void* grad;
-  if (!balance_args(a[0], a[1], a[2], a[3], a[6], a[7], a[8], a[9], &b) || !whole(a[4], at::kFloat, {b.S}, &grad) ||
-      !rows_of(a[5], &dz) || dz.type != b.z.type || dz.rows != b.z.rows || dz.cols != b.z.cols) {
-    if (PyErr_Occurred()) return nullptr;
+  if (!balance_numbers(a[6], a[7], &b)) return nullptr;
+  if (!balance_args(a[0], a[1], a[2], a[3], a[8], a[9], &b) || !whole(a[4], at::kFloat, {b.S}, &grad) ||
+      !rows_of(a[5], &dz) || dz.type != b.z.type || dz.rows != b.z.rows || dz.cols != b.z.cols)
     Py_RETURN_NONE;
-  }
-  if (PyErr_Occurred() || !stream_of(a[9], &b.s)) return nullptr;
+  if (!stream_of(a[9], &b.s)) return nullptr;
   return call([&] {
     return moe_balance_loss_backward(b.z.p, float_type(b.z.type), b.z.ld, narrow(b.z.rows), narrow(b.z.cols),
                                      (const int32_t*)b.idx, narrow(b.k), (int32_t)b.score, (float)b.alpha,
