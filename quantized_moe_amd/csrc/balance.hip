@@ -410,9 +410,9 @@ __global__ __launch_bounds__(256) void balance_sum_kernel(Balance a, int run) {
   if ((threadIdx.x & 63) == 0) a.loss[s] = loss_of(a, v, a.tokens[s]);
 }
 
-// Backward: every wave takes `run` tokens in a row.
+// Backward: every wave takes `run` tokens in a row.  scale = alpha E / k.
 template <int ZDT, int PER, bool SOFTMAX>
-__global__ __launch_bounds__(256) void balance_backward_kernel(Balance a, int run) {
+__global__ __launch_bounds__(256) void balance_backward_kernel(Balance a, int run, double scale) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int first = (blockIdx.x * 4 + wave) * run, last = min(first + run, a.T);
   if (first >= last) return;
@@ -427,7 +427,7 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(Balance a, int ru
           seq.enter(a, starts, t, x);
           if (seq.s >= 0) {
             const float n = (float)a.tokens[seq.s];
-            coef = a.grad[seq.s] * (a.alpha * a.E / a.k) / (n * n);
+            coef = (float)((double)a.grad[seq.s] * scale * (1.0f / (n * n)));  // (parts of it may be past fp32)
           }
         }
         return seq.c;
@@ -536,10 +536,11 @@ template <int ZDT, int PER>
 static hipError_t launch_backward(const Balance& a, hipStream_t s) {
   const int run = run_of(a.T);
   const dim3 grid((unsigned)((a.T + 4 * run - 1) / (4 * run)));
+  const double scale = (double)a.alpha * a.E / a.k;
   if (a.softmax)
-    QMOE_LAUNCH((balance_backward_kernel<ZDT, PER, true>), grid, dim3(256), 0, s, a, run);
+    QMOE_LAUNCH((balance_backward_kernel<ZDT, PER, true>), grid, dim3(256), 0, s, a, run, scale);
   else
-    QMOE_LAUNCH((balance_backward_kernel<ZDT, PER, false>), grid, dim3(256), 0, s, a, run);
+    QMOE_LAUNCH((balance_backward_kernel<ZDT, PER, false>), grid, dim3(256), 0, s, a, run, scale);
   return hipGetLastError();
 }
 
