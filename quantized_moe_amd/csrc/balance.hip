@@ -6,6 +6,7 @@
 // tokens is ever kept; every token gives one number, and the gradient
 //   dz_te = g_s alpha E / (k n_s^2) p_te (c_se - q_t)   (sigmoid: (1 - sigma_te) times that)
 // needs the token's own row again and nothing else.  Bound by the logits' bytes.
+#include "balance_places.hpp"
 #include "blockscale.hpp"
 
 namespace qmoe {
@@ -288,21 +289,13 @@ __device__ __forceinline__ float loss_of(const Balance& a, double sum, int token
   return tokens > 0 ? (float)((double)a.alpha * a.E / a.k * sum / (n * n)) : 0.0f;
 }
 
-constexpr int ROW_WAVES = 16;  // of a block of the forward pass
-
-// The loss of sequence s, by one wave: the sums of q that the blocks of `tokens`
-// tokens left in a.q.  In the block that the sequence begins in behind the block's
-// first token, every wave left one, at the later of its own and the sequence's first
-// token; where it holds the block's first token, the block left one there.
+// The loss of sequence s, by one wave.
 __device__ __forceinline__ double sequence_sum(const Balance& a, int s, int run) {
   const int lane = threadIdx.x & 63, per = ROW_WAVES * run;
   const int first = bound_of(a.starts, s, a.T), end = bound_of(a.starts, s + 1, a.T);
   double v = 0.0;
-  int block = (first + per - 1) / per;
-  if (first < min(end, block * per) && lane < ROW_WAVES) {  // (an empty sequence at T has no place in a.q)
-    const int w = (block - 1) * per + lane * run;
-    if (w + run > first && w < end) v = a.q[max(w, first)];
-  }
+  const int block = block_from(first, run), at = wave_place(first, end, lane, run);
+  if (lane < ROW_WAVES && at >= 0) v = a.q[at];
   for (int b = block + lane; b * per < end; b += 64 * 8) {  // (T and a stride of 512 blocks stay below 2^27)
     double part[8];
 #pragma unroll
@@ -357,7 +350,7 @@ struct Sequence {
 };
 
 // Forward: every wave takes `run` tokens in a row; q of its tokens in 64 bits, one
-// sum for each sequence that it meets (sequence_sum says where it goes).
+// sum for each sequence that it meets (balance_places.hpp says where it goes).
 template <int ZDT, int PER, bool SOFTMAX>
 __global__ __launch_bounds__(64 * ROW_WAVES) void balance_forward_kernel(Balance a, int run) {
   __shared__ double sums[ROW_WAVES];  // of the sequence of the block's first token
@@ -510,9 +503,6 @@ __global__ __launch_bounds__(1024) void balance_small_kernel(Balance a) {
 static bool is_small(int T, int S, int E) { return T <= SMALL_TOKENS && S <= held_sequences(E); }
 
 size_t balance_ws(int T, int S, int E) { return is_small(T, S, E) ? 0 : (size_t)T * 8; }
-
-// Tokens of a wave: as many as make one round of waves.
-static int run_of(int T) { return (T + 8191) / 8192; }
 
 template <int ZDT, int PER>
 static hipError_t launch_small(const Balance& a, hipStream_t s) {
