@@ -47,7 +47,7 @@ __global__ __launch_bounds__(512) void i8_matmul_rows_kernel(I8Matmul a) {
   i32x4_t y = part[0][lane];
 #pragma unroll
   for (int u = 1; u < 8; u++) y += part[u][lane];
-  const bool vec = a.ldy % 4 == 0 && ((uintptr_t)a.y & (4 * sizeof(OUT) - 1)) == 0;
+  const bool vec = a.ldy % 4 == 0;  // (y itself is 16-byte aligned)
   if (r < a.M) store4(static_cast<OUT*>(a.y) + r * a.ldy + n, i8_values(y, xs, ws), a.N - n, vec);
 }
 
@@ -97,14 +97,14 @@ __global__ __launch_bounds__(C::THREADS, C::WAVES_PER_SIMD) void i8_matmul_tile_
   }
   OUT* y = static_cast<OUT*>(a.y) + m0 * a.ldy + n0;
   if constexpr (C::KS == 1) {
-    const uint32_t bits = (uint32_t)(a.ldy * sizeof(OUT)) | (uint32_t)(uintptr_t)a.y;
+    const uint32_t bits = (uint32_t)(a.ldy * sizeof(OUT));  // (y itself is 16-byte aligned)
     const int align = bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 2;
     i8_store<C>(lds, y, a.ldy, rows_m, rows_n, align, [&](int i, int j, int g, int n, float xs) {
       return i8_values(i8_run(acc[0][i][j], g), xs, i8_wscale<C>(lds, 0, n));
     });
   } else {
     // four outputs leave as one store where every row allows it
-    const bool vec = a.ldy % 4 == 0 && ((uintptr_t)a.y & (4 * sizeof(OUT) - 1)) == 0;
+    const bool vec = a.ldy % 4 == 0;
 #pragma unroll
     for (int j = 0; j < C::TM; j++) {
       const int mi = (wm * C::TM + j) * 32 + r;
