@@ -647,12 +647,13 @@ int moe_int8_matmul(const int8_t* xq, int64_t ldx, const float* xs, int32_t M,
  * expert e (offsets[e] <= r < offsets[e + 1], offsets and perm as moe_bucket
  * writes them for T tokens of k routes) with token t = perm[r] / k
  *   h[r] = silu(G_e x_t) * (U_e x_t)    (silu with the hardware's exponential and
- * reciprocal, a few ulp).  xq [T][d], xs [T]; w_gate, w_up [E][f][d] with scales
- * [E][f]; h [T*k][f] in h_dtype (MOE_F32 or MOE_BF16, rounded once): rows from
- * offsets[E] on are not written.  (moe_bucket sets offsets[E] to T*k: the rows of
- * routes without a place lie behind the last expert's and are written with it, from
- * any token or from zeros; no pos names them.)  moe_int8_quantize of h gives the down
- * product's codes, one scale for a whole row.  d and f obey the limits of K.
+ * reciprocal: up to (2 |g| + 8) 2^-24 of the value for a gate g).  xq [T][d], xs [T];
+ * w_gate, w_up [E][f][d] with scales [E][f]; h [T*k][f] in h_dtype (MOE_F32 or
+ * MOE_BF16, rounded once): rows from offsets[E] on are not written.  (moe_bucket sets
+ * offsets[E] to T*k: the rows of routes without a place lie behind the last expert's
+ * and are written with it, from any token or from zeros; no pos names them.)
+ * moe_int8_quantize of h gives the down product's codes, one scale for a whole row.  d
+ * and f obey the limits of K.
  */
 int moe_int8_gateup(const int8_t* xq, const float* xs, int32_t T, int32_t k,
                     const int32_t* offsets, const int32_t* perm, int32_t E,
@@ -701,17 +702,20 @@ int moe_int8_down(const int8_t* hq, const float* hs, int32_t T, int32_t k, const
  * g[s] the gradient of whatever is minimised with respect to loss[s]:
  *   w[t][e]  = g[s] alpha E counts[s][e] / (k n_s^2)
  *   dz[t][e] = p[t][e] (w[t][e] - sum_e' p[t][e'] w[t][e'])
- *              (MOE_SCORE_SIGMOID: times 1 - sigmoid(z[t][e]))
+ *              (MOE_SCORE_SIGMOID: times 1 - sigmoid(z[t][e]), z clamped likewise),
+ *              the factor g[s] alpha E / (k n_s^2) rounded to fp32,
  * and 0 for masked experts and for tokens that take no part.
  *
  * z [T] rows of E logits in z_dtype (MOE_F32 or MOE_BF16), z_stride elements
  * apart; idx int32 [T][k]; all arrays but the workspace at any element-aligned
  * address; dz as z, in the same dtype, rounded once, not overlapping it.  z, idx,
  * starts, counts and tokens of the backward call are those of the forward one, with
- * what they held then.  Scores and sums are fp32 (exponentials and reciprocals of the
- * hardware, a few ulp), the sum over tokens fp64; identical inputs give bitwise
- * identical outputs.  1 <= E <= 1024, 1 <= k <= min(E, 16), 1 <= S <= 65536; T = 0 gives
- * zeros.  Workspace: moe_balance_loss_workspace_bytes.
+ * what they held then.  Scores and sums are fp32, with exponentials and reciprocals of
+ * the hardware: of logits up to Z in magnitude a softmax term exp(z - max z) is off by up
+ * to (6 Z + 2) 2^-24 of itself, a sigmoid by (2 Z + 6) 2^-24.  The sum over tokens is
+ * fp64; identical inputs give bitwise identical outputs.  1 <= E <= 1024, 1 <= k <=
+ * min(E, 16), 1 <= S <= 65536; T = 0 gives zeros.  Workspace:
+ * moe_balance_loss_workspace_bytes.
  */
 int moe_balance_loss_workspace_bytes(int32_t T, int32_t S, int32_t E, size_t* bytes);
 int moe_balance_loss(const void* z, int32_t z_dtype, int64_t z_stride, int32_t T, int32_t E,

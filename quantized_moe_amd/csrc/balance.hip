@@ -5,7 +5,9 @@
 // c_se come from the routes alone, so no column sum of probabilities over the
 // tokens is ever kept; every token gives one number, and the gradient
 //   dz_te = g_s alpha E / (k n_s^2) p_te (c_se - q_t)   (sigmoid: (1 - sigma_te) times that)
-// needs the token's own row again and nothing else.  Bound by the logits' bytes.
+// needs the token's own row again and nothing else.  65536 tokens x 384 experts: fp32
+// forward 20.5 us, 4.9 TB/s of logits, with vector instructions in 73 % of the cycles;
+// backward 33, 6.1 TB/s, 75 %; bf16 19.7 and 25 us, bound by vector instructions (98 %).
 #include "balance_places.hpp"
 #include "blockscale.hpp"
 

@@ -1,5 +1,8 @@
-// Shared pieces of the block-scaled E4M3 operators (contracts: include/moe.h).
+// Shared pieces of the 8-bit operators (contracts: include/moe.h): the block-scaled E4M3
+// ones, and what the int8 ones and the balance loss take from here (buffers, copies into
+// LDS, waits, exact quotients, the M tiles of experts).
 //
+// The block-scaled operators:
 // Matrix-unit step: a block of 128 inputs is 16 x 16 dot products that leave
 // the matrix unit on their own and meet the product of their two scales in one
 // fused multiply-add.  The E4M3 codes enter as fp16, which holds each exactly,
@@ -73,7 +76,7 @@ __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v
 // residual, exact by the fused multiply-add, times r.  The first leaves a
 // neighbour of the quotient, the second the nearest.  6 instructions for the
 // general division's 10; s >= 2^-80 keeps the residuals of all quotients that
-// E4M3 tells from 0 out of the subnormal range.
+// E4M3 or whole numbers tell from 0 out of the subnormal range.
 __device__ __forceinline__ float divide_exact(float x, float s, float r) {
   float q = x * r;
   q = __builtin_fmaf(__builtin_fmaf(-s, q, x), r, q);

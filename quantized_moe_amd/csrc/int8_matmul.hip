@@ -189,10 +189,15 @@ static hipError_t launch_rows(const I8Matmul& a, hipStream_t s) {
 //   128 x 128, four stages            640 19.8 (19.7) 768 20.3 (20.7)  1024 22.2 (22.8)  2048 45.1 (45.6)
 //   128 x 128, two, two blocks a CU   1024 26.6 (26.5) 1500 32.8 (32.8) 2048 39.0 (39.0) 2800 59 (62)  5000 93 (104)
 //   256 x 256                         2048 45.7 (45.5) 2800 48.4 (51.3) 4096 61.3 (61.0)  5000 110 (99)
-// 8192 x 8192 x 8192 on 256 x 256: 444 to 458 (2.4 POP/s; the library's int8 product
-// without scales 526).  There the card's power is the bound: tiles that need fewer
-// cycles ran at a lower clock (798 thousand at 1.68 GHz, 922 at 1.97), and the same
-// loop without its copies into LDS took 367.
+// At K = 272, 1040, 2320, 4096 and 8192 with N = 4096 and 1300, M = 33 to 4096 and both
+// output types the model's tile was the fastest (within 0.5 %) in 122 of 130 cases; else it was 1 to 7 %
+// slower, in two of K = 272 11 and 14 % (128 x 4096 to bf16 4.8 and 4.4 us, 4096 x 4096
+// to fp32 20.0 and 17.6).
+// 8192 x 8192 x 8192 on 256 x 256: 441 to 479 (2.3 to 2.5 POP/s; the library's int8 product
+// without scales 526).  There the card's power is the bound: 756 to 766 thousand cycles,
+// the matrix units busy for 524 of them, at 1.6 to 1.7 GHz; tiles of 128 x 128 a wave (fewer
+// reads of LDS) 927 thousand at 1.96 GHz in as much time (474), and the loop without its
+// copies into LDS took 367.
 // Rows against 32 x 32 tiles at M = 1, 8 and 16: 4096 x 4096 5.3, 6.0 and 6.6 for 6.6;
 // 8192 x 8192 14.1, 15.3 and 17.8 for 13; 700 x 1040 3.8 for 4.9.
 template <typename OUT>
