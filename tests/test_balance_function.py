@@ -154,3 +154,18 @@ def test_expanded_logits(T, score):
     tol = unit * (2 * Q(E, 6.0) + 8 * STEP) + 2.0 ** -126
     # torch's sum over the rows: at most T fp32 additions of the terms' magnitudes
     assert (np.abs(leaf.grad.double().cpu().numpy() - dz.sum(0)) <= tol.sum(0) + T * STEP * np.abs(dz).sum(0)).all()
+
+
+@gpu
+@pytest.mark.parametrize("S", [1, 2000])
+def test_a_batch_without_tokens(S):
+    """No rows at all: losses of 0 and a gradient of no rows; without a gradient to take, the same."""
+    E = 16
+    starts = None if S == 1 else torch.zeros(S + 1, dtype=torch.int32, device=DEV)
+    idx = torch.empty(0, 2, dtype=torch.int32, device=DEV)
+    leaf = torch.empty(0, E, device=DEV, requires_grad=True)
+    loss, counts, tokens = balance.balance_loss(leaf, idx, starts=starts)
+    loss.sum().backward()
+    assert loss.shape == (S,) and not loss.any() and not counts.any() and not tokens.any() and leaf.grad.shape == (0, E)
+    with torch.no_grad():
+        assert not balance.balance_loss(leaf, idx, starts=starts)[0].requires_grad
