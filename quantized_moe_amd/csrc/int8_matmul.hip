@@ -194,7 +194,7 @@ static hipError_t launch_rows(const I8Matmul& a, hipStream_t s) {
 // slower, in two of K = 272 11 and 14 % (128 x 4096 to bf16 4.8 and 4.4 us, 4096 x 4096
 // to fp32 20.0 and 17.6).
 // 8192 x 8192 x 8192 on 256 x 256: 441 to 479 (2.3 to 2.5 POP/s; the library's int8 product
-// without scales 526).  There the card's power is the bound: 756 to 766 thousand cycles,
+// without scales 526).  There the card's power is the bound: 738 to 766 thousand cycles,
 // the matrix units busy for 524 of them, at 1.6 to 1.7 GHz; tiles of 128 x 128 a wave (fewer
 // reads of LDS) 927 thousand at 1.96 GHz in as much time (474), and the loop without its
 // copies into LDS took 367.
